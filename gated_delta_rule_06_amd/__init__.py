@@ -20,6 +20,9 @@ __all__ = [
     "chunk_fwd_scalar_erase_solve",
     "chunk_fwd_scalar_erase_scan", "lowrank_gates", "chunk_fwd_lowrank", "decode_step",
     "chunk_bwd", "chunk_bwd_workspace_size", "BWD_GRADS",
+    "chunk_fwd_head_decay", "chunk_fwd_head_decay_workspace_size", "chunk_bwd_head_decay",
+    "chunk_bwd_head_decay_workspace_size", "HEAD_DECAY_GRADS", "decode_step_head_decay",
+    "rms_norm", "rms_norm_bwd", "rms_norm_bwd_workspace_size", "rms_norm_8bit", "matvec_q4",
     "status_string", "last_error", "version", "MUIR_F32", "MUIR_BF16", "STATUS",
 ]
 
@@ -94,6 +97,27 @@ def lib():
         L.muir_chunk_bwd.restype = i
         L.muir_decode_step.argtypes = [vp] * 10 + [i] * 5 + [vp]
         L.muir_decode_step.restype = i
+        f = ctypes.c_float
+        L.muir_chunk_fwd_head_decay_workspace_size.argtypes = [i] * 7
+        L.muir_chunk_fwd_head_decay_workspace_size.restype = sz
+        L.muir_chunk_fwd_head_decay.argtypes = [vp] * 8 + [i] * 8 + [vp, sz, vp]
+        L.muir_chunk_fwd_head_decay.restype = i
+        L.muir_chunk_bwd_head_decay_workspace_size.argtypes = [i] * 7
+        L.muir_chunk_bwd_head_decay_workspace_size.restype = sz
+        L.muir_chunk_bwd_head_decay.argtypes = [vp] * 13 + [i] * 8 + [vp, sz, vp]
+        L.muir_chunk_bwd_head_decay.restype = i
+        L.muir_decode_step_head_decay.argtypes = [vp] * 6 + [i] * 7 + [vp]
+        L.muir_decode_step_head_decay.restype = i
+        L.muir_rms_norm.argtypes = [vp] * 6 + [i, i, f, i, i, vp]
+        L.muir_rms_norm.restype = i
+        L.muir_rms_norm_bwd_workspace_size.argtypes = [i, i]
+        L.muir_rms_norm_bwd_workspace_size.restype = sz
+        L.muir_rms_norm_bwd.argtypes = [vp] * 7 + [i] * 4 + [vp, sz, vp]
+        L.muir_rms_norm_bwd.restype = i
+        L.muir_rms_norm_8bit.argtypes = [vp] * 6 + [i, i, f, i, i, i, i, vp]
+        L.muir_rms_norm_8bit.restype = i
+        L.muir_matvec_q4.argtypes = [vp] * 5 + [i] * 6 + [vp]
+        L.muir_matvec_q4.restype = i
         L.muir_status_string.argtypes = [i]
         L.muir_status_string.restype = ctypes.c_char_p
         L.muir_last_error.argtypes = []
@@ -525,3 +549,265 @@ def decode_step(q, k, v, a, g, e, w, r, state, *, o=None):
         _ptr(state), _ptr(o), B, H, dk, dv, code, _stream(dev))
     _check(status)
     return o
+
+
+def _call(fn, device, *args):
+    """One library call on ``device``'s current stream, with that device current."""
+    import torch
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(device)))
+
+
+def _out(t, name, dtype, shape, device):
+    """``t`` checked as an output, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _require(t, name, dtype, shape, device)
+    return t
+
+
+def _workspace(t, need, device):
+    import torch
+    return _out(t, "workspace", torch.uint8, (max(need, 1),) if t is None else None, device)
+
+
+def _rank(t, name, n):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+
+
+def _head_decay_inputs(q, k, v, a, s0, lens):
+    import torch
+    for name, t in (("q", q), ("v", v)):
+        _rank(t, name, 4)
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    dev = q.device
+    for name, t, shape in (("q", q, (B, T, Hk, dk)), ("k", k, (B, T, Hk, dk)), ("v", v, (B, T, H, dv))):
+        _require(t, name, q.dtype, shape, dev)
+    code = _dtype_code(q)
+    per_token = not (isinstance(a, torch.Tensor) and a.dim() == 1)
+    _require(a, "a", torch.float32, (B, T, H) if per_token else (H,), dev)
+    if s0 is not None:
+        _require(s0, "s0", torch.float32, (B, H, dk, dv), dev)
+    if lens is not None:
+        _require(lens, "lens", torch.int32, (B,), dev)
+    return (B, T, H, Hk, dk, dv), int(per_token), code, dev
+
+
+def chunk_fwd_head_decay_workspace_size(B: int, T: int, H: int, Hk: int, dk: int, dv: int,
+                                        dtype_code: int) -> int:
+    return int(lib().muir_chunk_fwd_head_decay_workspace_size(B, T, H, Hk, dk, dv, dtype_code))
+
+
+def chunk_fwd_head_decay(q, k, v, a, s0=None, *, lens=None, o=None, s_out=None,
+                         return_state: bool = True, workspace=None):
+    """Linear attention with one decay per head over whole sequences
+    (``muir_chunk_fwd_head_decay``): S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k [B,T,Hk,dk] and v [B,T,H,dv] in float32 or bfloat16 (same dtype), each key head
+    shared by H / Hk value heads; a [B,T,H] or [H] float32 in [0, 1]; s0 [B,H,dk,dv]
+    float32 or None; lens [B] int32 or None: the tokens of each sequence, those behind
+    are not read and their rows of o are zeros. Returns (o, s_out): o [B,T,H,dv] and the
+    state after each sequence's last token (None with ``return_state=False``). ``s_out``
+    may be ``s0`` itself.
+    """
+    import torch
+    sizes, per_token, code, dev = _head_decay_inputs(q, k, v, a, s0, lens)
+    B, T, H, Hk, dk, dv = sizes
+    o = _out(o, "o", q.dtype, (B, T, H, dv), dev)
+    if s_out is not None or return_state:
+        s_out = _out(s_out, "s_out", torch.float32, (B, H, dk, dv), dev)
+    workspace = _workspace(workspace, chunk_fwd_head_decay_workspace_size(*sizes, code), dev)
+    _call(lib().muir_chunk_fwd_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0),
+          _ptr(lens), _ptr(o), _ptr(s_out), *sizes, per_token, code, _ptr(workspace),
+          workspace.numel())
+    return o, s_out
+
+
+def chunk_bwd_head_decay_workspace_size(B: int, T: int, H: int, Hk: int, dk: int, dv: int,
+                                        dtype_code: int) -> int:
+    return int(lib().muir_chunk_bwd_head_decay_workspace_size(B, T, H, Hk, dk, dv, dtype_code))
+
+
+HEAD_DECAY_GRADS = ("q", "k", "v", "la", "s0")
+
+
+def chunk_bwd_head_decay(q, k, v, a, s0=None, *, do, ds_out=None, lens=None, workspace=None,
+                         out=None):
+    """Backward pass of :func:`chunk_fwd_head_decay` (``muir_chunk_bwd_head_decay``).
+
+    Inputs as for the forward, plus ``do`` (dL/do, [B,T,H,dv], the q/k/v dtype) and
+    ``ds_out`` (dL/ds_out, [B,H,dk,dv] float32 or None). Returns a dict keyed by
+    ``HEAD_DECAY_GRADS``: "q", "k" and "v" shaped and typed as the inputs (shared heads
+    summed), "la" = a * dL/da float32 shaped as a, "s0" [B,H,dk,dv] float32. Gradients of
+    tokens behind ``lens`` are zeros. ``out`` may hold pre-allocated tensors under those keys.
+    """
+    import torch
+    sizes, per_token, code, dev = _head_decay_inputs(q, k, v, a, s0, lens)
+    B, T, H, Hk, dk, dv = sizes
+    _require(do, "do", q.dtype, (B, T, H, dv), dev)
+    if ds_out is not None:
+        _require(ds_out, "ds_out", torch.float32, (B, H, dk, dv), dev)
+    out = dict(out or {})
+    f32 = torch.float32
+    for n, dtype, shape in (("q", q.dtype, q.shape), ("k", q.dtype, k.shape),
+                            ("v", q.dtype, v.shape), ("la", f32, a.shape),
+                            ("s0", f32, (B, H, dk, dv))):
+        out[n] = _out(out.get(n), "d" + n, dtype, tuple(shape), dev)
+    workspace = _workspace(workspace, chunk_bwd_head_decay_workspace_size(*sizes, code), dev)
+    _call(lib().muir_chunk_bwd_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0),
+          _ptr(lens), _ptr(do), _ptr(ds_out), *[_ptr(out[n]) for n in HEAD_DECAY_GRADS], *sizes,
+          per_token, code, _ptr(workspace), workspace.numel())
+    return out
+
+
+def decode_step_head_decay(q, k, v, a, state, *, o=None):
+    """One token of :func:`chunk_fwd_head_decay`'s recurrence, updating ``state`` in place
+    (``muir_decode_step_head_decay``).
+
+    q, k [B,Hk,dk], v [B,H,dv] (float32 or bfloat16); a [B,H] or [H] float32; state
+    [B,H,dk,dv] float32. Returns o [B,H,dv] (q/k/v dtype).
+    """
+    import torch
+    for name, t in (("q", q), ("v", v)):
+        _rank(t, name, 3)
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    dev = q.device
+    for name, t, shape in (("q", q, (B, Hk, dk)), ("k", k, (B, Hk, dk)), ("v", v, (B, H, dv))):
+        _require(t, name, q.dtype, shape, dev)
+    code = _dtype_code(q)
+    per_token = not (isinstance(a, torch.Tensor) and a.dim() == 1)
+    _require(a, "a", torch.float32, (B, H) if per_token else (H,), dev)
+    _require(state, "state", torch.float32, (B, H, dk, dv), dev)
+    o = _out(o, "o", q.dtype, (B, H, dv), dev)
+    _call(lib().muir_decode_step_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(state),
+          _ptr(o), B, H, Hk, dk, dv, int(per_token), code)
+    return o
+
+
+def _norm_inputs(x, weight, residual, h):
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with at least one dimension")
+    D, dev = x.shape[-1], x.device
+    code = _dtype_code(x)
+    _require(x, "x", x.dtype, None, dev)
+    _require(weight, "weight", torch.float32, (D,), dev)
+    hcode = code
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only with a residual")
+    else:
+        _require(residual, "residual", residual.dtype, tuple(x.shape), dev)
+        hcode = _dtype_code(residual)
+        h = _out(h, "h", residual.dtype, tuple(x.shape), dev)
+    return x.numel() // D if D else 0, D, dev, code, hcode, h
+
+
+def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None):
+    """Root-mean-square norm over the last dimension with the residual's addition
+    (``muir_rms_norm``): h = x + residual, y = h / rms(h) * weight.
+
+    x [..., D] float32 or bfloat16; weight [D] float32; residual like x, or float32 beside
+    bfloat16 x, or None. Returns (y, h, rstd): y like x, h like residual (x itself without
+    one), rstd [...] float32, which :func:`rms_norm_bwd` takes. ``h`` may be ``residual``
+    itself (in place).
+    """
+    import torch
+    rows, D, dev, code, hcode, h = _norm_inputs(x, weight, residual, h)
+    y = _out(y, "y", x.dtype, tuple(x.shape), dev)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _call(lib().muir_rms_norm, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
+          _ptr(rstd), rows, D, eps, code, hcode)
+    return y, x if residual is None else h, rstd
+
+
+def rms_norm_bwd_workspace_size(rows: int, D: int) -> int:
+    return int(lib().muir_rms_norm_bwd_workspace_size(rows, D))
+
+
+def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspace=None):
+    """Backward pass of :func:`rms_norm` (``muir_rms_norm_bwd``).
+
+    dy [..., D] in y's dtype; h and rstd from the forward; ``dh`` the gradient that reaches h
+    from the residual stream, in h's dtype, or None. Returns (dx, dweight): dx in h's dtype,
+    the gradient of x and of the residual alike, and dweight [D] float32. ``dx`` may be
+    ``dh`` itself.
+    """
+    import torch
+    if not isinstance(h, torch.Tensor) or h.dim() < 1:
+        raise TypeError("h must be a torch.Tensor with at least one dimension")
+    D, dev = h.shape[-1], h.device
+    rows = h.numel() // D if D else 0
+    hcode = _dtype_code(h)
+    _require(h, "h", h.dtype, None, dev)
+    _require(dy, "dy", dy.dtype if isinstance(dy, torch.Tensor) else None, tuple(h.shape), dev)
+    code = _dtype_code(dy)
+    _require(weight, "weight", torch.float32, (D,), dev)
+    _require(rstd, "rstd", torch.float32, tuple(h.shape[:-1]), dev)
+    if dh is not None:
+        _require(dh, "dh", h.dtype, tuple(h.shape), dev)
+    dx = _out(dx, "dx", h.dtype, tuple(h.shape), dev)
+    dweight = _out(dweight, "dweight", torch.float32, (D,), dev)
+    workspace = _workspace(workspace, rms_norm_bwd_workspace_size(rows, D), dev)
+    _call(lib().muir_rms_norm_bwd, dev, _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh),
+          _ptr(dx), _ptr(dweight), rows, D, code, hcode, _ptr(workspace), workspace.numel())
+    return dx, dweight
+
+
+def rms_norm_8bit(x, weight, residual=None, *, eps: float = 1e-6, format: str = "e4m3",
+                  group: int = 0, y=None, scale=None, h=None):
+    """:func:`rms_norm` with its output in 8 bits (``muir_rms_norm_8bit``).
+
+    ``format`` "e4m3" (torch.float8_e4m3fn) or "int8"; one float32 scale for each row
+    (``group=0``) or each 128 columns (``group=128``). Returns (y, scale, h): the 8-bit
+    values [..., D], scale [...] or [..., D / 128] with y * scale the normed rows, and h as
+    :func:`rms_norm`.
+    """
+    import torch
+    formats = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
+    if format not in formats:
+        raise ValueError(f"format must be one of {sorted(formats)}, got {format!r}")
+    fmt, dtype = formats[format]
+    rows, D, dev, code, hcode, h = _norm_inputs(x, weight, residual, h)
+    y = _out(y, "y", dtype, tuple(x.shape), dev)
+    shape = tuple(x.shape[:-1]) + ((D // group,) if group > 0 else ())
+    scale = _out(scale, "scale", torch.float32, shape, dev)
+    _call(lib().muir_rms_norm_8bit, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
+          _ptr(scale), rows, D, eps, fmt, group, code, hcode)
+    return y, scale, x if residual is None else h
+
+
+def matvec_q4(x, w, scale, zero=None, *, group: int = 128, y=None):
+    """Product of up to 64 rows with 4-bit weights (``muir_matvec_q4``):
+    y[m, n] = sum_k x[m, k] (nib[n, k] - zero[n, k / group]) scale[n, k / group].
+
+    x [..., K] float32 or bfloat16; w [N, K / 2] uint8, columns 2j (low half) and 2j + 1
+    (high half) in byte j of a row; scale [N, K / group] float32 or bfloat16; zero the same
+    or None for 8; group 32, 64 or 128. Returns y [..., N] in x's dtype.
+    """
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a torch.Tensor with at least one dimension")
+    _rank(w, "w", 2)
+    K, N, dev = x.shape[-1], w.shape[0], x.device
+    code = _dtype_code(x)
+    if group <= 0 or K % 2 or K % group:
+        raise ValueError(f"K={K} must be a multiple of the group, {group}")
+    _require(x, "x", x.dtype, None, dev)
+    _require(w, "w", torch.uint8, (N, K // 2), dev)
+    _require(scale, "scale", scale.dtype if isinstance(scale, torch.Tensor) else None,
+             (N, K // group), dev)
+    scode = _dtype_code(scale)
+    if zero is not None:
+        _require(zero, "zero", scale.dtype, (N, K // group), dev)
+    y = _out(y, "y", x.dtype, tuple(x.shape[:-1]) + (N,), dev)
+    _call(lib().muir_matvec_q4, dev, _ptr(x), _ptr(w), _ptr(scale), _ptr(zero), _ptr(y),
+          x.numel() // K if K else 0, N, K, group, code, scode)
+    return y

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuir.so")
 SOURCES = ["api.cpp", "sizes.cpp", "decode.hip", "chunk_fwd.hip", "chunk_bwd.hip", "wy_fwd.hip", "gates_fwd.hip",
-           "noalloc.hip", "chunk_scan_split.hip"]
+           "noalloc.hip", "chunk_scan_split.hip", "op_api.cpp", "op_sizes.cpp", "head_decay.hip",
+           "head_decay_step.hip", "rms_norm.hip", "matvec_q4.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are kept out of every kernel. MFMA accumulators are kept

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "muir.h"
+#include "checks.hpp"
 #include "kernels.hpp"
 #include "layout.hpp"
 
@@ -18,7 +19,9 @@ namespace {
 
 thread_local char g_last_error[512] = "";
 
-muir_status_t fail(muir_status_t s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace muir {
 
 muir_status_t fail(muir_status_t s, const char *fmt, ...) {
     va_list ap;
@@ -33,40 +36,14 @@ muir_status_t ok() {
     return MUIR_OK;
 }
 
-struct Range {
-    const char *name;
-    uintptr_t lo, hi;  // [lo, hi)
-};
+}  // namespace muir
 
-Range range(const char *name, const void *p, size_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + bytes : lo};
-}
+namespace {
 
-bool overlaps(const Range &x, const Range &y) {
-    if (x.lo == x.hi || y.lo == y.hi) return false;
-    return x.lo < y.hi && y.lo < x.hi;
-}
-
-// size = a*b*c*d with overflow detection (all factors >= 0).
-bool mul_size(size_t &out, std::initializer_list<size_t> f) {
-    size_t acc = 1;
-    for (size_t x : f) {
-        if (x != 0 && acc > SIZE_MAX / x) return false;
-        acc *= x;
-    }
-    out = acc;
-    return true;
-}
+using namespace muir;
 
 bool supported_d(int d) { return d == 64 || d == 128; }
 bool supported_chunk(int c) { return c == 64 || c == 128 || c == 256; }
-
-muir_status_t check_hip(hipError_t err, const char *what) {
-    if (err != hipSuccess)
-        return fail(MUIR_ERR_HIP, "%s: %s", what, hipGetErrorString(err));
-    return ok();
-}
 
 }  // namespace
 

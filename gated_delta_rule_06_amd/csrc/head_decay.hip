@@ -1,0 +1,601 @@
+// Linear attention with one decay per head: chunked forward and backward (head_decay.hpp has the
+// formulas). Four kernels:
+//   pass_kernel, LOCAL      each segment's own contribution to the state at its end, and its decay
+//   join_kernel             the state at each segment's start from those, in order
+//   pass_kernel             one walk over a segment's chunks: outputs (or one gradient) with the state in registers
+//   dla_kernel, *_sum       the decay's gradient from the row sums of two passes; sums over shared heads
+// Where B * H workgroups fill the card there is one segment per head and the pass is the only launch of a forward.
+#include <algorithm>
+
+#include "head_decay.hpp"
+#include "op_kernels.hpp"
+
+namespace muir {
+namespace {
+
+using namespace hd;
+
+struct PassArgs {
+    const void *x, *y, *z;  // [B, T, h*, D*]
+    int hx, hy, hz;
+    const float *a;         // [B, T, H], or [H]
+    bool a_fixed;
+    const int *lens;        // [B] or NULL
+    const float *start;     // [B*H, nseg] states [DX, DZ] at the segments' starts, or NULL for zeros
+    bool start_t;           // the states are stored [DZ, DX]
+    void *out;              // [B, T, H, DZ] in the element type, or float32 with out_f32
+    bool out_f32;
+    float *s_out;           // state after the last token, [DX, DZ], or NULL; LOCAL: [B*H, nseg] states
+    float *dec;             // LOCAL: [B*H, nseg]
+    const void *w;          // KEEP: [B, T, hw, DZ], dots [B, T, H] = out . w
+    int hw;
+    float *dots;
+    float *anchors;         // KEEP: [B*H, groups] states, written in order and read reversed
+    float *edges;           // KEEP, reversed: [B*H, groups, 4] parts of <S, A>
+    int B, T, H, nseg, seg_chunks, nchunks;
+};
+
+template <typename T, int D> struct Tile {
+    static constexpr int VEC = 16 / sizeof(T);
+    static constexpr int LD = D + Op<T>::PAD;
+    static constexpr int N = C * D / VEC / THREADS;  // 16-byte vectors of a thread
+    uint4 r[N];
+    // Rows t0.. of one head; tokens from `end` on are zeros and are not read.
+    __device__ __forceinline__ void load(const T *base, size_t stride, int t0, int end, int tid) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = tid + THREADS * j, row = i / (D / VEC), c = i % (D / VEC), t = t0 + row;
+            r[j] = t < end ? *reinterpret_cast<const uint4 *>(base + t * stride + c * VEC) : uint4{0, 0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ void put(T *lds, int tid) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = tid + THREADS * j, row = i / (D / VEC), c = i % (D / VEC);
+            *reinterpret_cast<uint4 *>(lds + row * LD + c * VEC) = r[j];
+        }
+    }
+};
+
+template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
+    static constexpr int LDX = DX + Op<T>::PAD, LDZ = DZ + Op<T>::PAD, LDP = C + Op<T>::PAD;
+    static constexpr int Y = 0, Z = Y + C * LDX, X = Z + C * LDZ, P = X + (LOCAL ? 0 : C * LDX);
+    static constexpr int ELEMS = P + (LOCAL ? 0 : NTP * C * LDP);
+    static constexpr int TAIL = ELEMS * sizeof(T);
+    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 4 * C * 4;
+};
+
+// One wavefront owns DZ / 4 columns of the state and of the output; see head_decay.hpp for the operand order.
+// Rounding, for bf16 inputs: the products x.y are exact in float32; D (x.y) and the state go into the second
+// products as NTP and NTS bf16 terms, the decayed z into the state's update as three, so states, and the
+// row sums that the decay's gradient is made of, keep float32 accuracy.
+template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, int NTS, int NTU>
+__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(PassArgs p) {
+    using O = Op<T>;
+    using L = PassLds<T, DX, DZ, LOCAL, NTP>;
+    using frag = typename O::frag;
+    constexpr int NCT = DZ / 64, RT = DX / 16;
+    extern __shared__ __align__(16) unsigned char smem[];
+    T *const lds = reinterpret_cast<T *>(smem);
+    T *const ly = lds + L::Y, *const lz = lds + L::Z, *const lx = lds + L::X, *const lp = lds + L::P;
+    double *const sh_L = reinterpret_cast<double *>(smem + L::TAIL);  // sums of log2 a from the chunk's start
+    float *const sh_out = reinterpret_cast<float *>(sh_L + C);        // decay between a token and the start state
+    float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
+    float *const sh_dot = sh_upd + C;                                 // [4][C]
+
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, m = lane & 15, g = lane >> 4;
+    const int seg = blockIdx.x % p.nseg, bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    const int end = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
+    const int col0 = wv * (DZ / 4);
+    const size_t bT = static_cast<size_t>(b) * p.T;
+    const T *gx = LOCAL ? nullptr : static_cast<const T *>(p.x) + (bT * p.hx + h / (p.H / p.hx)) * DX;
+    const T *gy = static_cast<const T *>(p.y) + (bT * p.hy + h / (p.H / p.hy)) * DX;
+    const T *gz = static_cast<const T *>(p.z) + (bT * p.hz + h / (p.H / p.hz)) * DZ;
+    const size_t sx = static_cast<size_t>(p.hx) * DX, sy = static_cast<size_t>(p.hy) * DX,
+                 sz = static_cast<size_t>(p.hz) * DZ;
+    const int groups = (p.nchunks + ANCHOR - 1) / ANCHOR;
+    constexpr int DUMP = DX * DZ;
+
+    f32x4_t S[RT][NCT];
+    if (!LOCAL && p.start) {
+        const float *s = p.start + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const int row = 16 * rt + 4 * g, col = col0 + 16 * ct + m;
+                if (p.start_t) {
+                    S[rt][ct] = *reinterpret_cast<const f32x4_t *>(s + col * DX + row);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[rt][ct][i] = s[(row + i) * DZ + col];
+                }
+            }
+    } else {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = zero4();
+    }
+    const float a_h = p.a_fixed && p.nchunks > 0 ? p.a[h] : 1.f;
+    double seg_log = 0.0;
+
+    Tile<T, DX> rx, ry;
+    Tile<T, DZ> rz;
+    float ra = 1.f;
+    auto fetch = [&](int c) {
+        const int t0 = c * C;
+        if constexpr (!LOCAL) rx.load(gx, sx, t0, end, tid);
+        ry.load(gy, sy, t0, end, tid);
+        rz.load(gz, sz, t0, end, tid);
+        ra = t0 + lane >= end ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+    };
+    if (c0 < c1) fetch(REV ? c1 - 1 : c0);
+
+    for (int it = 0; it < c1 - c0; ++it) {
+        const int c = REV ? c1 - 1 - it : c0 + it, t0 = c * C;
+        if constexpr (!LOCAL) rx.put(lx, tid);
+        ry.put(ly, tid);
+        rz.put(lz, tid);
+        const double Lt = scan64(log2_decay(ra), lane);
+        const double Lc = __shfl(Lt, 63, 64);
+        const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(Lc - Lt));
+        if (wv == 0) {
+            sh_L[lane] = Lt;
+            sh_out[lane] = REV ? to_end : to_start;
+            sh_upd[lane] = REV ? to_start : to_end;
+        }
+        const float carry = exp2_f(static_cast<float>(Lc));
+        seg_log += Lc;
+        if constexpr (KEEP) {
+            // <S, A> at the end of every ANCHOR-th chunk: the pass in order leaves S, the reversed one takes its product.
+            if (REV ? (c + 1) % ANCHOR == 0 || c + 1 == p.nchunks : c % ANCHOR == 0 && c > 0) {
+                const int entry = REV ? c / ANCHOR : c / ANCHOR - 1;
+                f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + entry) * DUMP) +
+                              wv * (RT * NCT * 64) + lane;
+                f32x4_t sum = zero4();
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        if constexpr (REV) sum += S[rt][ct] * at[(rt * NCT + ct) * 64];
+                        else at[(rt * NCT + ct) * 64] = S[rt][ct];
+                    }
+                if constexpr (REV) {
+                    const float e = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    if (lane == 0) p.edges[(static_cast<size_t>(bh) * groups + entry) * 4 + wv] = e;
+                }
+            }
+        }
+        if (it + 1 < c1 - c0) fetch(REV ? c - 1 : c + 1);
+        lds_barrier();
+
+        if constexpr (!LOCAL) {
+            // P[i][j] = D (x_i . y_j) of this wavefront's 16 tokens i, over the 32-token blocks of j that it
+            // can reach; the product's rows are j, so a lane stores four consecutive j.
+            const int i = 16 * wv + m;
+            const double Li = sh_L[i];
+#pragma unroll
+            for (int pr = 0; pr < 2; ++pr) {
+                if (REV ? pr < wv / 2 : pr > wv / 2) continue;
+                f32x4_t acc[2] = {zero4(), zero4()};
+#pragma unroll
+                for (int k0 = 0; k0 < DX; k0 += 32) {
+                    const frag fx = O::row(lx, L::LDX, 16 * wv, k0, lane);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) acc[u] = O::mma(O::row(ly, L::LDX, 32 * pr + 16 * u, k0, lane), fx, acc[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j0 = 32 * pr + 16 * u + 4 * g;
+                    f32x4_t v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + e;
+                        const float d = static_cast<float>(REV ? sh_L[j] - Li : Li - sh_L[j]);
+                        v[e] = (REV ? j >= i : j <= i) ? acc[u][e] * exp2_f(d) : 0.f;
+                    }
+                    O::template put4<NTP>(lp + i * L::LDP + j0, C * L::LDP, v);
+                }
+            }
+            lds_barrier();
+        }
+
+        frag zf[2][NCT];
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) zf[pr][ct] = O::col(lz, L::LDZ, 32 * pr, col0 + 16 * ct, lane);
+
+        if constexpr (!LOCAL) {
+            // Output tiles with a token in each lane's column: decayed state . x, then P z.
+            f32x4_t acc[4][NCT];
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] = zero4();
+#pragma unroll
+            for (int k = 0; k < RT / 2; ++k) {
+                frag sf[NCT][NTS];
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    float s8[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s8[e] = S[2 * k][ct][e];
+                        s8[4 + e] = S[2 * k + 1][ct][e];
+                    }
+                    O::template split<NTS>(s8, sf[ct]);
+                }
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) {
+                    const frag fx = O::row(lx, L::LDX, 16 * tb, 32 * k, lane);
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                        for (int n = 0; n < NTS; ++n) acc[tb][ct] = O::mma(sf[ct][n], fx, acc[tb][ct]);
+                }
+            }
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                const float sc = sh_out[16 * tb + m];
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] *= sc;
+#pragma unroll
+                for (int pr = 0; pr < 2; ++pr) {
+                    if (REV ? pr < tb / 2 : pr > tb / 2) continue;
+#pragma unroll
+                    for (int n = 0; n < NTP; ++n) {
+                        const frag fp = O::row(lp + n * C * L::LDP, L::LDP, 16 * tb, 32 * pr, lane);
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] = O::mma(zf[pr][ct], fp, acc[tb][ct]);
+                    }
+                }
+                const int t = t0 + 16 * tb + m;
+                float dot = 0.f;
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    if (t >= end) acc[tb][ct] = zero4();
+                    const int col = col0 + 16 * ct + 4 * g;
+                    if (t < p.T) {
+                        const size_t at = ((bT + t) * p.H + h) * DZ + col;
+                        if (p.out_f32) store4(static_cast<float *>(p.out) + at, acc[tb][ct]);
+                        else store4(static_cast<T *>(p.out) + at, acc[tb][ct]);
+                    }
+                    if constexpr (KEEP) {
+                        if (t < end) {
+                            float w4[4];
+                            load_vec<4>(static_cast<const T *>(p.w) + ((bT + t) * p.hw + h / (p.H / p.hw)) * DZ + col, w4);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) dot += w4[e] * acc[tb][ct][e];
+                        }
+                    }
+                }
+                if constexpr (KEEP) {
+                    dot += __shfl_xor(dot, 16, 64);
+                    dot += __shfl_xor(dot, 32, 64);
+                    if (g == 0) sh_dot[wv * C + 16 * tb + m] = dot;
+                }
+            }
+        }
+
+        // The state: decayed over the chunk, then y^T (decayed z).
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] *= carry;
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) {
+            frag zs[NCT][NTU];
+            const f32x4_t ulo = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 4 * g);
+            const f32x4_t uhi = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 16 + 4 * g);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                float z8[8];
+                O::floats(zf[pr][ct], z8);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z8[e] *= ulo[e];
+                    z8[4 + e] *= uhi[e];
+                }
+                O::template split<NTU>(z8, zs[ct]);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const frag fy = O::col(ly, L::LDX, 32 * pr, 16 * rt, lane);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                    for (int n = NTU - 1; n >= 0; --n) S[rt][ct] = O::mma(fy, zs[ct][n], S[rt][ct]);
+            }
+        }
+        lds_barrier();
+        if constexpr (KEEP) {
+            if (tid < C && t0 + tid < p.T)
+                p.dots[(bT + t0 + tid) * p.H + h] = (sh_dot[tid] + sh_dot[C + tid]) + (sh_dot[2 * C + tid] + sh_dot[3 * C + tid]);
+        }
+    }
+
+    if constexpr (KEEP && !REV) {
+        if (seg == p.nseg - 1 && p.nchunks > 0) {
+            f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + groups - 1) * DUMP) +
+                          wv * (RT * NCT * 64) + lane;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) at[(rt * NCT + ct) * 64] = S[rt][ct];
+        }
+    }
+    float *so = nullptr;
+    if (LOCAL) {
+        so = p.s_out + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
+        if (tid == 0) p.dec[static_cast<size_t>(bh) * p.nseg + seg] = exp2_f(static_cast<float>(seg_log));
+    } else if (p.s_out && seg == (REV ? 0 : p.nseg - 1)) {
+        so = p.s_out + static_cast<size_t>(bh) * DUMP;
+    }
+    if (so) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) so[(16 * rt + 4 * g + i) * DZ + col0 + 16 * ct + m] = S[rt][ct][i];
+    }
+}
+
+// The state at each segment's start (reversed: end), in place of the segments' own contributions:
+// x <- s0 (or zeros); segment by segment: start = x, x <- dec x + contribution.
+template <bool REV>
+__global__ __launch_bounds__(256) void join_kernel(const float *s0, const float *dec, float *seg, int nseg, int n4) {
+    const int blocks = (n4 + 255) / 256, bh = blockIdx.x / blocks, i = blockIdx.x % blocks * 256 + threadIdx.x;
+    if (i >= n4) return;
+    f32x4_t x = s0 ? reinterpret_cast<const f32x4_t *>(s0)[static_cast<size_t>(bh) * n4 + i] : zero4();
+    f32x4_t *at = reinterpret_cast<f32x4_t *>(seg) + static_cast<size_t>(bh) * nseg * n4 + i;
+    const float *d = dec + static_cast<size_t>(bh) * nseg;
+#pragma unroll 4
+    for (int s = 0; s < nseg; ++s) {
+        const int k = REV ? nseg - 1 - s : s;
+        const f32x4_t own = at[static_cast<size_t>(k) * n4];
+        at[static_cast<size_t>(k) * n4] = x;
+        x = x * d[k] + own;
+    }
+}
+
+// dla of one group of ANCHOR chunks: sums of q.dq - k.dk from each token to the group's end, plus <S, A> there.
+// In 64 bits: the terms cancel where the decay is strong.
+__global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const float *cols, const float *edges,
+                                                        const int *lens, float *dla, double *part, int T, int H,
+                                                        int groups) {
+    __shared__ double sh[ANCHOR];
+    const int grp = blockIdx.x % groups, bh = blockIdx.x / groups, b = bh / H, h = bh % H;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int t = grp * (ANCHOR * C) + ANCHOR * C - 1 - static_cast<int>(threadIdx.x);
+    const int end = lens ? min(max(lens[b], 0), T) : T;
+    const size_t at = (static_cast<size_t>(b) * T + t) * H + h;
+    double x = t < end ? static_cast<double>(rows[at]) - static_cast<double>(cols[at]) : 0.0;
+    x = scan64(x, lane);
+    if (lane == 63) sh[wv] = x;
+    __syncthreads();
+    for (int w = 0; w < wv; ++w) x += sh[w];
+    const float *e = edges + (static_cast<size_t>(bh) * groups + grp) * 4;
+    x += (static_cast<double>(e[0]) + e[1]) + (static_cast<double>(e[2]) + e[3]);
+    if (t >= end) x = 0.0;
+    if (dla) {
+        if (t < T) dla[at] = static_cast<float>(x);
+        return;
+    }
+    __syncthreads();
+    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+    if (lane == 0) sh[wv] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) part[static_cast<size_t>(bh) * groups + grp] = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+// A fixed decay's gradient: one wavefront per head sums its groups over the batch, in a fixed order.
+__global__ __launch_bounds__(64) void dla_sum_kernel(const double *part, float *dla, int B, int H, int groups) {
+    const int h = blockIdx.x;
+    double x = 0.0;
+    for (int i = threadIdx.x; i < B * groups; i += 64)
+        x += part[(static_cast<size_t>(i / groups) * H + h) * groups + i % groups];
+    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+    if (threadIdx.x == 0) dla[h] = static_cast<float>(x);
+}
+
+// Gradients of shared heads: out [rows, Hk, d] = sum over the rep value heads of part [rows, Hk * rep, d].
+template <typename T>
+__global__ __launch_bounds__(256) void head_sum_kernel(const float *part, T *out, size_t n4, int rep, int d4) {
+    const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n4) return;
+    const size_t head = i / d4, c = i % d4;
+    const f32x4_t *p = reinterpret_cast<const f32x4_t *>(part) + head * rep * d4 + c;
+    f32x4_t x = p[0];
+    for (int r = 1; r < rep; ++r) x += p[static_cast<size_t>(r) * d4];
+    store4(out + 4 * i, x);
+}
+
+template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, int NTS, int NTU>
+hipError_t launch_pass(const PassArgs &p, hipStream_t stream) {
+    auto kern = pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>;
+    constexpr int bytes = PassLds<T, DX, DZ, LOCAL, NTP>::BYTES;
+    const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != hipSuccess) return err;
+    const unsigned grid = static_cast<unsigned>(p.B) * p.H * p.nseg;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(THREADS), bytes, stream, p);
+    return hipGetLastError();
+}
+
+// The kinds of pass: terms of each operand by what its results need.
+enum class Kind { Forward, LocalFwd, LocalRev, Dq, Dk, Dv };
+
+template <typename T, int DX, int DZ> hipError_t launch_kind(Kind kind, const PassArgs &p, hipStream_t s) {
+    constexpr bool BF = sizeof(T) == 2;
+    constexpr int N3 = BF ? 3 : 1;
+    switch (kind) {
+        case Kind::Forward: return launch_pass<T, DX, DZ, false, false, false, 1, 1, N3>(p, s);
+        case Kind::LocalFwd: return launch_pass<T, DX, DZ, false, true, false, 1, 1, N3>(p, s);
+        case Kind::LocalRev: return launch_pass<T, DX, DZ, true, true, false, 1, 1, N3>(p, s);
+        case Kind::Dq: return launch_pass<T, DX, DZ, false, false, true, N3, N3, N3>(p, s);
+        case Kind::Dk: return launch_pass<T, DX, DZ, true, false, true, N3, N3, N3>(p, s);
+        case Kind::Dv: return launch_pass<T, DX, DZ, true, false, false, 1, 1, N3>(p, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_any(Kind kind, bool bf16, int dx, int dz, const PassArgs &p, hipStream_t s) {
+#define MUIR_HD(X, Z) \
+    if (dx == X && dz == Z) return bf16 ? launch_kind<bf16_t, X, Z>(kind, p, s) : launch_kind<float, X, Z>(kind, p, s);
+    MUIR_HD(64, 64) MUIR_HD(64, 128) MUIR_HD(128, 64) MUIR_HD(128, 128)
+#undef MUIR_HD
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_join(bool rev, const float *s0, const float *dec, float *seg, int bh, int nseg, int n,
+                       hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256) * bh);
+    if (rev) hipLaunchKernelGGL(join_kernel<true>, grid, dim3(256), 0, s, s0, dec, seg, nseg, n / 4);
+    else hipLaunchKernelGGL(join_kernel<false>, grid, dim3(256), 0, s, s0, dec, seg, nseg, n / 4);
+    return hipGetLastError();
+}
+
+struct Carver {
+    unsigned char *base;
+    size_t at = 0;
+    template <typename V> V *take(size_t n) {
+        V *p = reinterpret_cast<V *>(base + at);
+        at += up256(n * sizeof(V));
+        return p;
+    }
+};
+
+PassArgs pass_args(const HeadDecayCall &c) {
+    PassArgs p{};
+    p.a = c.a;
+    p.a_fixed = c.a_fixed;
+    p.lens = c.lens;
+    p.B = c.B;
+    p.T = c.T;
+    p.H = c.H;
+    p.nchunks = chunks_of(c.T);
+    p.nseg = head_decay_segments(c.B, c.T, c.H, c.bf16);
+    p.seg_chunks = (p.nchunks + p.nseg - 1) / p.nseg;
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_head_decay_fwd(const HeadDecayCall &c, void *o, float *s_out, void *workspace, hipStream_t stream) {
+    PassArgs p = pass_args(c);
+    p.x = c.q;
+    p.y = c.k;
+    p.z = c.v;
+    p.hx = p.hy = c.Hk;
+    p.hz = c.H;
+    p.start = c.s0;
+    if (p.nseg > 1) {
+        Carver w{static_cast<unsigned char *>(workspace)};
+        const size_t bhs = static_cast<size_t>(c.B) * c.H * p.nseg;
+        float *seg = w.take<float>(bhs * c.dk * c.dv), *dec = w.take<float>(bhs);
+        p.s_out = seg;
+        p.dec = dec;
+        hipError_t err = launch_any(Kind::LocalFwd, c.bf16, c.dk, c.dv, p, stream);
+        if (err != hipSuccess) return err;
+        err = launch_join(false, c.s0, dec, seg, c.B * c.H, p.nseg, c.dk * c.dv, stream);
+        if (err != hipSuccess) return err;
+        p.start = seg;
+    }
+    p.out = o;
+    p.s_out = s_out;
+    return launch_any(Kind::Forward, c.bf16, c.dk, c.dv, p, stream);
+}
+
+hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g, void *workspace, hipStream_t stream) {
+    const PassArgs p0 = pass_args(c);
+    const int groups = groups_of(c.T), BH = c.B * c.H, rep = c.H / c.Hk;
+    const size_t bh = BH, tok = bh * c.T, st = static_cast<size_t>(c.dk) * c.dv;
+    Carver w{static_cast<unsigned char *>(workspace)};
+    float *rows = w.take<float>(tok), *cols = w.take<float>(tok);
+    float *anchors = w.take<float>(bh * groups * st), *edges = w.take<float>(bh * groups * 4);
+    double *part = w.take<double>(bh * groups);
+    const float *s_start = c.s0, *a_start = g.ds_out;
+    hipError_t err;
+    if (p0.nseg > 1) {
+        float *seg[2] = {w.take<float>(bh * p0.nseg * st), w.take<float>(bh * p0.nseg * st)};
+        float *dec = w.take<float>(bh * p0.nseg);
+        for (int rev = 0; rev < 2; ++rev) {
+            PassArgs p = p0;
+            p.y = rev ? c.q : c.k;
+            p.z = rev ? g.dout : c.v;
+            p.hx = p.hy = c.Hk;
+            p.hz = c.H;
+            p.s_out = seg[rev];
+            p.dec = dec;
+            err = launch_any(rev ? Kind::LocalRev : Kind::LocalFwd, c.bf16, c.dk, c.dv, p, stream);
+            if (err != hipSuccess) return err;
+            err = launch_join(rev, rev ? g.ds_out : c.s0, dec, seg[rev], BH, p0.nseg, c.dk * c.dv, stream);
+            if (err != hipSuccess) return err;
+        }
+        s_start = seg[0];
+        a_start = seg[1];
+    }
+    float *shared = rep > 1 ? w.take<float>(tok * c.dk) : nullptr;
+    for (int pass = 0; pass < 2; ++pass) {  // dq in order, then dk reversed
+        PassArgs p = p0;
+        p.x = pass ? c.v : g.dout;
+        p.y = pass ? g.dout : c.v;
+        p.z = pass ? c.q : c.k;
+        p.hx = p.hy = c.H;
+        p.hz = c.Hk;
+        p.start = pass ? a_start : s_start;
+        p.start_t = true;
+        void *out = pass ? g.dk : g.dq;
+        p.out = shared ? shared : out;
+        p.out_f32 = shared != nullptr;
+        p.w = pass ? c.k : c.q;
+        p.hw = c.Hk;
+        p.dots = pass ? cols : rows;
+        p.anchors = anchors;
+        p.edges = edges;
+        if (c.T > 0) {
+            err = launch_any(pass ? Kind::Dk : Kind::Dq, c.bf16, c.dv, c.dk, p, stream);
+            if (err != hipSuccess) return err;
+            if (shared) {
+                const size_t n4 = tok / rep * c.dk / 4;
+                const dim3 grid(static_cast<unsigned>((n4 + 255) / 256));
+                if (c.bf16)
+                    hipLaunchKernelGGL(head_sum_kernel<bf16_t>, grid, dim3(256), 0, stream, shared,
+                                       static_cast<bf16_t *>(out), n4, rep, c.dk / 4);
+                else
+                    hipLaunchKernelGGL(head_sum_kernel<float>, grid, dim3(256), 0, stream, shared,
+                                       static_cast<float *>(out), n4, rep, c.dk / 4);
+                err = hipGetLastError();
+                if (err != hipSuccess) return err;
+            }
+        }
+    }
+    PassArgs p = p0;
+    p.x = c.k;
+    p.y = c.q;
+    p.z = g.dout;
+    p.hx = p.hy = c.Hk;
+    p.hz = c.H;
+    p.start = a_start;
+    p.out = g.dv;
+    p.s_out = g.ds0;
+    err = launch_any(Kind::Dv, c.bf16, c.dk, c.dv, p, stream);
+    if (err != hipSuccess) return err;
+    if (c.T > 0) {
+        hipLaunchKernelGGL(dla_kernel, dim3(static_cast<unsigned>(groups) * BH), dim3(ANCHOR * C), 0, stream, rows, cols, edges, c.lens,
+                           c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    if (c.a_fixed) {
+        hipLaunchKernelGGL(dla_sum_kernel, dim3(c.H), dim3(64), 0, stream, part, g.dla, c.B, c.H, groups);
+        err = hipGetLastError();
+    }
+    return err;
+}
+
+}  // namespace muir

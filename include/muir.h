@@ -422,6 +422,140 @@ muir_status_t muir_chunk_bwd(
  */
 size_t muir_state_bytes(int B, int H, int dk, int dv);
 
+/*
+ * Layer operators around the chunk forward.
+ *
+ * They follow the conventions above. Buffers that are read and written one element at a time (a, lens, dla,
+ * rstd, scale, zero, dweight, y of muir_matvec_q4) need only their element's alignment.
+ */
+
+/*
+ * Linear attention with one decay per head (no erase, no gates): per (batch, value head)
+ *     S_t = a_t S_{t-1} + k_t v_t^T          o_t = S_t^T q_t
+ * chunked (64 tokens) on the matrix cores, the token axis split into segments that run side by side where
+ * the heads alone do not fill the GPU.
+ *
+ *   q, k    [B, T, Hk, dk]  dtype `qkv`      shared by H / Hk consecutive value heads each
+ *   v       [B, T, H, dv]   dtype `qkv`
+ *   a       [B, T, H] float32 with a_per_token != 0, else [H]   decay in [0, 1]; 0 drops the state
+ *   s0      [B, H, dk, dv]  float32 or NULL  initial state (NULL = zeros)
+ *   lens    [B] int32 or NULL                tokens of each sequence (clamped to 0..T; NULL = T). Tokens from
+ *                                            lens[b] on are not read: their rows of o are zeros and s_out is the
+ *                                            state after token lens[b] - 1
+ *   o       [B, T, H, dv]   dtype `qkv`
+ *   s_out   [B, H, dk, dv]  float32 or NULL  final state; may equal s0 (in place)
+ *   H a multiple of Hk; dk and dv each 64 or 128; T >= 0 (T == 0 copies s0, or zeros, into s_out)
+ *   workspace: muir_chunk_fwd_head_decay_workspace_size(...) bytes (0 where one segment a head is used)
+ *
+ * bf16: o is rounded once from float32 sums whose operands (q.k times its decay, the state) are bf16 terms;
+ * s_out keeps float32 accuracy. Errors as for muir_chunk_fwd, and MUIR_ERR_UNSUPPORTED for B * H above 2^21 or
+ * B * (T + 64) * H above 2^31.
+ */
+size_t muir_chunk_fwd_head_decay_workspace_size(int B, int T, int H, int Hk, int dk, int dv,
+                                                muir_dtype_t qkv);
+muir_status_t muir_chunk_fwd_head_decay(
+    const void *q, const void *k, const void *v, const float *a, const float *s0, const int *lens,
+    void *o, float *s_out, int B, int T, int H, int Hk, int dk, int dv, int a_per_token,
+    muir_dtype_t qkv, void *workspace, size_t workspace_bytes, muir_stream_t stream);
+
+/*
+ * Backward pass of muir_chunk_fwd_head_decay: the gradients of a scalar loss L given dL/do and dL/ds_out.
+ *
+ *   inputs   as for the forward; dout [B, T, H, dv] dtype `qkv`; ds_out [B, H, dk, dv] float32 or NULL (zero)
+ *   dq, dk   [B, T, Hk, dk] dtype `qkv`, summed over the value heads that share them; dv [B, T, H, dv] dtype `qkv`
+ *   dla      float32, shaped as a: a * dL/da, the gradient with respect to log a (finite at a = 0); with
+ *            a_per_token == 0 summed over batch and tokens
+ *   ds0      [B, H, dk, dv] float32 or NULL to skip
+ *   workspace: muir_chunk_bwd_head_decay_workspace_size(...) bytes
+ *
+ * Gradients of tokens from lens[b] on are zeros (dout is not read there). Every sum is in float32 or more, in a
+ * fixed order.
+ */
+size_t muir_chunk_bwd_head_decay_workspace_size(int B, int T, int H, int Hk, int dk, int dv,
+                                                muir_dtype_t qkv);
+muir_status_t muir_chunk_bwd_head_decay(
+    const void *q, const void *k, const void *v, const float *a, const float *s0, const int *lens,
+    const void *dout, const float *ds_out, void *dq, void *dk, void *dv, float *dla, float *ds0,
+    int B, int T, int H, int Hk, int dk_, int dv_, int a_per_token, muir_dtype_t qkv,
+    void *workspace, size_t workspace_bytes, muir_stream_t stream);
+
+/*
+ * One token of the same recurrence, updating the state in place.
+ *
+ *   q, k [B, Hk, dk], v [B, H, dv] dtype `qkv`; a [B, H] float32 with a_per_token != 0, else [H]
+ *   state [B, H, dk, dv] float32, read and written; o [B, H, dv] dtype `qkv`
+ */
+muir_status_t muir_decode_step_head_decay(
+    const void *q, const void *k, const void *v, const float *a, float *state, void *o,
+    int B, int H, int Hk, int dk, int dv, int a_per_token, muir_dtype_t qkv, muir_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *     h = x + residual      rstd = (mean(h^2) + eps)^(-1/2)      y = h rstd weight
+ *
+ *   x, y      [rows, D]  dtype `x_type`
+ *   residual  [rows, D]  dtype `h_type`, or NULL: h is x, and `h` must be NULL and h_type is not looked at
+ *   h         [rows, D]  dtype `h_type`: the sum, rounded to its type; the norm is taken of the rounded value.
+ *                        May equal residual (in place)
+ *   weight    [D] float32
+ *   rstd      [rows] float32 or NULL
+ *   h_type is x_type, or MUIR_F32 with bf16 rows; D a multiple of 8 up to 16384; rows >= 0; eps >= 0
+ */
+muir_status_t muir_rms_norm(
+    const void *x, const void *residual, const float *weight, void *h, void *y, float *rstd,
+    int rows, int D, float eps, muir_dtype_t x_type, muir_dtype_t h_type, muir_stream_t stream);
+
+/*
+ * Its backward pass. With p = dy weight and n = h rstd:
+ *     dx = rstd (p - n mean(p n)) + dh        dweight = sum over rows of dy n
+ *
+ *   dy [rows, D] dtype `y_type`; h [rows, D] dtype `h_type` and rstd [rows] from the forward
+ *   dh [rows, D] dtype `h_type` or NULL: the gradient that reaches h from the residual stream
+ *   dx [rows, D] dtype `h_type`: the gradient of x and of residual alike; may equal dh
+ *   dweight [D] float32
+ *   workspace: muir_rms_norm_bwd_workspace_size(rows, D) bytes
+ */
+size_t muir_rms_norm_bwd_workspace_size(int rows, int D);
+muir_status_t muir_rms_norm_bwd(
+    const void *dy, const void *h, const float *weight, const float *rstd, const void *dh, void *dx,
+    float *dweight, int rows, int D, muir_dtype_t y_type, muir_dtype_t h_type,
+    void *workspace, size_t workspace_bytes, muir_stream_t stream);
+
+typedef enum {
+    MUIR_E4M3 = 0,            /* 8-bit float, 4 exponent bits, no infinities (largest 448) */
+    MUIR_INT8 = 1             /* two's complement, -127..127                               */
+} muir_format_t;
+
+/*
+ * The norm with its output in 8 bits: y8 = y / scale rounded to nearest even, scale = max|y| / 448 (e4m3)
+ * or max|y| / 127 (int8), over the whole row (group 0) or over each 128 columns (group 128).
+ *
+ *   y8     [rows, D] one byte each
+ *   scale  [rows] float32, or [rows, D / 128] with group 128; 1 where all of y is zero, never below the
+ *          smallest normal float32. A NaN or infinity in a row makes its scale so (int8 has no NaN of its own)
+ *   the rest as for muir_rms_norm
+ */
+muir_status_t muir_rms_norm_8bit(
+    const void *x, const void *residual, const float *weight, void *h, void *y8, float *scale,
+    int rows, int D, float eps, muir_format_t format, int group, muir_dtype_t x_type,
+    muir_dtype_t h_type, muir_stream_t stream);
+
+/*
+ * Product of a few rows with 4-bit weights, as at single-token steps:
+ *     y[m, n] = sum_k x[m, k] (nib[n, k] - zero[n, k / group]) scale[n, k / group]
+ *
+ *   x      [M, K] dtype `x_type`, y [M, N] the same; M up to 64
+ *   w      [N, K / 2] bytes: columns 2 j (low half) and 2 j + 1 (high half) in byte j of a row, each 0..15
+ *   scale  [N, K / group] dtype `scale_type`; zero the same, or NULL for 8
+ *   group  32, 64 or 128; K a multiple of it
+ *
+ * Weights are exact; sums are float32 (float32 x is three bf16 terms, exact to its last bit or two). An
+ * infinity in x makes that row of y NaN or infinite.
+ */
+muir_status_t muir_matvec_q4(
+    const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K,
+    int group, muir_dtype_t x_type, muir_dtype_t scale_type, muir_stream_t stream);
+
 /* Static, never-NULL name of a status code ("MUIR_OK", ...). */
 const char *muir_status_string(muir_status_t s);
 

@@ -1,0 +1,293 @@
+"""Linear attention with one decay per head against its recurrence in 64 bits: forward, backward, single-token step.
+
+Tolerances are sums of roundings, element by element: U is half a step of the output type, F one float32 rounding,
+and `mag` the same sums with every term's absolute value (the operators on absolute inputs). A float32 sum of n
+terms is off by at most n F mag; the chains here are a product over dk or dv (128), a chunk's 64 tokens twice, the
+carries of the chunks, and a decay as exp2 of a sum of log2 (at most 34 F for one that is not below 2^-24):
+KF bounds them together. In bf16 the outputs have two operands of one bf16 rounding each (the decayed products, the state),
+so one more U of each part's mag; dq and dk have none, their operands are three terms."""
+import pytest
+import torch
+
+import gated_delta_rule_06_amd as muir
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+F = 2.0 ** -24
+
+
+def kf(T):
+    return (2 * (128 + 128 + 34) + 4 * (T // 64 + 1)) * F
+
+
+def inputs(device, B, T, H, Hk, dk, dv, dtype, fixed=False, lens=None, s0=True, kind="mixed", seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = {"q": r(B, T, Hk, dk) / dk ** 0.5, "k": r(B, T, Hk, dk) / dk ** 0.5, "v": r(B, T, H, dv), "do": r(B, T, H, dv)}
+    x = {n: t.to(dtype) for n, t in x.items()}
+    shape = (H,) if fixed else (B, T, H)
+    if kind == "ones":
+        a = torch.ones(shape)
+    else:
+        a = torch.exp(-torch.exp(2.0 * r(*shape) - 3.0))
+        if kind == "mixed" and not fixed:
+            a = torch.where(torch.rand(shape, generator=g) < 0.03, 0.0, a)
+        a[..., 0] = 0.01 if kind == "mixed" else a[..., 0]
+    x["a"] = a
+    x["s0"] = 0.5 * r(B, H, dk, dv) if s0 else None
+    x["ds"] = 0.5 * r(B, H, dk, dv) if s0 else None
+    x["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    return {n: t if t is None else t.to(device) for n, t in x.items()}
+
+
+def absolute(x):
+    return {n: t if t is None or n in ("a", "lens") else t.abs() for n, t in x.items()}
+
+
+def forward64(x):
+    return layer.head_decay_forward(x["q"], x["k"], x["v"], x["a"], x["s0"], x["lens"])
+
+
+def backward64(x):
+    return layer.head_decay_backward(x["q"], x["k"], x["v"], x["a"], x["do"], x["s0"], x["ds"], x["lens"])
+
+
+def forward(x, **kw):
+    return muir.chunk_fwd_head_decay(x["q"], x["k"], x["v"], x["a"], x["s0"], lens=x["lens"], **kw)
+
+
+def backward(x, **kw):
+    return muir.chunk_bwd_head_decay(x["q"], x["k"], x["v"], x["a"], x["s0"], do=x["do"], ds_out=x["ds"],
+                                     lens=x["lens"], **kw)
+
+
+def within(got, want, bound, name):
+    d = (got.double().cpu() - want).abs()
+    assert torch.isfinite(got).all(), name
+    over = (d - bound).max().item() if d.numel() else -1.0
+    print(f"  {name}: worst {d.max().item() if d.numel() else 0:.3e}, over its bound by {over:.3e}", flush=True)
+    assert over <= 0, name
+
+
+def check_forward(x, o, s):
+    dtype, T = x["q"].dtype, x["v"].shape[1]
+    o64, s64 = forward64(x)
+    mo, ms = forward64(absolute(x))
+    u = U[dtype]
+    two = 2 * u if dtype == torch.bfloat16 else 0.0
+    within(o, o64, u * o64.abs() + (two + kf(T)) * (1 + u) * mo + 1e-30, "o")
+    within(s, s64, kf(T) * ms + 1e-30, "s_out")
+
+
+def check_backward(x, g):
+    dtype, T = x["q"].dtype, x["v"].shape[1]
+    want, mag = backward64(x), backward64(absolute(x))
+    u, k = U[dtype], kf(T) * (2 if x["v"].shape[2] > x["q"].shape[2] else 1)
+    for n in ("q", "k"):
+        within(g[n], want[n], u * want[n].abs() + k * (1 + u) * mag[n] + 1e-30, "d" + n)
+    two = 2 * u if dtype == torch.bfloat16 else 0.0
+    within(g["v"], want["v"], u * want["v"].abs() + (two + k) * (1 + u) * mag["v"] + 1e-30, "dv")
+    within(g["s0"], want["s0"], k * mag["s0"] + 1e-30, "ds0")
+    # dla: up to 256 tokens' q.dq and k.dk and one <S, A> (dk dv terms in 64-lane sums of 64: 128 F more).
+    rep = x["v"].shape[2] // x["q"].shape[2]
+    up = lambda t: t.double().abs().cpu().repeat_interleave(rep, 2)  # noqa: E731
+    live = mag["edge"] * 0 + 1 if x["lens"] is None else (
+        torch.arange(T)[None] < x["lens"].cpu().clamp(0, T)[:, None]).double()[..., None].expand_as(mag["edge"])
+    zero = lambda t: torch.where(live[..., None] > 0, t, 0.0)  # noqa: E731
+    terms = (zero(up(x["q"])) * mag["qh"]).sum(-1) + (zero(up(x["k"])) * mag["kh"]).sum(-1)
+    total = torch.zeros_like(terms)
+    for t0 in range(0, T, 256):
+        part = terms[:, t0:t0 + 256]
+        total[:, t0:t0 + 256] = part.flip(1).cumsum(1).flip(1) + mag["edge"][:, min(t0 + 255, T - 1)][:, None]
+    bound = (k + 256 * F) * total * live + 1e-30
+    if x["a"].dim() == 1:
+        bound = bound.sum((0, 1))
+    within(g["la"], want["la"], bound + U[torch.float32] * want["la"].abs(), "dla")
+
+
+CASES = [
+    # B, T, H, Hk, dk, dv, type, fixed, lens, s0, kind
+    (1, 1, 1, 1, 64, 64, "bf16", False, None, False, "mixed"),
+    (2, 1, 4, 2, 128, 128, "f32", False, None, True, "mixed"),
+    (1, 2, 3, 1, 64, 128, "bf16", True, None, True, "mixed"),
+    (2, 63, 2, 2, 128, 64, "bf16", False, None, True, "mixed"),
+    (1, 64, 2, 1, 128, 128, "bf16", False, None, True, "mixed"),
+    (1, 65, 2, 2, 64, 64, "f32", False, None, True, "mixed"),
+    (4, 150, 2, 1, 64, 128, "f32", False, [0, 1, 150, 64], True, "mixed"),
+    (4, 150, 4, 2, 128, 128, "bf16", False, [-3, 129, 999, 65], True, "mixed"),
+    (1, 257, 2, 2, 128, 128, "bf16", False, None, True, "ones"),
+    (1, 700, 2, 1, 64, 64, "bf16", False, None, False, "mixed"),
+    (1, 700, 3, 3, 128, 64, "f32", True, None, True, "slow"),
+    (2, 1111, 2, 2, 64, 128, "bf16", False, [1111, 500], True, "slow"),
+    (1, 1100, 1, 1, 128, 128, "bf16", True, None, True, "slow"),
+    (1, 1025, 2, 2, 128, 128, "f32", False, None, True, "slow"),
+]
+
+
+def ids(c):
+    return "-".join(str(v) for v in c)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_forward(device, case):
+    B, T, H, Hk, dk, dv, typ, fixed, lens, s0, kind = case
+    x = inputs(device, B, T, H, Hk, dk, dv, {"bf16": torch.bfloat16, "f32": torch.float32}[typ], fixed, lens, s0, kind, T)
+    o, s = forward(x)
+    torch.cuda.synchronize()
+    check_forward(x, o, s)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_backward(device, case):
+    B, T, H, Hk, dk, dv, typ, fixed, lens, s0, kind = case
+    x = inputs(device, B, T, H, Hk, dk, dv, {"bf16": torch.bfloat16, "f32": torch.float32}[typ], fixed, lens, s0, kind, T)
+    g = backward(x)
+    torch.cuda.synchronize()
+    check_backward(x, g)
+
+
+@pytest.mark.parametrize("typ", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,H,Hk,dk,dv,fixed", [(1, 1, 1, 64, 64, False), (3, 4, 2, 128, 64, True), (2, 6, 1, 64, 128, False),
+                                                 (5, 16, 16, 128, 128, False), (64, 4, 4, 128, 128, False)])
+def test_step(device, typ, B, H, Hk, dk, dv, fixed):
+    x = inputs(device, B, 3, H, Hk, dk, dv, typ, fixed, None, True, "mixed", B + dk)
+    state = x["s0"].clone()
+    o = torch.stack([muir.decode_step_head_decay(*[x[n][:, t].contiguous() for n in "qkv"],
+                                                 x["a"] if fixed else x["a"][:, t].contiguous(), state)
+                     for t in range(3)], 1)
+    torch.cuda.synchronize()
+    o64, s64 = forward64(x)
+    mo, ms = forward64(absolute(x))
+    # A state element is one fused operation a token beside a rounded product; an output a sum over dk.
+    within(o, o64, U[typ] * o64.abs() + (2 * dk + 12) * F * mo + 1e-30, "o")
+    within(state, s64, 8 * F * ms + 1e-30, "state")
+
+
+def test_no_tokens(device):
+    x = inputs(device, 2, 0, 4, 2, 64, 128, torch.bfloat16)
+    o, s = forward(x)
+    assert o.numel() == 0 and torch.equal(s, x["s0"])
+    _, s = muir.chunk_fwd_head_decay(x["q"], x["k"], x["v"], x["a"])
+    assert s.abs().max().item() == 0
+    g = backward(x)
+    assert torch.equal(g["s0"], x["ds"]) and g["q"].numel() == 0
+    x = inputs(device, 2, 0, 4, 2, 64, 128, torch.float32, fixed=True)
+    g = backward(x)
+    assert torch.equal(g["s0"], x["ds"]) and torch.equal(g["la"], torch.zeros(4, device=device))
+
+
+def test_padding_is_not_read(device):
+    """NaN and infinities behind each sequence's end change nothing, and the outputs there are zeros."""
+    x = inputs(device, 3, 300, 4, 2, 128, 64, torch.bfloat16, False, [0, 70, 299], True)
+    clean_o, clean_s = forward(x)
+    clean = backward(x)
+    y = dict(x)
+    live = torch.arange(300, device=device)[None] < x["lens"][:, None]
+    for n in ("q", "k", "v", "do", "a"):
+        y[n] = x[n].clone()
+        y[n][~live] = float("nan") if n != "v" else float("inf")
+    o, s = forward(y)
+    g = backward(y)
+    assert torch.equal(o, clean_o) and torch.equal(s, clean_s)
+    assert o[~live].abs().max().item() == 0
+    for n in muir.HEAD_DECAY_GRADS:
+        assert torch.equal(g[n], clean[n]), n
+    for n in ("q", "k", "v", "la"):
+        assert g[n][~live].abs().max().item() == 0, n
+
+
+def test_state_carries_over_calls_and_in_place(device):
+    """A sequence in three calls, the state written over its own input, equals one call to the bound of two such sums."""
+    x = inputs(device, 2, 500, 4, 4, 64, 64, torch.float32, False, None, True)
+    o, s = forward(x)
+    state, parts = x["s0"].clone(), []
+    for t0, t1 in ((0, 130), (130, 131), (131, 500)):
+        part = [x[n][:, t0:t1].contiguous() for n in ("q", "k", "v", "a")]
+        po, ps = muir.chunk_fwd_head_decay(*part, state, s_out=state)
+        assert ps is state
+        parts.append(po)
+    mo, ms = forward64(absolute(x))
+    within(torch.cat(parts, 1), o.double().cpu(), 2 * kf(500) * mo + 1e-30, "o")
+    within(state, s.double().cpu(), 2 * kf(500) * ms + 1e-30, "s")
+
+
+def test_chunk_forward_and_steps_agree(device):
+    x = inputs(device, 2, 70, 4, 2, 128, 128, torch.bfloat16)
+    o, s = forward(x)
+    state = x["s0"].clone()
+    outs = [muir.decode_step_head_decay(*[x[n][:, t].contiguous() for n in "qkva"], state) for t in range(70)]
+    mo, ms = forward64(absolute(x))
+    o64, _ = forward64(x)
+    u = U[torch.bfloat16]
+    within(torch.stack(outs, 1), o.double().cpu(), 2 * u * o64.abs() + (2 * u + 2 * kf(70)) * 1.01 * mo, "o")
+    within(state, s.double().cpu(), 2 * kf(70) * ms, "state")
+
+
+def test_repeats_bit_for_bit_with_every_output_given(device):
+    x = inputs(device, 2, 1000, 4, 2, 128, 64, torch.bfloat16, True, [1000, 333])
+    o, s = forward(x)
+    g = backward(x)
+    for _ in range(2):
+        o2 = torch.full_like(o, float("nan"))
+        s2 = torch.full_like(s, float("nan"))
+        ws = torch.full((muir.chunk_bwd_head_decay_workspace_size(2, 1000, 4, 2, 128, 64, muir.MUIR_BF16),), 255,
+                        dtype=torch.uint8, device=device)
+        out = {n: torch.full_like(t, float("nan")) for n, t in g.items()}
+        forward(x, o=o2, s_out=s2, workspace=ws)
+        ws.fill_(255)
+        backward(x, out=out, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(s, s2)
+        for n in g:
+            assert torch.equal(g[n], out[n]), n
+
+
+def test_other_stream_and_graph_replays(device):
+    x = inputs(device, 1, 900, 4, 2, 128, 128, torch.bfloat16, False, [890])
+    o, s = forward(x)
+    g = backward(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device)
+    with torch.cuda.stream(side):
+        o2, s2 = forward(x)
+        g2 = backward(x)
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(s, s2) and all(torch.equal(g[n], g2[n]) for n in g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, s3 = forward(x)
+        g3 = backward(x)
+    for i in range(3):
+        v = x["v"] * (i + 1)
+        keep = x["v"].clone()
+        x["v"].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        eo, es = forward(x)
+        eg = backward(x)
+        assert torch.equal(o3, eo) and torch.equal(s3, es) and all(torch.equal(g3[n], eg[n]) for n in eg)
+        x["v"].copy_(keep)
+
+
+def test_gradients_against_differences(device):
+    """The gradients along a random direction of every input against a central difference of the recurrence in 64
+    bits, L = <o, do> + <s_out, ds>. The difference's own error is far below: L is a polynomial, step 1e-5."""
+    x = inputs(device, 2, 90, 4, 2, 64, 64, torch.float32, False, None, True, "slow")
+    g = backward(x)
+    d64 = {n: t.double().cpu() for n, t in x.items() if t is not None}
+
+    def loss(e, n, direction):
+        y = dict(d64)
+        y[n] = y[n] * torch.exp(e * direction) if n == "a" else y[n] + e * direction
+        o, s = layer.head_decay_forward(y["q"], y["k"], y["v"], y["a"], y["s0"])
+        return (o * d64["do"]).sum() + (s * d64["ds"]).sum()
+
+    mag = backward64(absolute(x))
+    for n, key in (("q", "q"), ("k", "k"), ("v", "v"), ("s0", "s0"), ("a", "la")):
+        r = torch.randn(x[n].shape, generator=torch.Generator().manual_seed(5), dtype=torch.float64)
+        want = (loss(1e-5, n, r) - loss(-1e-5, n, r)) / 2e-5
+        got = (g[key].double().cpu() * r).sum()
+        scale = (mag[key].abs() * r.abs()).sum() if key != "la" else (backward64(x)["la"].abs() * r.abs()).sum() * 64
+        print(f"  {n}: {got.item():.8f} against {want.item():.8f}", flush=True)
+        assert abs(got - want) <= 2 * kf(90) * scale + 1e-7 * scale
