@@ -551,25 +551,53 @@ def decode_step(q, k, v, a, g, e, w, r, state, *, o=None):
     return o
 
 
-def _call(fn, device, *args):
-    """One library call on ``device``'s current stream, with that device current."""
+# The layer operators below are called once per token and layer: their checks are one expression per tensor, and the
+# message is made only when it is false.
+
+def _is(t, name, dtype, shape, index):
+    """``t`` is a contiguous GPU tensor of this type and shape on device ``index`` (or the error says what is not)."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == index and index >= 0
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     import torch
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(device)))
+    _require(t, name, dtype, shape, torch.device("cuda", max(index, 0)))
 
 
-def _out(t, name, dtype, shape, device):
-    """``t`` checked as an output, or a new one."""
+def _call(fn, index, *args):
+    """One library call on device ``index``'s current stream, with that device current."""
+    import torch
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        raise MuirError(status, last_error())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name, dtype, shape, like):
+    """``t`` checked as an output beside ``like``, or a new tensor."""
     import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _require(t, name, dtype, shape, device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _is(t, name, dtype, shape, like.get_device())
     return t
 
 
-def _workspace(t, need, device):
+def _workspace(t, need, like):
+    """(pointer's tensor, bytes): ``t`` checked, a new one, or none where none is needed."""
     import torch
-    return _out(t, "workspace", torch.uint8, (max(need, 1),) if t is None else None, device)
+    if t is None:
+        return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
+    _is(t, "workspace", torch.uint8, t.shape, like.get_device())
+    return t, t.numel()
 
 
 def _rank(t, name, n):
@@ -582,21 +610,23 @@ def _rank(t, name, n):
 
 def _head_decay_inputs(q, k, v, a, s0, lens):
     import torch
-    for name, t in (("q", q), ("v", v)):
-        _rank(t, name, 4)
+    _rank(q, "q", 4)
+    _rank(v, "v", 4)
     B, T, Hk, dk = q.shape
     H, dv = v.shape[2:]
-    dev = q.device
-    for name, t, shape in (("q", q, (B, T, Hk, dk)), ("k", k, (B, T, Hk, dk)), ("v", v, (B, T, H, dv))):
-        _require(t, name, q.dtype, shape, dev)
+    i, dt = q.get_device(), q.dtype
+    _is(q, "q", dt, (B, T, Hk, dk), i)
+    _is(k, "k", dt, (B, T, Hk, dk), i)
+    _is(v, "v", dt, (B, T, H, dv), i)
     code = _dtype_code(q)
-    per_token = not (isinstance(a, torch.Tensor) and a.dim() == 1)
-    _require(a, "a", torch.float32, (B, T, H) if per_token else (H,), dev)
+    _rank(a, "a", 1 if getattr(a, "ndim", 3) == 1 else 3)
+    per_token = a.ndim == 3
+    _is(a, "a", torch.float32, (B, T, H) if per_token else (H,), i)
     if s0 is not None:
-        _require(s0, "s0", torch.float32, (B, H, dk, dv), dev)
+        _is(s0, "s0", torch.float32, (B, H, dk, dv), i)
     if lens is not None:
-        _require(lens, "lens", torch.int32, (B,), dev)
-    return (B, T, H, Hk, dk, dv), int(per_token), code, dev
+        _is(lens, "lens", torch.int32, (B,), i)
+    return (B, T, H, Hk, dk, dv), int(per_token), code, i
 
 
 def chunk_fwd_head_decay_workspace_size(B: int, T: int, H: int, Hk: int, dk: int, dv: int,
@@ -617,15 +647,15 @@ def chunk_fwd_head_decay(q, k, v, a, s0=None, *, lens=None, o=None, s_out=None,
     may be ``s0`` itself.
     """
     import torch
-    sizes, per_token, code, dev = _head_decay_inputs(q, k, v, a, s0, lens)
+    sizes, per_token, code, i = _head_decay_inputs(q, k, v, a, s0, lens)
     B, T, H, Hk, dk, dv = sizes
-    o = _out(o, "o", q.dtype, (B, T, H, dv), dev)
+    o = _out(o, "o", q.dtype, (B, T, H, dv), q)
     if s_out is not None or return_state:
-        s_out = _out(s_out, "s_out", torch.float32, (B, H, dk, dv), dev)
-    workspace = _workspace(workspace, chunk_fwd_head_decay_workspace_size(*sizes, code), dev)
-    _call(lib().muir_chunk_fwd_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0),
-          _ptr(lens), _ptr(o), _ptr(s_out), *sizes, per_token, code, _ptr(workspace),
-          workspace.numel())
+        s_out = _out(s_out, "s_out", torch.float32, (B, H, dk, dv), q)
+    workspace, size = _workspace(workspace, chunk_fwd_head_decay_workspace_size(*sizes, code), q)
+    _call(lib().muir_chunk_fwd_head_decay, i, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          a.data_ptr(), _at(s0), _at(lens), o.data_ptr(), _at(s_out), B, T, H, Hk, dk, dv,
+          per_token, code, _at(workspace), size)
     return o, s_out
 
 
@@ -648,21 +678,22 @@ def chunk_bwd_head_decay(q, k, v, a, s0=None, *, do, ds_out=None, lens=None, wor
     tokens behind ``lens`` are zeros. ``out`` may hold pre-allocated tensors under those keys.
     """
     import torch
-    sizes, per_token, code, dev = _head_decay_inputs(q, k, v, a, s0, lens)
+    sizes, per_token, code, i = _head_decay_inputs(q, k, v, a, s0, lens)
     B, T, H, Hk, dk, dv = sizes
-    _require(do, "do", q.dtype, (B, T, H, dv), dev)
-    if ds_out is not None:
-        _require(ds_out, "ds_out", torch.float32, (B, H, dk, dv), dev)
-    out = dict(out or {})
     f32 = torch.float32
+    _is(do, "do", q.dtype, (B, T, H, dv), i)
+    if ds_out is not None:
+        _is(ds_out, "ds_out", f32, (B, H, dk, dv), i)
+    out = dict(out) if out else {}
     for n, dtype, shape in (("q", q.dtype, q.shape), ("k", q.dtype, k.shape),
                             ("v", q.dtype, v.shape), ("la", f32, a.shape),
                             ("s0", f32, (B, H, dk, dv))):
-        out[n] = _out(out.get(n), "d" + n, dtype, tuple(shape), dev)
-    workspace = _workspace(workspace, chunk_bwd_head_decay_workspace_size(*sizes, code), dev)
-    _call(lib().muir_chunk_bwd_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(s0),
-          _ptr(lens), _ptr(do), _ptr(ds_out), *[_ptr(out[n]) for n in HEAD_DECAY_GRADS], *sizes,
-          per_token, code, _ptr(workspace), workspace.numel())
+        out[n] = _out(out.get(n), "d" + n, dtype, shape, q)
+    workspace, size = _workspace(workspace, chunk_bwd_head_decay_workspace_size(*sizes, code), q)
+    _call(lib().muir_chunk_bwd_head_decay, i, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          a.data_ptr(), _at(s0), _at(lens), do.data_ptr(), _at(ds_out),
+          *[out[n].data_ptr() for n in HEAD_DECAY_GRADS], B, T, H, Hk, dk, dv, per_token, code,
+          _at(workspace), size)
     return out
 
 
@@ -674,20 +705,25 @@ def decode_step_head_decay(q, k, v, a, state, *, o=None):
     [B,H,dk,dv] float32. Returns o [B,H,dv] (q/k/v dtype).
     """
     import torch
-    for name, t in (("q", q), ("v", v)):
-        _rank(t, name, 3)
+    _rank(q, "q", 3)
+    _rank(v, "v", 3)
     B, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    dev = q.device
-    for name, t, shape in (("q", q, (B, Hk, dk)), ("k", k, (B, Hk, dk)), ("v", v, (B, H, dv))):
-        _require(t, name, q.dtype, shape, dev)
+    _, H, dv = v.shape
+    i, dt = q.get_device(), q.dtype
+    _is(q, "q", dt, (B, Hk, dk), i)
+    _is(k, "k", dt, (B, Hk, dk), i)
+    _is(v, "v", dt, (B, H, dv), i)
     code = _dtype_code(q)
-    per_token = not (isinstance(a, torch.Tensor) and a.dim() == 1)
-    _require(a, "a", torch.float32, (B, H) if per_token else (H,), dev)
-    _require(state, "state", torch.float32, (B, H, dk, dv), dev)
-    o = _out(o, "o", q.dtype, (B, H, dv), dev)
-    _call(lib().muir_decode_step_head_decay, dev, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(state),
-          _ptr(o), B, H, Hk, dk, dv, int(per_token), code)
+    _rank(a, "a", 1 if getattr(a, "ndim", 2) == 1 else 2)
+    per_token = a.ndim == 2
+    _is(a, "a", torch.float32, (B, H) if per_token else (H,), i)
+    _is(state, "state", torch.float32, (B, H, dk, dv), i)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _is(o, "o", dt, (B, H, dv), i)
+    _call(lib().muir_decode_step_head_decay, i, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          a.data_ptr(), state.data_ptr(), o.data_ptr(), B, H, Hk, dk, dv, per_token, code)
     return o
 
 
@@ -695,19 +731,21 @@ def _norm_inputs(x, weight, residual, h):
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor with at least one dimension")
-    D, dev = x.shape[-1], x.device
-    code = _dtype_code(x)
-    _require(x, "x", x.dtype, None, dev)
-    _require(weight, "weight", torch.float32, (D,), dev)
-    hcode = code
-    if residual is None:
-        if h is not None:
-            raise ValueError("h is written only with a residual")
-    else:
-        _require(residual, "residual", residual.dtype, tuple(x.shape), dev)
+    shape, i = x.shape, x.get_device()
+    D = shape[-1]
+    code = hcode = _dtype_code(x)
+    _is(x, "x", x.dtype, shape, i)
+    _is(weight, "weight", torch.float32, (D,), i)
+    if residual is not None:
+        _is(residual, "residual", getattr(residual, "dtype", None), shape, i)
         hcode = _dtype_code(residual)
-        h = _out(h, "h", residual.dtype, tuple(x.shape), dev)
-    return x.numel() // D if D else 0, D, dev, code, hcode, h
+        if h is None:
+            h = torch.empty_like(residual)
+        else:
+            _is(h, "h", residual.dtype, shape, i)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    return x.numel() // D if D else 0, D, i, code, hcode, h
 
 
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None):
@@ -720,11 +758,14 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None):
     itself (in place).
     """
     import torch
-    rows, D, dev, code, hcode, h = _norm_inputs(x, weight, residual, h)
-    y = _out(y, "y", x.dtype, tuple(x.shape), dev)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _call(lib().muir_rms_norm, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
-          _ptr(rstd), rows, D, eps, code, hcode)
+    rows, D, i, code, hcode, h = _norm_inputs(x, weight, residual, h)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _is(y, "y", x.dtype, x.shape, i)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _call(lib().muir_rms_norm, i, x.data_ptr(), _at(residual), weight.data_ptr(), _at(h),
+          y.data_ptr(), rstd.data_ptr(), rows, D, eps, code, hcode)
     return y, x if residual is None else h, rstd
 
 
@@ -743,21 +784,23 @@ def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspa
     import torch
     if not isinstance(h, torch.Tensor) or h.dim() < 1:
         raise TypeError("h must be a torch.Tensor with at least one dimension")
-    D, dev = h.shape[-1], h.device
+    shape, i = h.shape, h.get_device()
+    D = shape[-1]
     rows = h.numel() // D if D else 0
     hcode = _dtype_code(h)
-    _require(h, "h", h.dtype, None, dev)
-    _require(dy, "dy", dy.dtype if isinstance(dy, torch.Tensor) else None, tuple(h.shape), dev)
+    _is(h, "h", h.dtype, shape, i)
+    _is(dy, "dy", getattr(dy, "dtype", None), shape, i)
     code = _dtype_code(dy)
-    _require(weight, "weight", torch.float32, (D,), dev)
-    _require(rstd, "rstd", torch.float32, tuple(h.shape[:-1]), dev)
+    _is(weight, "weight", torch.float32, (D,), i)
+    _is(rstd, "rstd", torch.float32, shape[:-1], i)
     if dh is not None:
-        _require(dh, "dh", h.dtype, tuple(h.shape), dev)
-    dx = _out(dx, "dx", h.dtype, tuple(h.shape), dev)
-    dweight = _out(dweight, "dweight", torch.float32, (D,), dev)
-    workspace = _workspace(workspace, rms_norm_bwd_workspace_size(rows, D), dev)
-    _call(lib().muir_rms_norm_bwd, dev, _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh),
-          _ptr(dx), _ptr(dweight), rows, D, code, hcode, _ptr(workspace), workspace.numel())
+        _is(dh, "dh", h.dtype, shape, i)
+    dx = _out(dx, "dx", h.dtype, shape, h)
+    dweight = _out(dweight, "dweight", torch.float32, (D,), h)
+    workspace, size = _workspace(workspace, rms_norm_bwd_workspace_size(rows, D), h)
+    _call(lib().muir_rms_norm_bwd, i, dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
+          rstd.data_ptr(), _at(dh), dx.data_ptr(), dweight.data_ptr(), rows, D, code, hcode,
+          _at(workspace), size)
     return dx, dweight
 
 
@@ -771,16 +814,18 @@ def rms_norm_8bit(x, weight, residual=None, *, eps: float = 1e-6, format: str = 
     :func:`rms_norm`.
     """
     import torch
-    formats = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
-    if format not in formats:
-        raise ValueError(f"format must be one of {sorted(formats)}, got {format!r}")
-    fmt, dtype = formats[format]
-    rows, D, dev, code, hcode, h = _norm_inputs(x, weight, residual, h)
-    y = _out(y, "y", dtype, tuple(x.shape), dev)
-    shape = tuple(x.shape[:-1]) + ((D // group,) if group > 0 else ())
-    scale = _out(scale, "scale", torch.float32, shape, dev)
-    _call(lib().muir_rms_norm_8bit, dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
-          _ptr(scale), rows, D, eps, fmt, group, code, hcode)
+    if format == "e4m3":
+        fmt, dtype = 0, torch.float8_e4m3fn
+    elif format == "int8":
+        fmt, dtype = 1, torch.int8
+    else:
+        raise ValueError(f'format must be "e4m3" or "int8", got {format!r}')
+    rows, D, i, code, hcode, h = _norm_inputs(x, weight, residual, h)
+    y = _out(y, "y", dtype, x.shape, x)
+    shape = x.shape[:-1] + ((D // group,) if group > 0 else ())
+    scale = _out(scale, "scale", torch.float32, shape, x)
+    _call(lib().muir_rms_norm_8bit, i, x.data_ptr(), _at(residual), weight.data_ptr(), _at(h),
+          y.data_ptr(), scale.data_ptr(), rows, D, eps, fmt, group, code, hcode)
     return y, scale, x if residual is None else h
 
 
@@ -796,18 +841,17 @@ def matvec_q4(x, w, scale, zero=None, *, group: int = 128, y=None):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a torch.Tensor with at least one dimension")
     _rank(w, "w", 2)
-    K, N, dev = x.shape[-1], w.shape[0], x.device
+    K, N, i = x.shape[-1], w.shape[0], x.get_device()
     code = _dtype_code(x)
     if group <= 0 or K % 2 or K % group:
         raise ValueError(f"K={K} must be a multiple of the group, {group}")
-    _require(x, "x", x.dtype, None, dev)
-    _require(w, "w", torch.uint8, (N, K // 2), dev)
-    _require(scale, "scale", scale.dtype if isinstance(scale, torch.Tensor) else None,
-             (N, K // group), dev)
+    _is(x, "x", x.dtype, x.shape, i)
+    _is(w, "w", torch.uint8, (N, K // 2), i)
+    _is(scale, "scale", getattr(scale, "dtype", None), (N, K // group), i)
     scode = _dtype_code(scale)
     if zero is not None:
-        _require(zero, "zero", scale.dtype, (N, K // group), dev)
-    y = _out(y, "y", x.dtype, tuple(x.shape[:-1]) + (N,), dev)
-    _call(lib().muir_matvec_q4, dev, _ptr(x), _ptr(w), _ptr(scale), _ptr(zero), _ptr(y),
-          x.numel() // K if K else 0, N, K, group, code, scode)
+        _is(zero, "zero", scale.dtype, (N, K // group), i)
+    y = _out(y, "y", x.dtype, x.shape[:-1] + (N,), x)
+    _call(lib().muir_matvec_q4, i, x.data_ptr(), w.data_ptr(), scale.data_ptr(), _at(zero),
+          y.data_ptr(), x.numel() // K if K else 0, N, K, group, code, scode)
     return y

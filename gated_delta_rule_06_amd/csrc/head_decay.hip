@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "head_decay.hpp"
+#include "launch.hpp"
 #include "op_kernels.hpp"
 
 namespace muir {
@@ -418,8 +419,7 @@ template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, 
 hipError_t launch_pass(const PassArgs &p, hipStream_t stream) {
     auto kern = pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>;
     constexpr int bytes = PassLds<T, DX, DZ, LOCAL, NTP>::BYTES;
-    const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const hipError_t err = allow_lds<pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>>(bytes);
     if (err != hipSuccess) return err;
     const unsigned grid = static_cast<unsigned>(p.B) * p.H * p.nseg;
     hipLaunchKernelGGL(kern, dim3(grid), dim3(THREADS), bytes, stream, p);

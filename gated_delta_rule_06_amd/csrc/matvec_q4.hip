@@ -2,22 +2,25 @@
 //
 // What bounds it is reading the weights once (N K / 2 bytes). The products run on the matrix cores with rows m of x
 // as A and 16 weight rows as B, contraction 32 at a time and so inside one group: nibbles become the bf16
-// numbers 16 + nib (exact, two to three operations for two of them: the nibble moves to mantissa bits 3..6 of
+// numbers 16 + nib (exact, a shift and a mask-or for two of them: the nibble moves to mantissa bits 3..6 of
 // 16.0), and a group's sum is finished in float32 as scale (sum x (16 + nib) - (16 + zero) sum x). The second
 // sum is a product with ones, shared by the NT weight tiles of a wavefront. float32 x goes in as three bf16
 // terms (to its last bit or two).
 //
-// A lane loads 16 bytes, 32 weights of one row, and the four lanes of a row exchange them (4x4 transpose in
-// registers) so that each product's contraction is 32 consecutive columns. The wavefronts of a workgroup split
-// K; their sums meet in LDS in a fixed order.
+// A workgroup walks K in tiles of 1024 columns, 128 to each of its eight wavefronts, whose sums meet in LDS in a fixed
+// order. A tile's weights, x and scales come as whole cache lines through LDS, the next tile's in flight. Reading
+// them straight into the lanes that multiply them (16 rows, 64 bytes each, the scales one by one) took 51 us at
+// M = 16, N = 16384, K = 8192, G = 64 where this takes 24: the vector cache looks up every row of a load on its own.
+// Fetching two or three tiles ahead changed nothing. A lane takes 16 bytes, 32 weights of one row, from
+// LDS, and the four lanes of a row exchange them (4x4 transpose in registers) so that each product's contraction
+// is 32 consecutive columns.
 #include "common.hpp"
+#include "launch.hpp"
 #include "mfma.hpp"
 #include "op_kernels.hpp"
 
 namespace muir {
 namespace {
-
-constexpr int WAVES = 8;
 
 // Lanes 16 g + m: on entry dword u of lane g is dword u of chunk g, on return dword g of chunk u.
 __device__ __forceinline__ void exchange(uint4 &d) {
@@ -29,9 +32,9 @@ __device__ __forceinline__ void exchange(uint4 &d) {
 }
 
 // The eight nibbles of a dword as bf16 16 + nib, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8_t nibbles(uint32_t w) {
-    constexpr uint32_t M = 0x00780078u, B = 0x41804180u;
-    const uint4 u{((w << 3) & M) | B, ((w >> 1) & M) | B, ((w >> 5) & M) | B, ((w >> 9) & M) | B};
+__device__ __forceinline__ bf16x8_t nibbles(uint32_t w, uint32_t base) {
+    constexpr uint32_t M = 0x00780078u;
+    const uint4 u{((w << 3) & M) | base, ((w >> 1) & M) | base, ((w >> 5) & M) | base, ((w >> 9) & M) | base};
     return __builtin_bit_cast(bf16x8_t, u);
 }
 
@@ -58,115 +61,201 @@ __device__ __forceinline__ XFrag<3> x_frag(const float *p) {
     return r;
 }
 
-template <typename XT, typename ST, int NT, int GROUP>
+// LDS of one step: 16 NT rows of weights, 16 rows of bf16 x, the groups' scales with 16 + zero beside them.
+template <typename XT, int NT, int WAVES, int GROUP> constexpr int q4_tile_bytes() {
+    const int sc = 16 * NT * (WAVES * (128 / GROUP) + 1) * 8;
+    return 16 * NT * (WAVES * 64 + 16) + (sizeof(XT) == 2 ? 16 * (WAVES * 256 + 16) : 0) + (sc + 15) / 16 * 16;
+}
+
+template <typename XT, typename ST, int NT, int WAVES, int GROUP, bool ZERO>
 __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restrict__ x, const uint8_t *__restrict__ w,
                                                                const ST *__restrict__ scale, const ST *__restrict__ zero,
                                                                XT *__restrict__ y, int M, int N, int K) {
     constexpr int NX = sizeof(XT) == 2 ? 1 : 3;
-    constexpr int PER = GROUP / 32;  // products of a group
-    __shared__ f32x4_t sh[WAVES][NT][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    constexpr bool XLDS = NX == 1;
+    constexpr int PER = GROUP / 32, NG = 4 / PER;  // products of a group, groups of a step
+    constexpr int THREADS = WAVES * 64, KT = WAVES * 128;
+    constexpr int WC = KT / 32, XC = KT / 8;             // 16-byte chunks of a row of the tile
+    constexpr int LW = WC * 16 + 16, LX = XC * 16 + 16;  // row strides, padded by 16 bytes: rows in different banks
+    constexpr int NWL = 16 * NT * WC / THREADS, NXL = XLDS ? 16 * XC / THREADS : 1;
+    static_assert(16 * NT * WC % THREADS == 0 && 16 * XC % THREADS == 0, "whole chunks");
+    constexpr int SC = WAVES * NG, NSCALE = 16 * NT * SC, NSL = (NSCALE + THREADS - 1) / THREADS;  // scales of the tile
+    constexpr int LS = SC + 1;                                                                    // row stride, in pairs
+    constexpr int XAT = 16 * NT * LW, SAT = XAT + (XLDS ? 16 * LX : 0), TILE = q4_tile_bytes<XT, NT, WAVES, GROUP>();
+    static_assert(TILE >= SAT + 16 * NT * LS * 8, "tile");
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, m = lane & 15, g = lane >> 4;
     const int mt = blockIdx.y * 16, n0 = blockIdx.x * (16 * NT), KG = K / GROUP;
-    const int steps = (K + 127) / 128;
-    const int s0 = steps * wv / WAVES, s1 = steps * (wv + 1) / WAVES;
-    const XT *xr = x + static_cast<size_t>(mt + m < M ? mt + m : 0) * K;
-    const uint8_t *wr[NT];
-    const ST *sr[NT], *zr[NT];
+    const int tiles = (K + KT - 1) / KT, live = min(M - mt, 16), rows = N - n0;
+    // One base for the workgroup; a lane's own offsets fit 32 bits (64 rows of at most 2^25 bytes).
+    const uint8_t *wb = w + static_cast<size_t>(n0) * (K / 2);
+    const ST *sb = scale + static_cast<size_t>(n0) * KG, *zb = ZERO ? zero + static_cast<size_t>(n0) * KG : nullptr;
+    const XT *xb = x + static_cast<size_t>(mt) * K;
+
+    uint32_t base = 0x41804180u;  // 16.0 twice, kept in a register: mask and or are then one instruction
+    asm volatile("" : "+v"(base));
+
+    // What a step needs from memory, fetched while the step before is multiplied.
+    struct Step {
+        uint4 w[NWL], x[NXL];
+        ST sc[NSL], zp[NSL];
+    };
+    Step ahead;
+    auto fetch = [&](Step &f, int t) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int n = min(n0 + 16 * t + m, N - 1);  // rows behind the last are computed and not stored
-        wr[t] = w + static_cast<size_t>(n) * (K / 2);
-        sr[t] = scale + static_cast<size_t>(n) * KG;
-        zr[t] = zero ? zero + static_cast<size_t>(n) * KG : nullptr;
-    }
+        for (int j = 0; j < NWL; ++j) {
+            const int i = tid + THREADS * j, k = t * KT + i % WC * 32;
+            // Rows behind the last are the last again, computed and not stored.
+            const uint32_t at = static_cast<uint32_t>(min(i / WC, rows - 1)) * (K / 2) + k / 2;
+            f.w[j] = k < K ? *reinterpret_cast<const uint4 *>(wb + at) : uint4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < NSL; ++j) {
+            const int i = tid + THREADS * j;
+            const uint32_t at = static_cast<uint32_t>(min(i / SC, rows - 1)) * KG + min(t * SC + i % SC, KG - 1);
+            if (NSCALE % THREADS == 0 || i < NSCALE) {
+                f.sc[j] = sb[at];
+                if constexpr (ZERO) f.zp[j] = zb[at];
+            }
+        }
+        if constexpr (XLDS) {
+#pragma unroll
+            for (int j = 0; j < NXL; ++j) {
+                const int i = tid + THREADS * j, row = i / XC, k = t * KT + i % XC * 8;
+                f.x[j] = k < K && row < live ? *reinterpret_cast<const uint4 *>(xb + static_cast<size_t>(row) * K + k) : uint4{0, 0, 0, 0};
+            }
+        }
+    };
     bf16x8_t ones;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ones[j] = static_cast<__bf16>(1.0f);
-
     f32x4_t sum[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) sum[t] = zero4();
-    for (int s = s0; s < s1; ++s) {
-        const int k0 = 128 * s;
-        uint4 d[NT];
+
+    auto step = [&](Step &f, int t) {
+        unsigned char *lw = smem + (t & 1) * TILE, *lx = lw + XAT;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            d[t] = k0 + 32 * g < K ? *reinterpret_cast<const uint4 *>(wr[t] + (k0 + 32 * g) / 2) : uint4{0, 0, 0, 0};
+        for (int j = 0; j < NWL; ++j) {
+            const int i = tid + THREADS * j;
+            *reinterpret_cast<uint4 *>(lw + i / WC * LW + i % WC * 16) = f.w[j];
+        }
+        if constexpr (XLDS) {
+#pragma unroll
+            for (int j = 0; j < NXL; ++j) {
+                const int i = tid + THREADS * j;
+                if (i / XC < live) *reinterpret_cast<uint4 *>(lx + i / XC * LX + i % XC * 16) = f.x[j];
+            }
+        }
+        float2 *ls = reinterpret_cast<float2 *>(lw + SAT);
+#pragma unroll
+        for (int j = 0; j < NSL; ++j) {
+            const int i = tid + THREADS * j;
+            float2 v{to_f32(f.sc[j]), 24.f};
+            if constexpr (ZERO) v.y = 16.f + to_f32(f.zp[j]);
+            if (NSCALE % THREADS == 0 || i < NSCALE) ls[i / SC * LS + i % SC] = v;
+        }
+        if (t + 1 < tiles) fetch(f, t + 1);
+        lds_barrier();
+        // This wavefront's 128 columns of the tile.
+        const int k0 = t * KT + 128 * wv;
+        if (k0 >= K) return;
         XFrag<NX> fx[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int k = k0 + 32 * u + 8 * g;
-            if (k < K && mt + m < M) {
-                fx[u] = x_frag(xr + k);
-            } else {
+            const int k = 32 * u + 8 * g;
 #pragma unroll
-                for (int n = 0; n < NX; ++n) fx[u].f[n] = Mma<bf16_t>::zero();
+            for (int n = 0; n < NX; ++n) fx[u].f[n] = Mma<bf16_t>::zero();
+            if constexpr (XLDS) {
+                if (m < live) fx[u] = x_frag(reinterpret_cast<const XT *>(lx + m * LX) + 128 * wv + k);
+            } else {
+                if (m < live && k0 + k < K) fx[u] = x_frag(xb + static_cast<size_t>(m) * K + k0 + k);
             }
         }
-        float sc[NT][4 / PER], zp[NT][4 / PER];
+        uint4 d[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int n = 0; n < NT; ++n) {
+            d[n] = *reinterpret_cast<const uint4 *>(lw + (16 * n + m) * LW + (4 * wv + g) * 16);
+            exchange(d[n]);
+        }
 #pragma unroll
-            for (int q = 0; q < 4 / PER; ++q) {
-                const int kg = min(k0 / GROUP + q, KG - 1);
-                sc[t][q] = to_f32(sr[t][kg]);
-                zp[t][q] = 16.f + (zr[t] ? to_f32(zr[t][kg]) : 8.f);
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) exchange(d[t]);
-#pragma unroll
-        for (int q = 0; q < 4 / PER; ++q) {
+        for (int q = 0; q < NG; ++q) {
             f32x4_t xs = zero4(), acc[NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = zero4();
+            for (int n = 0; n < NT; ++n) acc[n] = zero4();
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
                 const int u = q * PER + e;
 #pragma unroll
-                for (int n = NX - 1; n >= 0; --n) xs = Mma<bf16_t>::mma(fx[u].f[n], ones, xs);
+                for (int c = NX - 1; c >= 0; --c) xs = Mma<bf16_t>::mma(fx[u].f[c], ones, xs);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint32_t dw[4] = {d[t].x, d[t].y, d[t].z, d[t].w};
-                    const bf16x8_t fw = nibbles(dw[u]);
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t dw[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
+                    const bf16x8_t fw = nibbles(dw[u], base);
 #pragma unroll
-                    for (int n = NX - 1; n >= 0; --n) acc[t] = Mma<bf16_t>::mma(fx[u].f[n], fw, acc[t]);
+                    for (int c = NX - 1; c >= 0; --c) acc[n] = Mma<bf16_t>::mma(fx[u].f[c], fw, acc[n]);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int n = 0; n < NT; ++n) {
+                const float2 v = ls[(16 * n + m) * LS + wv * NG + q];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[t][i] = fmaf(sc[t][q], fmaf(-zp[t][q], xs[i], acc[t][i]), sum[t][i]);
+                for (int i = 0; i < 4; ++i) sum[n][i] = fmaf(v.x, fmaf(-v.y, xs[i], acc[n][i]), sum[n][i]);
+            }
         }
-    }
+    };
+    fetch(ahead, 0);
+    for (int t = 0; t < tiles; ++t) step(ahead, t);
+    __syncthreads();
+    f32x4_t *sh = reinterpret_cast<f32x4_t *>(smem);  // [WAVES][NT][64]
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sh[wv][t][lane] = sum[t];
+    for (int t = 0; t < NT; ++t) sh[(wv * NT + t) * 64 + lane] = sum[t];
     __syncthreads();
     if (wv >= NT) return;
     // Wavefront t finishes weight tile t: rows m = 4 g + i of x, column n = lane % 16.
-    f32x4_t r = sh[0][wv][lane];
+    f32x4_t r = sh[wv * 64 + lane];
 #pragma unroll
-    for (int i = 1; i < WAVES; ++i) r += sh[i][wv][lane];
+    for (int i = 1; i < WAVES; ++i) r += sh[(i * NT + wv) * 64 + lane];
     const int n = n0 + 16 * wv + m;
     if (n >= N) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (mt + 4 * g + i < M) elem<XT>::store(y, static_cast<size_t>(mt + 4 * g + i) * N + n, r[i]);
+        if (4 * g + i < live) elem<XT>::store(y, static_cast<size_t>(mt + 4 * g + i) * N + n, r[i]);
 }
 
-template <typename XT, typename ST, int NT>
+template <typename XT, typename ST, int NT, int WAVES>
 hipError_t go(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K, int group,
               hipStream_t s) {
+    static_assert(WAVES >= NT, "a wavefront finishes each tile");
     const dim3 grid((N + 16 * NT - 1) / (16 * NT), (M + 15) / 16), block(WAVES * 64);
-#define MUIR_Q4(G)                                                                                                  \
-    if (group == G) {                                                                                               \
-        hipLaunchKernelGGL((matvec_q4_kernel<XT, ST, NT, G>), grid, block, 0, s, static_cast<const XT *>(x),        \
+#define MUIR_Q4(G, Z)                                                                                               \
+    if (group == G && (zero != nullptr) == Z) {                                                                     \
+        auto kern = matvec_q4_kernel<XT, ST, NT, WAVES, G, Z>;                                               \
+        constexpr int two = 2 * q4_tile_bytes<XT, NT, WAVES, G>(), sums = WAVES * NT * 1024;                        \
+        constexpr int bytes = two > sums ? two : sums;                                                              \
+        const hipError_t err = allow_lds<matvec_q4_kernel<XT, ST, NT, WAVES, G, Z>>(bytes);                            \
+        if (err != hipSuccess) return err;                                                                          \
+        hipLaunchKernelGGL(kern, grid, block, bytes, s, static_cast<const XT *>(x),                                 \
                            static_cast<const uint8_t *>(w), static_cast<const ST *>(scale),                         \
                            static_cast<const ST *>(zero), static_cast<XT *>(y), M, N, K);                           \
         return hipGetLastError();                                                                                   \
     }
-    MUIR_Q4(32) MUIR_Q4(64) MUIR_Q4(128)
+    MUIR_Q4(32, false) MUIR_Q4(64, false) MUIR_Q4(128, false) MUIR_Q4(32, true) MUIR_Q4(64, true) MUIR_Q4(128, true)
 #undef MUIR_Q4
     return hipErrorInvalidValue;
+}
+
+template <typename XT, typename ST>
+hipError_t pick(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K, int group,
+                hipStream_t s) {
+    // As many weight rows to a workgroup as leave one workgroup for each of the 256 compute units: x is read and unpacked
+    // once for them all. At M = 1 (us, for 16, 32 and 64 rows): N = 2048, K = 2048: 3.8, 4.3, 5.6; N = 8192, K = 2048:
+    // 6.8, 4.9, 6.0; N = 16384, K = 8192: 36.3, 26.4, 21.9; M = 64, N = K = 4096 (four times the workgroups): 22.2, 14.3, 10.4.
+    // Four wavefronts instead of eight were slower at each choice but N = 8192 with 16 rows.
+    const long long work = static_cast<long long>(N) * ((M + 15) / 16);
+    if (work >= 256 * 64) return go<XT, ST, 4, 8>(x, w, scale, zero, y, M, N, K, group, s);
+    if (work >= 256 * 32) return go<XT, ST, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);
+    return go<XT, ST, 1, 8>(x, w, scale, zero, y, M, N, K, group, s);
 }
 
 }  // namespace
@@ -174,10 +263,10 @@ hipError_t go(const void *x, const void *w, const void *scale, const void *zero,
 hipError_t launch_matvec_q4(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N,
                             int K, int group, bool bf16, bool scale_bf16, hipStream_t s) {
     if (bf16)
-        return scale_bf16 ? go<bf16_t, bf16_t, 1>(x, w, scale, zero, y, M, N, K, group, s)
-                          : go<bf16_t, float, 1>(x, w, scale, zero, y, M, N, K, group, s);
-    return scale_bf16 ? go<float, bf16_t, 1>(x, w, scale, zero, y, M, N, K, group, s)
-                      : go<float, float, 1>(x, w, scale, zero, y, M, N, K, group, s);
+        return scale_bf16 ? pick<bf16_t, bf16_t>(x, w, scale, zero, y, M, N, K, group, s)
+                          : pick<bf16_t, float>(x, w, scale, zero, y, M, N, K, group, s);
+    return scale_bf16 ? pick<float, bf16_t>(x, w, scale, zero, y, M, N, K, group, s)
+                      : pick<float, float>(x, w, scale, zero, y, M, N, K, group, s);
 }
 
 }  // namespace muir
