@@ -36,33 +36,29 @@ struct PassArgs {
     int B, T, H, nseg, seg_chunks, nchunks;
 };
 
+// A tile of 64 rows of one head on its way from memory to LDS.
 template <typename T, int D> struct Tile {
     static constexpr int VEC = 16 / sizeof(T);
-    static constexpr int LD = D + Op<T>::PAD;
-    static constexpr int N = C * D / VEC / THREADS;  // 16-byte vectors of a thread
-    uint4 r[N];
-    // Rows t0.. of one head; tokens from `end` on are zeros and are not read.
-    __device__ __forceinline__ void load(const T *base, size_t stride, int t0, int end, int tid) {
+    static constexpr int PER = D / VEC, N = C * PER / THREADS;  // 16-byte vectors of a row, of a thread
+    u32x4_t r[N];
+    // Rows from `rows` on are zeros and are not read: the buffer ends there.
+    __device__ __forceinline__ void load(const unsigned char *base, int stride, int rows, int tid) {
+        const rsrc_t b = make_rsrc(base, static_cast<unsigned>(rows) * stride);
+        const int off = tid / PER * stride + tid % PER * 16;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int i = tid + THREADS * j, row = i / (D / VEC), c = i % (D / VEC), t = t0 + row;
-            r[j] = t < end ? *reinterpret_cast<const uint4 *>(base + t * stride + c * VEC) : uint4{0, 0, 0, 0};
-        }
+        for (int j = 0; j < N; ++j) r[j] = __builtin_amdgcn_raw_buffer_load_b128(b, off, j * (THREADS / PER) * stride, 0);
     }
-    __device__ __forceinline__ void put(T *lds, int tid) const {
+    __device__ __forceinline__ void put(unsigned char *lds, int tid) const {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int i = tid + THREADS * j, row = i / (D / VEC), c = i % (D / VEC);
-            *reinterpret_cast<uint4 *>(lds + row * LD + c * VEC) = r[j];
-        }
+        for (int j = 0; j < N; ++j) Op<T>::template put16<D>(lds, (tid + THREADS * j) / PER, (tid + THREADS * j) % PER, r[j]);
     }
 };
 
 template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
-    static constexpr int LDX = DX + Op<T>::PAD, LDZ = DZ + Op<T>::PAD, LDP = C + Op<T>::PAD;
-    static constexpr int Y = 0, Z = Y + C * LDX, X = Z + C * LDZ, P = X + (LOCAL ? 0 : C * LDX);
-    static constexpr int ELEMS = P + (LOCAL ? 0 : NTP * C * LDP);
-    static constexpr int TAIL = ELEMS * sizeof(T);
+    using O = Op<T>;
+    static constexpr int Y = 0, Z = Y + O::template tile_bytes<DX>(), X = Z + O::template tile_bytes<DZ>();
+    static constexpr int P = X + (LOCAL ? 0 : O::template tile_bytes<DX>());
+    static constexpr int TAIL = P + (LOCAL ? 0 : NTP * O::template tile_bytes<C>());
     static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 4 * C * 4;
 };
 
@@ -75,26 +71,30 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
     using O = Op<T>;
     using L = PassLds<T, DX, DZ, LOCAL, NTP>;
     using frag = typename O::frag;
-    constexpr int NCT = DZ / 64, RT = DX / 16;
+    constexpr int NCT = DZ / 64, RT = DX / 16, ES = sizeof(T);
     extern __shared__ __align__(16) unsigned char smem[];
-    T *const lds = reinterpret_cast<T *>(smem);
-    T *const ly = lds + L::Y, *const lz = lds + L::Z, *const lx = lds + L::X, *const lp = lds + L::P;
+    unsigned char *const ly = smem + L::Y, *const lz = smem + L::Z, *const lx = smem + L::X, *const lp = smem + L::P;
     double *const sh_L = reinterpret_cast<double *>(smem + L::TAIL);  // sums of log2 a from the chunk's start
     float *const sh_out = reinterpret_cast<float *>(sh_L + C);        // decay between a token and the start state
     float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
     float *const sh_dot = sh_upd + C;                                 // [4][C]
 
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, m = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, m = lane & 15, g = lane >> 4;
     const int seg = blockIdx.x % p.nseg, bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
     const int end = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
     const int col0 = wv * (DZ / 4);
     const size_t bT = static_cast<size_t>(b) * p.T;
-    const T *gx = LOCAL ? nullptr : static_cast<const T *>(p.x) + (bT * p.hx + h / (p.H / p.hx)) * DX;
-    const T *gy = static_cast<const T *>(p.y) + (bT * p.hy + h / (p.H / p.hy)) * DX;
-    const T *gz = static_cast<const T *>(p.z) + (bT * p.hz + h / (p.H / p.hz)) * DZ;
-    const size_t sx = static_cast<size_t>(p.hx) * DX, sy = static_cast<size_t>(p.hy) * DX,
-                 sz = static_cast<size_t>(p.hz) * DZ;
+    // Row strides in bytes, and the head's first row in each tensor.
+    const int sx = p.hx * DX * ES, sy = p.hy * DX * ES, sz = p.hz * DZ * ES, sw = p.hw * DZ * ES;
+    const int so = p.H * DZ * (p.out_f32 ? 4 : ES);
+    auto head = [&](const void *t, int heads, int D) {
+        return static_cast<const unsigned char *>(t) + (bT * heads + h / (p.H / heads)) * (D * ES);
+    };
+    const unsigned char *gx = LOCAL ? nullptr : head(p.x, p.hx, DX), *gy = head(p.y, p.hy, DX), *gz = head(p.z, p.hz, DZ);
+    const unsigned char *gw = KEEP ? head(p.w, p.hw, DZ) : nullptr;
+    unsigned char *go = LOCAL ? nullptr : static_cast<unsigned char *>(p.out) + (bT * p.H + h) * (DZ * (p.out_f32 ? 4 : ES));
     const int groups = (p.nchunks + ANCHOR - 1) / ANCHOR;
     constexpr int DUMP = DX * DZ;
 
@@ -126,21 +126,24 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
     Tile<T, DZ> rz;
     float ra = 1.f;
     auto fetch = [&](int c) {
-        const int t0 = c * C;
-        if constexpr (!LOCAL) rx.load(gx, sx, t0, end, tid);
-        ry.load(gy, sy, t0, end, tid);
-        rz.load(gz, sz, t0, end, tid);
-        ra = t0 + lane >= end ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+        const int t0 = c * C, rows = min(max(end - t0, 0), C);
+        if constexpr (!LOCAL) rx.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
+        ry.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
+        rz.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
+        ra = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
     };
     if (c0 < c1) fetch(REV ? c1 - 1 : c0);
 
     for (int it = 0; it < c1 - c0; ++it) {
         const int c = REV ? c1 - 1 - it : c0 + it, t0 = c * C;
+        // Addresses that follow from the lane are made anew in each chunk: kept over the loop they would take some forty
+        // registers that the state and the tiles need.
+        asm volatile("" : "+v"(lane), "+v"(m), "+v"(g));
         if constexpr (!LOCAL) rx.put(lx, tid);
         ry.put(ly, tid);
         rz.put(lz, tid);
-        const double Lt = scan64(log2_decay(ra), lane);
-        const double Lc = __shfl(Lt, 63, 64);
+        const double Lt = scan64(log2_decay(ra));
+        const double Lc = lane_value(Lt, 63);
         const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(Lc - Lt));
         if (wv == 0) {
             sh_L[lane] = Lt;
@@ -169,6 +172,20 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                 }
             }
         }
+        // KEEP: the rows that this chunk's outputs are multiplied with, in the accumulators' layout.
+        using pack4_t = std::conditional_t<ES == 2, u32x2_t, u32x4_t>;
+        pack4_t w4[KEEP ? 4 : 1][NCT];
+        if constexpr (KEEP) {
+            const rsrc_t bw = make_rsrc(gw + static_cast<size_t>(t0) * sw, static_cast<unsigned>(min(max(end - t0, 0), C)) * sw);
+            const int off = m * sw + (col0 + 4 * g) * ES;
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    if constexpr (ES == 2) w4[tb][ct] = __builtin_amdgcn_raw_buffer_load_b64(bw, off + 16 * ct * ES, 16 * tb * sw, 0);
+                    else w4[tb][ct] = __builtin_amdgcn_raw_buffer_load_b128(bw, off + 16 * ct * ES, 16 * tb * sw, 0);
+                }
+        }
         if (it + 1 < c1 - c0) fetch(REV ? c - 1 : c + 1);
         lds_barrier();
 
@@ -183,9 +200,9 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                 f32x4_t acc[2] = {zero4(), zero4()};
 #pragma unroll
                 for (int k0 = 0; k0 < DX; k0 += 32) {
-                    const frag fx = O::row(lx, L::LDX, 16 * wv, k0, lane);
+                    const frag fx = O::template row<DX>(lx, 16 * wv, k0, lane);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) acc[u] = O::mma(O::row(ly, L::LDX, 32 * pr + 16 * u, k0, lane), fx, acc[u]);
+                    for (int u = 0; u < 2; ++u) acc[u] = O::mma(O::template row<DX>(ly, 32 * pr + 16 * u, k0, lane), fx, acc[u]);
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -197,7 +214,7 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                         const float d = static_cast<float>(REV ? sh_L[j] - Li : Li - sh_L[j]);
                         v[e] = (REV ? j >= i : j <= i) ? acc[u][e] * exp2_f(d) : 0.f;
                     }
-                    O::template put4<NTP>(lp + i * L::LDP + j0, C * L::LDP, v);
+                    O::template put4<C, NTP>(lp, i, j0 / 4, v);
                 }
             }
             lds_barrier();
@@ -207,7 +224,7 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
 #pragma unroll
         for (int pr = 0; pr < 2; ++pr)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) zf[pr][ct] = O::col(lz, L::LDZ, 32 * pr, col0 + 16 * ct, lane);
+            for (int ct = 0; ct < NCT; ++ct) zf[pr][ct] = O::template col<DZ>(lz, 32 * pr, col0 + 16 * ct, lane);
 
         if constexpr (!LOCAL) {
             // Output tiles with a token in each lane's column: decayed state . x, then P z.
@@ -231,13 +248,14 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                 }
 #pragma unroll
                 for (int tb = 0; tb < 4; ++tb) {
-                    const frag fx = O::row(lx, L::LDX, 16 * tb, 32 * k, lane);
+                    const frag fx = O::template row<DX>(lx, 16 * tb, 32 * k, lane);
 #pragma unroll
                     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                         for (int n = 0; n < NTS; ++n) acc[tb][ct] = O::mma(sf[ct][n], fx, acc[tb][ct]);
                 }
             }
+            const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(min(p.T - t0, C)) * so);
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
                 const float sc = sh_out[16 * tb + m];
@@ -248,35 +266,43 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                     if (REV ? pr < tb / 2 : pr > tb / 2) continue;
 #pragma unroll
                     for (int n = 0; n < NTP; ++n) {
-                        const frag fp = O::row(lp + n * C * L::LDP, L::LDP, 16 * tb, 32 * pr, lane);
+                        const frag fp = O::template row<C>(lp + n * O::template tile_bytes<C>(), 16 * tb, 32 * pr, lane);
 #pragma unroll
                         for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] = O::mma(zf[pr][ct], fp, acc[tb][ct]);
                     }
                 }
-                const int t = t0 + 16 * tb + m;
+                const int t = 16 * tb + m;
+                if (t0 + C > end) {
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct)
+                        if (t0 + t >= end) acc[tb][ct] = zero4();
+                }
                 float dot = 0.f;
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
-                    if (t >= end) acc[tb][ct] = zero4();
                     const int col = col0 + 16 * ct + 4 * g;
-                    if (t < p.T) {
-                        const size_t at = ((bT + t) * p.H + h) * DZ + col;
-                        if (p.out_f32) store4(static_cast<float *>(p.out) + at, acc[tb][ct]);
-                        else store4(static_cast<T *>(p.out) + at, acc[tb][ct]);
+                    if (ES == 4 || p.out_f32) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tb][ct]), bo, m * so + 4 * col, 16 * tb * so, 0);
+                    } else {
+                        u16x4_t u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16(acc[tb][ct][e]);
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, u), bo, m * so + 2 * col, 16 * tb * so, 0);
                     }
                     if constexpr (KEEP) {
-                        if (t < end) {
-                            float w4[4];
-                            load_vec<4>(static_cast<const T *>(p.w) + ((bT + t) * p.hw + h / (p.H / p.hw)) * DZ + col, w4);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) dot += w4[e] * acc[tb][ct][e];
+                        for (int e = 0; e < 4; ++e) {
+                            float w;
+                            if constexpr (ES == 2) w = bf16_to_f32(static_cast<uint16_t>(w4[tb][ct][e / 2] >> (16 * (e % 2))));
+                            else w = __uint_as_float(w4[tb][ct][e]);
+                            dot = fmaf(w, acc[tb][ct][e], dot);
                         }
                     }
                 }
                 if constexpr (KEEP) {
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
-                    if (g == 0) sh_dot[wv * C + 16 * tb + m] = dot;
+                    if (g == 0) sh_dot[wv * C + t] = dot;
                 }
             }
         }
@@ -304,7 +330,7 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const frag fy = O::col(ly, L::LDX, 32 * pr, 16 * rt, lane);
+                const frag fy = O::template col<DX>(ly, 32 * pr, 16 * rt, lane);
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -328,20 +354,20 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
                 for (int ct = 0; ct < NCT; ++ct) at[(rt * NCT + ct) * 64] = S[rt][ct];
         }
     }
-    float *so = nullptr;
+    float *st = nullptr;
     if (LOCAL) {
-        so = p.s_out + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
+        st = p.s_out + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
         if (tid == 0) p.dec[static_cast<size_t>(bh) * p.nseg + seg] = exp2_f(static_cast<float>(seg_log));
     } else if (p.s_out && seg == (REV ? 0 : p.nseg - 1)) {
-        so = p.s_out + static_cast<size_t>(bh) * DUMP;
+        st = p.s_out + static_cast<size_t>(bh) * DUMP;
     }
-    if (so) {
+    if (st) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) so[(16 * rt + 4 * g + i) * DZ + col0 + 16 * ct + m] = S[rt][ct][i];
+                for (int i = 0; i < 4; ++i) st[(16 * rt + 4 * g + i) * DZ + col0 + 16 * ct + m] = S[rt][ct][i];
     }
 }
 
@@ -375,7 +401,7 @@ __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const
     const int end = lens ? min(max(lens[b], 0), T) : T;
     const size_t at = (static_cast<size_t>(b) * T + t) * H + h;
     double x = t < end ? static_cast<double>(rows[at]) - static_cast<double>(cols[at]) : 0.0;
-    x = scan64(x, lane);
+    x = scan64(x);
     if (lane == 63) sh[wv] = x;
     __syncthreads();
     for (int w = 0; w < wv; ++w) x += sh[w];

@@ -13,6 +13,7 @@
 
 #include <type_traits>
 
+#include "chunk_layout.hpp"
 #include "common.hpp"
 #include "mfma.hpp"
 #include "op_layout.hpp"
@@ -29,23 +30,35 @@ constexpr int THREADS = 256;  // four wavefronts, each with a quarter of the sta
 template <typename T> struct Op;
 
 template <> struct Op<bf16_t> {
-    static constexpr int PAD = 8;  // row padding of an LDS tile: rows fall into different banks
     using frag = bf16x8_t;
-    static __device__ __forceinline__ frag row(const bf16_t *t, int ld, int r0, int k0, int lane) {
-        const bf16_t *p = t + (r0 + (lane & 15)) * ld + k0 + 4 * (lane >> 4);
-        const u16x4_t a = *reinterpret_cast<const u16x4_t *>(p);
-        const u16x4_t b = *reinterpret_cast<const u16x4_t *>(p + 16);
+    template <int D> static constexpr int tile_bytes() { return C * D * 2; }
+    // Byte offset of element (r, 4 c) of a tile [64][D]. Tiles have no padding; the 8-byte pieces of a row are permuted
+    // by its number so that both reads below, 32 lanes at a time, take every bank once: `row` takes piece c of 16 rows and
+    // c + 1 (or + 2, + 3), `col` takes four pieces of eight rows. Padded rows serve one of the two: with 272 bytes a row the
+    // transposing reads met in pairs, 2100 of 5200 LDS cycles a chunk. The permutation keeps 16-byte pieces whole.
+    template <int D> static __device__ __forceinline__ int at(int r, int c) {
+        const int f = D == 128 ? ((r & 7) << 2) | ((r >> 2) & 2) : ((r & 6) << 1) | ((r >> 2) & 2);
+        return r * (D * 2) + 8 * (c ^ f);
+    }
+    // r0 and k0 are constants, so what is left at run time is a handful of addresses per tile width.
+    template <int D> static __device__ __forceinline__ frag row(const unsigned char *t, int r0, int k0, int lane) {
+        const int base = at<D>(lane & 15, lane >> 4);
+        const u16x4_t a = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0)) + r0 * (D * 2)));
+        const u16x4_t b = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0 + 32)) + r0 * (D * 2)));
         return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     // Rows of the operand are columns c0.. of the tile. The transposing read gives lane m of a group of 16
     // the column m of the four tile rows whose 32 bytes the group's lanes address.
-    static __device__ __forceinline__ frag col(const bf16_t *t, int ld, int k0, int c0, int lane) {
+    template <int D> static __device__ __forceinline__ frag col(unsigned char *t, int k0, int c0, int lane) {
         typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-        const int m = lane & 15, g = lane >> 4;
-        const bf16_t *p = t + (k0 + 4 * g + (m >> 2)) * ld + c0 + 4 * (m & 3);
-        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * ld));
+        const int m = lane & 15, g = lane >> 4, base = at<D>(4 * g + (m >> 2), m & 3) ^ (2 * c0);
+        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + k0 * (D * 2))));
+        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + (k0 + 16) * (D * 2))));
         return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    // 16 bytes of row r, column piece c (of 8 elements).
+    template <int D> static __device__ __forceinline__ void put16(unsigned char *t, int r, int c, u32x4_t v) {
+        *reinterpret_cast<u32x4_t *>(t + at<D>(r, 2 * c)) = v;
     }
     static __device__ __forceinline__ void floats(frag f, float (&x)[8]) {
         const u16x8_t u = __builtin_bit_cast(u16x8_t, f);
@@ -69,8 +82,8 @@ template <> struct Op<bf16_t> {
     static __device__ __forceinline__ f32x4_t mma(frag a, frag b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    // Four consecutive values as N terms, one to each of N tiles `plane` elements apart.
-    template <int N> static __device__ __forceinline__ void put4(bf16_t *p, int plane, f32x4_t v) {
+    // Four consecutive values of row r from column 4 c on, as N terms, one to each of N tiles of width D.
+    template <int D, int N> static __device__ __forceinline__ void put4(unsigned char *t, int r, int c, f32x4_t v) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             u16x4_t u;
@@ -79,26 +92,33 @@ template <> struct Op<bf16_t> {
                 u[i] = f32_to_bf16(v[i]);
                 if (n + 1 < N) v[i] -= bf16_to_f32(u[i]);
             }
-            *reinterpret_cast<u16x4_t *>(p + n * plane) = u;
+            *reinterpret_cast<u16x4_t *>(t + n * tile_bytes<D>() + at<D>(r, c)) = u;
         }
     }
 };
 
 template <> struct Op<float> {
-    static constexpr int PAD = 4;
     struct frag { float v[8]; };
-    static __device__ __forceinline__ frag row(const float *t, int ld, int r0, int k0, int lane) {
-        const float *p = t + (r0 + (lane & 15)) * ld + k0 + 4 * (lane >> 4);
+    // Rows are padded by four elements: the eight single reads of `col` then take different banks.
+    template <int D> static constexpr int tile_bytes() { return C * (D + 4) * 4; }
+    template <int D> static __device__ __forceinline__ const float *elem(const unsigned char *t, int r, int c) {
+        return reinterpret_cast<const float *>(t) + r * (D + 4) + c;
+    }
+    template <int D> static __device__ __forceinline__ frag row(const unsigned char *t, int r0, int k0, int lane) {
+        const float *p = elem<D>(t, r0 + (lane & 15), k0 + 4 * (lane >> 4));
         const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p);
         const f32x4_t b = *reinterpret_cast<const f32x4_t *>(p + 16);
         return frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
     }
-    static __device__ __forceinline__ frag col(const float *t, int ld, int k0, int c0, int lane) {
-        const float *p = t + (k0 + 4 * (lane >> 4)) * ld + c0 + (lane & 15);
+    template <int D> static __device__ __forceinline__ frag col(unsigned char *t, int k0, int c0, int lane) {
+        const float *p = elem<D>(t, k0 + 4 * (lane >> 4), c0 + (lane & 15));
         frag f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f.v[j] = p[(16 * (j >> 2) + (j & 3)) * ld];
+        for (int j = 0; j < 8; ++j) f.v[j] = p[(16 * (j >> 2) + (j & 3)) * (D + 4)];
         return f;
+    }
+    template <int D> static __device__ __forceinline__ void put16(unsigned char *t, int r, int c, u32x4_t v) {
+        *reinterpret_cast<u32x4_t *>(const_cast<float *>(elem<D>(t, r, 4 * c))) = v;
     }
     static __device__ __forceinline__ void floats(const frag &f, float (&x)[8]) {
 #pragma unroll
@@ -114,9 +134,9 @@ template <> struct Op<float> {
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
         return c;
     }
-    template <int N> static __device__ __forceinline__ void put4(float *p, int, f32x4_t v) {
+    template <int D, int N> static __device__ __forceinline__ void put4(unsigned char *t, int r, int c, f32x4_t v) {
         static_assert(N == 1, "float32 operands are one term");
-        *reinterpret_cast<f32x4_t *>(p) = v;
+        *reinterpret_cast<f32x4_t *>(const_cast<float *>(elem<D>(t, r, 4 * c))) = v;
     }
 };
 
@@ -127,15 +147,33 @@ __device__ __forceinline__ double log2_decay(float a) {
     return l < -200.f ? -200.0 : static_cast<double>(l);
 }
 
-// Inclusive sum over the lanes up to this one. In 64 bits: the sums reach -12800 (64 zeros) while the
-// differences taken of them have to be exact to 2^-24.
-__device__ __forceinline__ double scan64(double x, int lane) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-    }
+// x of the lane that a DPP control names, 0 where it names none.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_or_zero(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Inclusive sum over the lanes up to this one (shifts by 1, 2, 4 and 8 inside rows of 16 lanes, then the last lane of a row
+// to the next one or two). In 64 bits: the sums reach -12800 (64 zeros) while the differences taken of them have to be
+// exact to 2^-24.
+__device__ __forceinline__ double scan64(double x) {
+    x += dpp_or_zero<0x111, 0xf>(x);
+    x += dpp_or_zero<0x112, 0xf>(x);
+    x += dpp_or_zero<0x114, 0xf>(x);
+    x += dpp_or_zero<0x118, 0xf>(x);
+    x += dpp_or_zero<0x142, 0xa>(x);
+    x += dpp_or_zero<0x143, 0xc>(x);
     return x;
+}
+
+// The value of one lane for the whole wavefront.
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }

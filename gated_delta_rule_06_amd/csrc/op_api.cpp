@@ -51,12 +51,14 @@ muir_status_t check_workspace(const char *fn, const void *workspace, size_t have
     return MUIR_OK;
 }
 
-// Largest B * H and B * (T + 64) * H: one workgroup or thread each has to fit a launch.
+// Largest B * H and B * (T + 64) * H: one workgroup or thread each has to fit a launch. Largest H: a chunk's 64 rows
+// are addressed with 32-bit offsets.
 constexpr long long kMaxHeads = 1 << 21, kMaxTokenHeads = 1LL << 31;
+constexpr int kMaxH = 1 << 15;
 
 bool head_sizes_ok(int B, int T, int H, int Hk, int dk, int dv, muir_dtype_t qkv) {
     return B >= 1 && T >= 0 && H >= 1 && Hk >= 1 && H % Hk == 0 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) &&
-           known(qkv) && static_cast<long long>(B) * H <= kMaxHeads &&
+           known(qkv) && H <= kMaxH && static_cast<long long>(B) * H <= kMaxHeads &&
            static_cast<long long>(B) * H <= kMaxTokenHeads / (static_cast<long long>(T) + 64);
 }
 
@@ -68,7 +70,7 @@ muir_status_t check_head_sizes(const char *fn, int B, int T, int H, int Hk, int 
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128))
         return fail(MUIR_ERR_UNSUPPORTED, "%s: dk and dv must be 64 or 128 (got %d, %d)", fn, dk, dv);
     if (!head_sizes_ok(B, T, H, Hk, dk, dv, qkv))
-        return fail(MUIR_ERR_UNSUPPORTED, "%s: B * H above 2^21 or B * (T + 64) * H above 2^31; split the call", fn);
+        return fail(MUIR_ERR_UNSUPPORTED, "%s: H above 2^15, B * H above 2^21 or B * (T + 64) * H above 2^31; split the call", fn);
     return MUIR_OK;
 }
 
