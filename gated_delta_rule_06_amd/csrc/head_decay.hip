@@ -32,12 +32,12 @@ struct PassArgs {
     int hw;
     float *dots;
     float *anchors;         // KEEP: [B*H, groups] states, written in order and read reversed
-    float *edges;           // KEEP, reversed: [B*H, groups, 4] parts of <S, A>
+    float *edges;           // KEEP, reversed: [B*H, groups, DZ / 16] parts of <S, A>
     int B, T, H, nseg, seg_chunks, nchunks;
 };
 
 // A tile of 64 rows of one head on its way from memory to LDS.
-template <typename T, int D> struct Tile {
+template <typename T, int D, int THREADS> struct Tile {
     static constexpr int VEC = 16 / sizeof(T);
     static constexpr int PER = D / VEC, N = C * PER / THREADS;  // 16-byte vectors of a row, of a thread
     u32x4_t r[N];
@@ -56,41 +56,48 @@ template <typename T, int D> struct Tile {
 
 template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
     using O = Op<T>;
+    static constexpr int THREADS = 4 * DZ, NW = DZ / 16;  // one wavefront for 16 columns
     static constexpr int Y = 0, Z = Y + O::template tile_bytes<DX>(), X = Z + O::template tile_bytes<DZ>();
     static constexpr int P = X + (LOCAL ? 0 : O::template tile_bytes<DX>());
     static constexpr int TAIL = P + (LOCAL ? 0 : NTP * O::template tile_bytes<C>());
-    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 4 * C * 4;
+    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + (LOCAL ? 0 : NW * C * 4);
 };
 
-// One wavefront owns DZ / 4 columns of the state and of the output; see head_decay.hpp for the operand order.
+// One wavefront owns 16 columns of the state and of the output; see head_decay.hpp for the operand order.
 // Rounding, for bf16 inputs: the products x.y are exact in float32; D (x.y) and the state go into the second
 // products as NTP and NTS bf16 terms, the decayed z into the state's update as three, so states, and the
 // row sums that the decay's gradient is made of, keep float32 accuracy.
 template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, int NTS, int NTU>
-__global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(PassArgs p) {
+__global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pass_kernel(PassArgs p) {
     using O = Op<T>;
     using L = PassLds<T, DX, DZ, LOCAL, NTP>;
     using frag = typename O::frag;
-    constexpr int NCT = DZ / 64, RT = DX / 16, ES = sizeof(T);
+    constexpr int RT = DX / 16, ES = sizeof(T), THREADS = L::THREADS, NW = L::NW;
+    constexpr int SIDE = KEEP ? 2 : 4;  // sums that are added to in turn, so that a product does not wait for the one before
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char *const ly = smem + L::Y, *const lz = smem + L::Z, *const lx = smem + L::X, *const lp = smem + L::P;
-    double *const sh_L = reinterpret_cast<double *>(smem + L::TAIL);  // sums of log2 a from the chunk's start
+    // Sums of log2 a from the chunk's start, each as a float32 and what it leaves of the 64-bit sum: differences of both
+    // parts are as good as a difference of the sums, and cheaper.
+    f32x2_t *const sh_L = reinterpret_cast<f32x2_t *>(smem + L::TAIL);
     float *const sh_out = reinterpret_cast<float *>(sh_L + C);        // decay between a token and the start state
     float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
-    float *const sh_dot = sh_upd + C;                                 // [4][C]
+    float *const sh_dot = sh_upd + C;                                 // [NW][C]
 
     const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = tid & 63, m = lane & 15, g = lane >> 4;
-    const int seg = blockIdx.x % p.nseg, bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
-    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    const int end = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
-    const int col0 = wv * (DZ / 4);
+    // Quotients and clamped values are made in vector registers; they are the same in every lane, and a buffer's
+    // description has to be known to be.
+    auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    const int bh = uniform(blockIdx.x / p.nseg), seg = blockIdx.x - bh * p.nseg, b = uniform(bh / p.H), h = bh - b * p.H;
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks), steps = c1 - c0;
+    const int end = uniform(p.lens ? min(max(p.lens[b], 0), p.T) : p.T);
+    const int col0 = wv * 16;
     const size_t bT = static_cast<size_t>(b) * p.T;
     // Row strides in bytes, and the head's first row in each tensor.
     const int sx = p.hx * DX * ES, sy = p.hy * DX * ES, sz = p.hz * DZ * ES, sw = p.hw * DZ * ES;
     const int so = p.H * DZ * (p.out_f32 ? 4 : ES);
     auto head = [&](const void *t, int heads, int D) {
-        return static_cast<const unsigned char *>(t) + (bT * heads + h / (p.H / heads)) * (D * ES);
+        return static_cast<const unsigned char *>(t) + (bT * heads + uniform(h / (p.H / heads))) * (D * ES);
     };
     const unsigned char *gx = LOCAL ? nullptr : head(p.x, p.hx, DX), *gy = head(p.y, p.hy, DX), *gz = head(p.z, p.hz, DZ);
     const unsigned char *gw = KEEP ? head(p.w, p.hw, DZ) : nullptr;
@@ -98,43 +105,40 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
     const int groups = (p.nchunks + ANCHOR - 1) / ANCHOR;
     constexpr int DUMP = DX * DZ;
 
-    f32x4_t S[RT][NCT];
+    // The state: tile rt holds rows 16 rt + 4 g .. + 3 of column col0 + m.
+    f32x4_t S[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) S[rt] = zero4();
     if (!LOCAL && p.start) {
         const float *s = p.start + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row = 16 * rt + 4 * g, col = col0 + m;
+            if (p.start_t) {
+                S[rt] = *reinterpret_cast<const f32x4_t *>(s + col * DX + row);
+            } else {
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const int row = 16 * rt + 4 * g, col = col0 + 16 * ct + m;
-                if (p.start_t) {
-                    S[rt][ct] = *reinterpret_cast<const f32x4_t *>(s + col * DX + row);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[rt][ct][i] = s[(row + i) * DZ + col];
-                }
+                for (int i = 0; i < 4; ++i) S[rt][i] = s[(row + i) * DZ + col];
             }
-    } else {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] = zero4();
+        }
     }
     const float a_h = p.a_fixed && p.nchunks > 0 ? p.a[h] : 1.f;
     double seg_log = 0.0;
 
-    Tile<T, DX> rx, ry;
-    Tile<T, DZ> rz;
+    Tile<T, DX, THREADS> rx, ry;
+    Tile<T, DZ, THREADS> rz;
     float ra = 1.f;
-    auto fetch = [&](int c) {
-        const int t0 = c * C, rows = min(max(end - t0, 0), C);
+    // The wavefronts take turns at a chunk's decays.
+    auto fetch = [&](int it) {
+        const int t0 = (REV ? c1 - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
         if constexpr (!LOCAL) rx.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
         ry.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
         rz.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
-        ra = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+        if (wv == it % NW) ra = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
     };
-    if (c0 < c1) fetch(REV ? c1 - 1 : c0);
+    if (steps > 0) fetch(0);
 
-    for (int it = 0; it < c1 - c0; ++it) {
+    for (int it = 0; it < steps; ++it) {
         const int c = REV ? c1 - 1 - it : c0 + it, t0 = c * C;
         // Addresses that follow from the lane are made anew in each chunk: kept over the loop they would take some forty
         // registers that the state and the tiles need.
@@ -142,164 +146,139 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
         if constexpr (!LOCAL) rx.put(lx, tid);
         ry.put(ly, tid);
         rz.put(lz, tid);
-        const double Lt = scan64(log2_decay(ra));
-        const double Lc = lane_value(Lt, 63);
-        const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(Lc - Lt));
-        if (wv == 0) {
-            sh_L[lane] = Lt;
+        if (wv == it % NW) {
+            const double Lt = scan64(log2_decay(ra));
+            const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(lane_value(Lt, 63) - Lt));
+            sh_L[lane] = f32x2_t{static_cast<float>(Lt), static_cast<float>(Lt - static_cast<float>(Lt))};
             sh_out[lane] = REV ? to_end : to_start;
             sh_upd[lane] = REV ? to_start : to_end;
         }
-        const float carry = exp2_f(static_cast<float>(Lc));
-        seg_log += Lc;
         if constexpr (KEEP) {
             // <S, A> at the end of every ANCHOR-th chunk: the pass in order leaves S, the reversed one takes its product.
             if (REV ? (c + 1) % ANCHOR == 0 || c + 1 == p.nchunks : c % ANCHOR == 0 && c > 0) {
                 const int entry = REV ? c / ANCHOR : c / ANCHOR - 1;
                 f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + entry) * DUMP) +
-                              wv * (RT * NCT * 64) + lane;
+                              wv * (RT * 64) + lane;
                 f32x4_t sum = zero4();
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        if constexpr (REV) sum += S[rt][ct] * at[(rt * NCT + ct) * 64];
-                        else at[(rt * NCT + ct) * 64] = S[rt][ct];
-                    }
+                for (int rt = 0; rt < RT; ++rt) {
+                    if constexpr (REV) sum += S[rt] * at[rt * 64];
+                    else at[rt * 64] = S[rt];
+                }
                 if constexpr (REV) {
                     const float e = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-                    if (lane == 0) p.edges[(static_cast<size_t>(bh) * groups + entry) * 4 + wv] = e;
+                    if (lane == 0) p.edges[(static_cast<size_t>(bh) * groups + entry) * NW + wv] = e;
                 }
             }
         }
         // KEEP: the rows that this chunk's outputs are multiplied with, in the accumulators' layout.
         using pack4_t = std::conditional_t<ES == 2, u32x2_t, u32x4_t>;
-        pack4_t w4[KEEP ? 4 : 1][NCT];
+        pack4_t w4[KEEP ? 4 : 1];
         if constexpr (KEEP) {
-            const rsrc_t bw = make_rsrc(gw + static_cast<size_t>(t0) * sw, static_cast<unsigned>(min(max(end - t0, 0), C)) * sw);
+            const rsrc_t bw = make_rsrc(gw + static_cast<size_t>(t0) * sw, static_cast<unsigned>(uniform(min(max(end - t0, 0), C))) * sw);
             const int off = m * sw + (col0 + 4 * g) * ES;
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    if constexpr (ES == 2) w4[tb][ct] = __builtin_amdgcn_raw_buffer_load_b64(bw, off + 16 * ct * ES, 16 * tb * sw, 0);
-                    else w4[tb][ct] = __builtin_amdgcn_raw_buffer_load_b128(bw, off + 16 * ct * ES, 16 * tb * sw, 0);
-                }
+            for (int tb = 0; tb < 4; ++tb) {
+                if constexpr (ES == 2) w4[tb] = __builtin_amdgcn_raw_buffer_load_b64(bw, off, 16 * tb * sw, 0);
+                else w4[tb] = __builtin_amdgcn_raw_buffer_load_b128(bw, off, 16 * tb * sw, 0);
+            }
         }
-        if (it + 1 < c1 - c0) fetch(REV ? c - 1 : c + 1);
+        if (it + 1 < steps) fetch(it + 1);
         lds_barrier();
+        const f32x2_t Lc = sh_L[C - 1];
+        const float carry = exp2_f(Lc[0] + Lc[1]);
+        if constexpr (LOCAL) seg_log += static_cast<double>(Lc[0]) + Lc[1];
+        frag zf[2];
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) zf[pr] = O::template col<DZ>(lz, 32 * pr, col0, lane);
 
         if constexpr (!LOCAL) {
-            // P[i][j] = D (x_i . y_j) of this wavefront's 16 tokens i, over the 32-token blocks of j that it
-            // can reach; the product's rows are j, so a lane stores four consecutive j.
-            const int i = 16 * wv + m;
-            const double Li = sh_L[i];
+            // P[i][j] = D (x_i . y_j) for a block of 16 tokens i and one of 32 tokens j: the six blocks that are not all
+            // zero, one to a wavefront (with four wavefronts, two to some). The product's rows are j, so a lane
+            // stores four consecutive j.
 #pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {
-                if (REV ? pr < wv / 2 : pr > wv / 2) continue;
+            for (int q = 0; q < 8 / NW; ++q) {
+                const int ib = NW == 8 ? wv >> 1 : wv, pr = NW == 8 ? wv & 1 : q;
+                if (REV ? pr < ib / 2 : pr > ib / 2) continue;
+                const int i = 16 * ib + m;
                 f32x4_t acc[2] = {zero4(), zero4()};
 #pragma unroll
                 for (int k0 = 0; k0 < DX; k0 += 32) {
-                    const frag fx = O::template row<DX>(lx, 16 * wv, k0, lane);
+                    const frag fx = O::template row<DX>(lx, 16 * ib, k0, lane);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) acc[u] = O::mma(O::template row<DX>(ly, 32 * pr + 16 * u, k0, lane), fx, acc[u]);
                 }
+                const f32x2_t Li = sh_L[i];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int j0 = 32 * pr + 16 * u + 4 * g;
                     f32x4_t v;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + e;
-                        const float d = static_cast<float>(REV ? sh_L[j] - Li : Li - sh_L[j]);
-                        v[e] = (REV ? j >= i : j <= i) ? acc[u][e] * exp2_f(d) : 0.f;
+                        const f32x2_t d = REV ? sh_L[j0 + e] - Li : Li - sh_L[j0 + e];
+                        const float w = acc[u][e] * exp2_f(d[0] + d[1]);
+                        v[e] = (REV ? j0 + e >= i : j0 + e <= i) ? w : 0.f;
                     }
                     O::template put4<C, NTP>(lp, i, j0 / 4, v);
                 }
             }
             lds_barrier();
-        }
 
-        frag zf[2][NCT];
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) zf[pr][ct] = O::template col<DZ>(lz, 32 * pr, col0 + 16 * ct, lane);
-
-        if constexpr (!LOCAL) {
             // Output tiles with a token in each lane's column: decayed state . x, then P z.
-            f32x4_t acc[4][NCT];
+            f32x4_t acc[4];
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] = zero4();
+            for (int tb = 0; tb < 4; ++tb) acc[tb] = zero4();
 #pragma unroll
             for (int k = 0; k < RT / 2; ++k) {
-                frag sf[NCT][NTS];
+                frag sf[NTS];
+                float s8[8];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    float s8[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s8[e] = S[2 * k][ct][e];
-                        s8[4 + e] = S[2 * k + 1][ct][e];
-                    }
-                    O::template split<NTS>(s8, sf[ct]);
+                for (int e = 0; e < 4; ++e) {
+                    s8[e] = S[2 * k][e];
+                    s8[4 + e] = S[2 * k + 1][e];
                 }
+                O::template split<NTS>(s8, sf);
 #pragma unroll
-                for (int tb = 0; tb < 4; ++tb) {
-                    const frag fx = O::template row<DX>(lx, 16 * tb, 32 * k, lane);
+                for (int t0b = 0; t0b < 4; t0b += SIDE) {
+                    frag fx[SIDE];
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
+                    for (int r = 0; r < SIDE; ++r) fx[r] = O::template row<DX>(lx, 16 * (t0b + r), 32 * k, lane);
 #pragma unroll
-                        for (int n = 0; n < NTS; ++n) acc[tb][ct] = O::mma(sf[ct][n], fx, acc[tb][ct]);
+                    for (int n = 0; n < NTS; ++n)
+#pragma unroll
+                        for (int r = 0; r < SIDE; ++r) acc[t0b + r] = O::mma(sf[n], fx[r], acc[t0b + r]);
                 }
             }
-            const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(min(p.T - t0, C)) * so);
+            const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(uniform(min(p.T - t0, C))) * so);
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
-                const float sc = sh_out[16 * tb + m];
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] *= sc;
+                acc[tb] *= sh_out[16 * tb + m];
 #pragma unroll
                 for (int pr = 0; pr < 2; ++pr) {
                     if (REV ? pr < tb / 2 : pr > tb / 2) continue;
 #pragma unroll
-                    for (int n = 0; n < NTP; ++n) {
-                        const frag fp = O::template row<C>(lp + n * O::template tile_bytes<C>(), 16 * tb, 32 * pr, lane);
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) acc[tb][ct] = O::mma(zf[pr][ct], fp, acc[tb][ct]);
-                    }
+                    for (int n = 0; n < NTP; ++n)
+                        acc[tb] = O::mma(zf[pr], O::template row<C>(lp + n * O::template tile_bytes<C>(), 16 * tb, 32 * pr, lane), acc[tb]);
                 }
-                const int t = 16 * tb + m;
-                if (t0 + C > end) {
+                const int t = 16 * tb + m, col = col0 + 4 * g;
+                if (t0 + C > end && t0 + t >= end) acc[tb] = zero4();
+                if (ES == 4 || p.out_f32) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tb]), bo, m * so + 4 * col, 16 * tb * so, 0);
+                } else {
+                    u16x4_t u;
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-                        if (t0 + t >= end) acc[tb][ct] = zero4();
-                }
-                float dot = 0.f;
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const int col = col0 + 16 * ct + 4 * g;
-                    if (ES == 4 || p.out_f32) {
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tb][ct]), bo, m * so + 4 * col, 16 * tb * so, 0);
-                    } else {
-                        u16x4_t u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16(acc[tb][ct][e]);
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, u), bo, m * so + 2 * col, 16 * tb * so, 0);
-                    }
-                    if constexpr (KEEP) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float w;
-                            if constexpr (ES == 2) w = bf16_to_f32(static_cast<uint16_t>(w4[tb][ct][e / 2] >> (16 * (e % 2))));
-                            else w = __uint_as_float(w4[tb][ct][e]);
-                            dot = fmaf(w, acc[tb][ct][e], dot);
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16(acc[tb][e]);
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, u), bo, m * so + 2 * col, 16 * tb * so, 0);
                 }
                 if constexpr (KEEP) {
+                    float dot = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float w;
+                        if constexpr (ES == 2) w = bf16_to_f32(static_cast<uint16_t>(w4[tb][e / 2] >> (16 * (e % 2))));
+                        else w = __uint_as_float(w4[tb][e]);
+                        dot = fmaf(w, acc[tb][e], dot);
+                    }
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
                     if (g == 0) sh_dot[wv * C + t] = dot;
@@ -309,49 +288,48 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
 
         // The state: decayed over the chunk, then y^T (decayed z).
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[rt][ct] *= carry;
+        for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
 #pragma unroll
         for (int pr = 0; pr < 2; ++pr) {
-            frag zs[NCT][NTU];
+            frag zs[NTU];
             const f32x4_t ulo = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 4 * g);
             const f32x4_t uhi = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 16 + 4 * g);
+            float z8[8];
+            O::floats(zf[pr], z8);
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                float z8[8];
-                O::floats(zf[pr][ct], z8);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z8[e] *= ulo[e];
-                    z8[4 + e] *= uhi[e];
-                }
-                O::template split<NTU>(z8, zs[ct]);
+            for (int e = 0; e < 4; ++e) {
+                z8[e] *= ulo[e];
+                z8[4 + e] *= uhi[e];
             }
+            O::template split<NTU>(z8, zs);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const frag fy = O::template col<DX>(ly, 32 * pr, 16 * rt, lane);
+            for (int r0 = 0; r0 < RT; r0 += SIDE) {
+                frag fy[SIDE];
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
+                for (int r = 0; r < SIDE; ++r) fy[r] = O::template col<DX>(ly, 32 * pr, 16 * (r0 + r), lane);
 #pragma unroll
-                    for (int n = NTU - 1; n >= 0; --n) S[rt][ct] = O::mma(fy, zs[ct][n], S[rt][ct]);
+                for (int n = NTU - 1; n >= 0; --n)
+#pragma unroll
+                    for (int r = 0; r < SIDE; ++r) S[r0 + r] = O::mma(fy[r], zs[n], S[r0 + r]);
             }
         }
         lds_barrier();
         if constexpr (KEEP) {
-            if (tid < C && t0 + tid < p.T)
-                p.dots[(bT + t0 + tid) * p.H + h] = (sh_dot[tid] + sh_dot[C + tid]) + (sh_dot[2 * C + tid] + sh_dot[3 * C + tid]);
+            if (tid < C && t0 + tid < p.T) {
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) x += sh_dot[w * C + tid];
+                p.dots[(bT + t0 + tid) * p.H + h] = x;
+            }
         }
     }
 
     if constexpr (KEEP && !REV) {
         if (seg == p.nseg - 1 && p.nchunks > 0) {
             f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + groups - 1) * DUMP) +
-                          wv * (RT * NCT * 64) + lane;
+                          wv * (RT * 64) + lane;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) at[(rt * NCT + ct) * 64] = S[rt][ct];
+            for (int rt = 0; rt < RT; ++rt) at[rt * 64] = S[rt];
         }
     }
     float *st = nullptr;
@@ -365,9 +343,7 @@ __global__ __launch_bounds__(THREADS, sizeof(T) == 2 ? 2 : 1) void pass_kernel(P
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) st[(16 * rt + 4 * g + i) * DZ + col0 + 16 * ct + m] = S[rt][ct][i];
+            for (int i = 0; i < 4; ++i) st[(16 * rt + 4 * g + i) * DZ + col0 + m] = S[rt][i];
     }
 }
 
@@ -393,7 +369,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float *s0, const float 
 // In 64 bits: the terms cancel where the decay is strong.
 __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const float *cols, const float *edges,
                                                         const int *lens, float *dla, double *part, int T, int H,
-                                                        int groups) {
+                                                        int groups, int parts) {
     __shared__ double sh[ANCHOR];
     const int grp = blockIdx.x % groups, bh = blockIdx.x / groups, b = bh / H, h = bh % H;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -405,8 +381,8 @@ __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const
     if (lane == 63) sh[wv] = x;
     __syncthreads();
     for (int w = 0; w < wv; ++w) x += sh[w];
-    const float *e = edges + (static_cast<size_t>(bh) * groups + grp) * 4;
-    x += (static_cast<double>(e[0]) + e[1]) + (static_cast<double>(e[2]) + e[3]);
+    const float *e = edges + (static_cast<size_t>(bh) * groups + grp) * parts;
+    for (int i = 0; i < parts; ++i) x += e[i];
     if (t >= end) x = 0.0;
     if (dla) {
         if (t < T) dla[at] = static_cast<float>(x);
@@ -448,7 +424,7 @@ hipError_t launch_pass(const PassArgs &p, hipStream_t stream) {
     const hipError_t err = allow_lds<pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>>(bytes);
     if (err != hipSuccess) return err;
     const unsigned grid = static_cast<unsigned>(p.B) * p.H * p.nseg;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(THREADS), bytes, stream, p);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(4 * DZ), bytes, stream, p);
     return hipGetLastError();
 }
 
@@ -542,7 +518,7 @@ hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g
     const size_t bh = BH, tok = bh * c.T, st = static_cast<size_t>(c.dk) * c.dv;
     Carver w{static_cast<unsigned char *>(workspace)};
     float *rows = w.take<float>(tok), *cols = w.take<float>(tok);
-    float *anchors = w.take<float>(bh * groups * st), *edges = w.take<float>(bh * groups * 4);
+    float *anchors = w.take<float>(bh * groups * st), *edges = w.take<float>(bh * groups * (c.dk / 16));
     double *part = w.take<double>(bh * groups);
     const float *s_start = c.s0, *a_start = g.ds_out;
     hipError_t err;
@@ -613,7 +589,7 @@ hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g
     if (err != hipSuccess) return err;
     if (c.T > 0) {
         hipLaunchKernelGGL(dla_kernel, dim3(static_cast<unsigned>(groups) * BH), dim3(ANCHOR * C), 0, stream, rows, cols, edges, c.lens,
-                           c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups);
+                           c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups, c.dk / 16);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }

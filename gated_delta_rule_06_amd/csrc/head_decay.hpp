@@ -21,7 +21,6 @@
 namespace muir {
 namespace hd {
 
-constexpr int THREADS = 256;  // four wavefronts, each with a quarter of the state's columns
 
 // A fragment holds 16 rows x 32 contraction indices of an operand: lane l has row l % 16, and its
 // element j is contraction index 16 (j / 4) + 4 (l / 16) + j % 4. In that order two stacked 16x16
@@ -31,20 +30,22 @@ template <typename T> struct Op;
 
 template <> struct Op<bf16_t> {
     using frag = bf16x8_t;
-    template <int D> static constexpr int tile_bytes() { return C * D * 2; }
+    template <int D> static constexpr int tile_bytes() { return C * D * 2 + C; }
     // Byte offset of element (r, 4 c) of a tile [64][D]. Tiles have no padding; the 8-byte pieces of a row are permuted
     // by its number so that both reads below, 32 lanes at a time, take every bank once: `row` takes piece c of 16 rows and
     // c + 1 (or + 2, + 3), `col` takes four pieces of eight rows. Padded rows serve one of the two: with 272 bytes a row the
     // transposing reads met in pairs, 2100 of 5200 LDS cycles a chunk. The permutation keeps 16-byte pieces whole.
+    // 16 bytes between blocks of 16 rows keep the compiler from reading two blocks with one instruction whose two
+    // addresses lie in the same banks (1460 cycles a chunk).
     template <int D> static __device__ __forceinline__ int at(int r, int c) {
         const int f = D == 128 ? ((r & 7) << 2) | ((r >> 2) & 2) : ((r & 6) << 1) | ((r >> 2) & 2);
-        return r * (D * 2) + 8 * (c ^ f);
+        return r * (D * 2) + (r >> 4) * 16 + 8 * (c ^ f);
     }
     // r0 and k0 are constants, so what is left at run time is a handful of addresses per tile width.
     template <int D> static __device__ __forceinline__ frag row(const unsigned char *t, int r0, int k0, int lane) {
         const int base = at<D>(lane & 15, lane >> 4);
-        const u16x4_t a = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0)) + r0 * (D * 2)));
-        const u16x4_t b = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0 + 32)) + r0 * (D * 2)));
+        const u16x4_t a = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0)) + r0 * (D * 2 + 1)));
+        const u16x4_t b = *reinterpret_cast<const u16x4_t *>(t + ((base ^ (2 * k0 + 32)) + r0 * (D * 2 + 1)));
         return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     // Rows of the operand are columns c0.. of the tile. The transposing read gives lane m of a group of 16
@@ -52,8 +53,8 @@ template <> struct Op<bf16_t> {
     template <int D> static __device__ __forceinline__ frag col(unsigned char *t, int k0, int c0, int lane) {
         typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
         const int m = lane & 15, g = lane >> 4, base = at<D>(4 * g + (m >> 2), m & 3) ^ (2 * c0);
-        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + k0 * (D * 2))));
-        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + (k0 + 16) * (D * 2))));
+        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + k0 * (D * 2 + 1))));
+        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (base + (k0 + 16) * (D * 2 + 1))));
         return __builtin_bit_cast(frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     // 16 bytes of row r, column piece c (of 8 elements).
@@ -65,17 +66,24 @@ template <> struct Op<bf16_t> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = bf16_to_f32(u[j]);
     }
+    // Two values rounded to bf16 in one register, and, where more terms follow, what the rounding left.
+    template <bool REST> static __device__ __forceinline__ uint32_t term(float &x, float &y) {
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        const uint32_t p = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{x, y}, bf16x2_t));
+        if constexpr (REST) {
+            x -= __uint_as_float(p << 16);
+            y -= __uint_as_float(p & 0xffff0000u);
+        }
+        return p;
+    }
     // x as the sum of N bf16 fragments: each rounds what the ones before left (8 bits each, so three
     // hold a float32 to its last bit or two).
     template <int N> static __device__ __forceinline__ void split(float (&x)[8], frag (&f)[N]) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            u16x8_t u;
+            u32x4_t u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u[j] = f32_to_bf16(x[j]);
-                if (n + 1 < N) x[j] -= bf16_to_f32(u[j]);
-            }
+            for (int j = 0; j < 4; ++j) u[j] = n + 1 < N ? term<true>(x[2 * j], x[2 * j + 1]) : term<false>(x[2 * j], x[2 * j + 1]);
             f[n] = __builtin_bit_cast(frag, u);
         }
     }
@@ -86,13 +94,12 @@ template <> struct Op<bf16_t> {
     template <int D, int N> static __device__ __forceinline__ void put4(unsigned char *t, int r, int c, f32x4_t v) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            u16x4_t u;
+            float w[4] = {v[0], v[1], v[2], v[3]};
+            u32x2_t u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u[i] = f32_to_bf16(v[i]);
-                if (n + 1 < N) v[i] -= bf16_to_f32(u[i]);
-            }
-            *reinterpret_cast<u16x4_t *>(t + n * tile_bytes<D>() + at<D>(r, c)) = u;
+            for (int i = 0; i < 2; ++i) u[i] = n + 1 < N ? term<true>(w[2 * i], w[2 * i + 1]) : term<false>(w[2 * i], w[2 * i + 1]);
+            v = f32x4_t{w[0], w[1], w[2], w[3]};
+            *reinterpret_cast<u32x2_t *>(t + n * tile_bytes<D>() + at<D>(r, c)) = u;
         }
     }
 };
@@ -157,7 +164,7 @@ template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_or_zero(doub
 
 // Inclusive sum over the lanes up to this one (shifts by 1, 2, 4 and 8 inside rows of 16 lanes, then the last lane of a row
 // to the next one or two). In 64 bits: the sums reach -12800 (64 zeros) while the differences taken of them have to be
-// exact to 2^-24.
+// good to 2^-24.
 __device__ __forceinline__ double scan64(double x) {
     x += dpp_or_zero<0x111, 0xf>(x);
     x += dpp_or_zero<0x112, 0xf>(x);
