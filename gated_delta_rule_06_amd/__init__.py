@@ -12,6 +12,7 @@ itself must be built (``python -m gated_delta_rule_06_amd._build``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -629,6 +630,7 @@ def _head_decay_inputs(q, k, v, a, s0, lens):
     return (B, T, H, Hk, dk, dv), int(per_token), code, i
 
 
+@functools.lru_cache(maxsize=256)
 def chunk_fwd_head_decay_workspace_size(B: int, T: int, H: int, Hk: int, dk: int, dv: int,
                                         dtype_code: int) -> int:
     return int(lib().muir_chunk_fwd_head_decay_workspace_size(B, T, H, Hk, dk, dv, dtype_code))
@@ -659,6 +661,7 @@ def chunk_fwd_head_decay(q, k, v, a, s0=None, *, lens=None, o=None, s_out=None,
     return o, s_out
 
 
+@functools.lru_cache(maxsize=256)
 def chunk_bwd_head_decay_workspace_size(B: int, T: int, H: int, Hk: int, dk: int, dv: int,
                                         dtype_code: int) -> int:
     return int(lib().muir_chunk_bwd_head_decay_workspace_size(B, T, H, Hk, dk, dv, dtype_code))
@@ -769,6 +772,7 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None):
     return y, x if residual is None else h, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def rms_norm_bwd_workspace_size(rows: int, D: int) -> int:
     return int(lib().muir_rms_norm_bwd_workspace_size(rows, D))
 

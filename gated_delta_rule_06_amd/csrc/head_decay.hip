@@ -83,14 +83,18 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
     float *const sh_dot = sh_upd + C;                                 // [NW][C]
 
-    const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tid = threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = tid & 63, m = lane & 15, g = lane >> 4;
     // Quotients and clamped values are made in vector registers; they are the same in every lane, and a buffer's
     // description has to be known to be.
     auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
-    const int bh = uniform(blockIdx.x / p.nseg), seg = blockIdx.x - bh * p.nseg, b = uniform(bh / p.H), h = bh - b * p.H;
-    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks), steps = c1 - c0;
+    // LOCAL: the last segment in the order of the walk is not needed.
+    const int per = LOCAL ? p.nseg - 1 : p.nseg;
+    const int bh = uniform(blockIdx.x / per), seg = blockIdx.x - bh * per + (LOCAL && REV ? 1 : 0), b = uniform(bh / p.H), h = bh - b * p.H;
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
     const int end = uniform(p.lens ? min(max(p.lens[b], 0), p.T) : p.T);
+    const int live = end / C + (end % C != 0), steps = max(min(c1, live) - c0, 0);  // chunks that hold a token
     const int col0 = wv * 16;
     const size_t bT = static_cast<size_t>(b) * p.T;
     // Row strides in bytes, and the head's first row in each tensor.
@@ -125,52 +129,76 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     const float a_h = p.a_fixed && p.nchunks > 0 ? p.a[h] : 1.f;
     double seg_log = 0.0;
 
-    Tile<T, DX, THREADS> rx, ry;
-    Tile<T, DZ, THREADS> rz;
-    float ra = 1.f;
+    struct Chunk {
+        Tile<T, DX, THREADS> x, y;
+        Tile<T, DZ, THREADS> z;
+        float a;
+    };
+    Chunk f;
     // The wavefronts take turns at a chunk's decays.
     auto fetch = [&](int it) {
-        const int t0 = (REV ? c1 - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
-        if constexpr (!LOCAL) rx.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
-        ry.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
-        rz.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
-        if (wv == it % NW) ra = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+        const int t0 = (REV ? c0 + steps - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
+        if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
+        f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
+        f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
+        if (wv == it % NW) f.a = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+    };
+    // KEEP: <S, A> at the end of every ANCHOR-th chunk. The pass in order leaves S there before it takes the next chunk,
+    // the reversed one takes the product.
+    auto anchor = [&](int c) {
+        if (REV ? (c + 1) % ANCHOR == 0 || c + 1 == p.nchunks : c % ANCHOR == 0 && c > 0) {
+            const int entry = REV ? c / ANCHOR : c / ANCHOR - 1;
+            f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + entry) * DUMP) +
+                          wv * (RT * 64) + lane;
+            f32x4_t sum = zero4();
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (REV) sum += S[rt] * at[rt * 64];
+                else at[rt * 64] = S[rt];
+            }
+            if constexpr (REV) {
+                const float e = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                if (lane == 0) p.edges[(static_cast<size_t>(bh) * groups + entry) * NW + wv] = e;
+            }
+        }
+    };
+    // Chunks behind the sequence's end leave the state as it is, and their outputs are zeros.
+    auto behind = [&] {
+        if constexpr (LOCAL) return;
+        for (int i = max(c0, live); i < c1; ++i) {
+            const int c = REV ? c1 - 1 - (i - max(c0, live)) : i, t0 = c * C;
+            if constexpr (KEEP) anchor(c);
+            const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(uniform(min(p.T - t0, C))) * so);
+            const int off = m * so + (col0 + 4 * g) * (p.out_f32 ? 4 : ES);
+            for (int tb = 0; tb < 4; ++tb) {
+                if (ES == 4 || p.out_f32) __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{0, 0, 0, 0}, bo, off, 16 * tb * so, 0);
+                else __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{0, 0}, bo, off, 16 * tb * so, 0);
+            }
+            if constexpr (KEEP) {
+                if (tid < C && t0 + tid < p.T) p.dots[(bT + t0 + tid) * p.H + h] = 0.f;
+            }
+        }
     };
     if (steps > 0) fetch(0);
+    if constexpr (REV) behind();
 
     for (int it = 0; it < steps; ++it) {
-        const int c = REV ? c1 - 1 - it : c0 + it, t0 = c * C;
+        const int c = REV ? c0 + steps - 1 - it : c0 + it, t0 = c * C;
         // Addresses that follow from the lane are made anew in each chunk: kept over the loop they would take some forty
         // registers that the state and the tiles need.
         asm volatile("" : "+v"(lane), "+v"(m), "+v"(g));
-        if constexpr (!LOCAL) rx.put(lx, tid);
-        ry.put(ly, tid);
-        rz.put(lz, tid);
+        if constexpr (KEEP) asm volatile("" : "+v"(tid));
+        if constexpr (!LOCAL) f.x.put(lx, tid);
+        f.y.put(ly, tid);
+        f.z.put(lz, tid);
         if (wv == it % NW) {
-            const double Lt = scan64(log2_decay(ra));
+            const double Lt = scan64(log2_decay(f.a));
             const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(lane_value(Lt, 63) - Lt));
             sh_L[lane] = f32x2_t{static_cast<float>(Lt), static_cast<float>(Lt - static_cast<float>(Lt))};
             sh_out[lane] = REV ? to_end : to_start;
             sh_upd[lane] = REV ? to_start : to_end;
         }
-        if constexpr (KEEP) {
-            // <S, A> at the end of every ANCHOR-th chunk: the pass in order leaves S, the reversed one takes its product.
-            if (REV ? (c + 1) % ANCHOR == 0 || c + 1 == p.nchunks : c % ANCHOR == 0 && c > 0) {
-                const int entry = REV ? c / ANCHOR : c / ANCHOR - 1;
-                f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + entry) * DUMP) +
-                              wv * (RT * 64) + lane;
-                f32x4_t sum = zero4();
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if constexpr (REV) sum += S[rt] * at[rt * 64];
-                    else at[rt * 64] = S[rt];
-                }
-                if constexpr (REV) {
-                    const float e = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-                    if (lane == 0) p.edges[(static_cast<size_t>(bh) * groups + entry) * NW + wv] = e;
-                }
-            }
-        }
+        if constexpr (KEEP) anchor(c);
         // KEEP: the rows that this chunk's outputs are multiplied with, in the accumulators' layout.
         using pack4_t = std::conditional_t<ES == 2, u32x2_t, u32x4_t>;
         pack4_t w4[KEEP ? 4 : 1];
@@ -324,6 +352,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
         }
     }
 
+    if constexpr (!REV) behind();
     if constexpr (KEEP && !REV) {
         if (seg == p.nseg - 1 && p.nchunks > 0) {
             f32x4_t *at = reinterpret_cast<f32x4_t *>(p.anchors + (static_cast<size_t>(bh) * groups + groups - 1) * DUMP) +
@@ -359,9 +388,10 @@ __global__ __launch_bounds__(256) void join_kernel(const float *s0, const float 
 #pragma unroll 4
     for (int s = 0; s < nseg; ++s) {
         const int k = REV ? nseg - 1 - s : s;
-        const f32x4_t own = at[static_cast<size_t>(k) * n4];
+        f32x4_t own = zero4();
+        if (s + 1 < nseg) own = at[static_cast<size_t>(k) * n4];  // the last one's is not made: no segment starts behind it
         at[static_cast<size_t>(k) * n4] = x;
-        x = x * d[k] + own;
+        if (s + 1 < nseg) x = x * d[k] + own;
     }
 }
 
@@ -423,7 +453,7 @@ hipError_t launch_pass(const PassArgs &p, hipStream_t stream) {
     constexpr int bytes = PassLds<T, DX, DZ, LOCAL, NTP>::BYTES;
     const hipError_t err = allow_lds<pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>>(bytes);
     if (err != hipSuccess) return err;
-    const unsigned grid = static_cast<unsigned>(p.B) * p.H * p.nseg;
+    const unsigned grid = static_cast<unsigned>(p.B) * p.H * (LOCAL ? p.nseg - 1 : p.nseg);
     hipLaunchKernelGGL(kern, dim3(grid), dim3(4 * DZ), bytes, stream, p);
     return hipGetLastError();
 }

@@ -5,11 +5,11 @@
 namespace muir {
 
 int head_decay_segments(int B, int T, int H, bool bf16) {
-    // As many workgroups as run at once (two to a compute unit in bf16, one in float32), of at least four
+    // As many workgroups as run at once (two to a compute unit in bf16, one in float32), of at least two
     // chunks each: a segment costs a second reading of its keys and values and a state written and read.
     const long long heads = static_cast<long long>(B) * H, room = bf16 ? 512 : 256;
     const int n = hd::chunks_of(T);
-    const int want = static_cast<int>(std::min<long long>(room / std::min(heads, room), n / 4));
+    const int want = static_cast<int>(std::min<long long>(room / std::min(heads, room), n / 2));
     if (want <= 1) return 1;
     const int per = (n + want - 1) / want;
     return (n + per - 1) / per;
