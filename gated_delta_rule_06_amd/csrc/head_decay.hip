@@ -136,12 +136,16 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     };
     Chunk f;
     // The wavefronts take turns at a chunk's decays.
-    auto fetch = [&](int it) {
+    auto fetch = [&](int it, bool first, bool second) {
         const int t0 = (REV ? c0 + steps - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
-        if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
-        f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
-        f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
-        if (wv == it % NW) f.a = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+        if (first) {
+            if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
+            if (wv == it % NW) f.a = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
+        }
+        if (second) {
+            f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
+            f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
+        }
     };
     // KEEP: <S, A> at the end of every ANCHOR-th chunk. The pass in order leaves S there before it takes the next chunk,
     // the reversed one takes the product.
@@ -153,8 +157,12 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             f32x4_t sum = zero4();
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                if constexpr (REV) sum += S[rt] * at[rt * 64];
-                else at[rt * 64] = S[rt];
+                if constexpr (REV) {
+                    sum += S[rt] * at[rt * 64];
+                    if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // four loads at a time: registers
+                } else {
+                    at[rt * 64] = S[rt];
+                }
             }
             if constexpr (REV) {
                 const float e = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             }
         }
     };
-    if (steps > 0) fetch(0);
+    if (steps > 0) fetch(0, true, true);
     if constexpr (REV) behind();
 
     for (int it = 0; it < steps; ++it) {
@@ -199,19 +207,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             sh_upd[lane] = REV ? to_start : to_end;
         }
         if constexpr (KEEP) anchor(c);
-        // KEEP: the rows that this chunk's outputs are multiplied with, in the accumulators' layout.
-        using pack4_t = std::conditional_t<ES == 2, u32x2_t, u32x4_t>;
-        pack4_t w4[KEEP ? 4 : 1];
-        if constexpr (KEEP) {
-            const rsrc_t bw = make_rsrc(gw + static_cast<size_t>(t0) * sw, static_cast<unsigned>(uniform(min(max(end - t0, 0), C))) * sw);
-            const int off = m * sw + (col0 + 4 * g) * ES;
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                if constexpr (ES == 2) w4[tb] = __builtin_amdgcn_raw_buffer_load_b64(bw, off, 16 * tb * sw, 0);
-                else w4[tb] = __builtin_amdgcn_raw_buffer_load_b128(bw, off, 16 * tb * sw, 0);
-            }
-        }
-        if (it + 1 < steps) fetch(it + 1);
+        if (it + 1 < steps) fetch(it + 1, true, !KEEP);
         lds_barrier();
         const f32x2_t Lc = sh_L[C - 1];
         const float carry = exp2_f(Lc[0] + Lc[1]);
@@ -277,6 +273,19 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
                         for (int r = 0; r < SIDE; ++r) acc[t0b + r] = O::mma(sf[n], fx[r], acc[t0b + r]);
                 }
             }
+            // KEEP: the rows that this chunk's outputs are multiplied with, in the accumulators' layout. Fetched only here: over
+            // the products with the state there is no register left for them.
+            using pack4_t = std::conditional_t<ES == 2, u32x2_t, u32x4_t>;
+            pack4_t w4[KEEP ? 4 : 1];
+            if constexpr (KEEP) {
+                const rsrc_t bw = make_rsrc(gw + static_cast<size_t>(t0) * sw, static_cast<unsigned>(uniform(min(max(end - t0, 0), C))) * sw);
+                const int off = m * sw + (col0 + 4 * g) * ES;
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb) {
+                    if constexpr (ES == 2) w4[tb] = __builtin_amdgcn_raw_buffer_load_b64(bw, off, 16 * tb * sw, 0);
+                    else w4[tb] = __builtin_amdgcn_raw_buffer_load_b128(bw, off, 16 * tb * sw, 0);
+                }
+            }
             const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(uniform(min(p.T - t0, C))) * so);
 #pragma unroll
             for (int tb = 0; tb < 4; ++tb) {
@@ -314,6 +323,9 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             }
         }
 
+        // KEEP has no registers for a whole chunk on its way while it multiplies with the state: y and z follow here. (All of
+        // it early, a part kept in memory: 211 and 232 us at B8 T4096 H16 d128; all of it here: 216 and 229; this: 206 and 216.)
+        if (KEEP && it + 1 < steps) fetch(it + 1, false, true);
         // The state: decayed over the chunk, then y^T (decayed z).
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
