@@ -1,8 +1,8 @@
 // Linear attention with one decay per head: chunked forward and backward (head_decay.hpp has the
 // formulas). Four kernels:
-//   pass_kernel, LOCAL      each segment's own contribution to the state at its end, and its decay
+//   pass, LOCAL             each segment's own contribution to the state at its end, and its decay
 //   join_kernel             the state at each segment's start from those, in order
-//   pass_kernel             one walk over a segment's chunks: outputs (or one gradient) with the state in registers
+//   pass                    one walk over a segment's chunks: outputs (or one gradient) with the state in registers
 //   dla_kernel, *_sum       the decay's gradient from the row sums of two passes; sums over shared heads
 // Where B * H workgroups fill the card there is one segment per head and the pass is the only launch of a forward.
 #include <algorithm>
@@ -67,8 +67,17 @@ template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
 // Rounding, for bf16 inputs: the products x.y are exact in float32; D (x.y) and the state go into the second
 // products as NTP and NTS bf16 terms, the decayed z into the state's update as three, so states, and the
 // row sums that the decay's gradient is made of, keep float32 accuracy.
-template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, int NTS, int NTU>
-__global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pass_kernel(PassArgs p) {
+template <typename T_, int DX_, int DZ_, bool REV_, bool LOCAL_, bool KEEP_, int NTP_, int NTS_, int NTU_> struct Pass {
+    using T = T_;
+    static constexpr int DX = DX_, DZ = DZ_, NTP = NTP_, NTS = NTS_, NTU = NTU_;
+    static constexpr bool REV = REV_, LOCAL = LOCAL_, KEEP = KEEP_;
+    static constexpr int BYTES = PassLds<T, DX, DZ, LOCAL, NTP>::BYTES;
+};
+
+template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, int block) {
+    using T = typename K::T;
+    constexpr int DX = K::DX, DZ = K::DZ, NTP = K::NTP, NTS = K::NTS, NTU = K::NTU;
+    constexpr bool REV = K::REV, LOCAL = K::LOCAL, KEEP = K::KEEP;
     using O = Op<T>;
     using L = PassLds<T, DX, DZ, LOCAL, NTP>;
     using frag = typename O::frag;
@@ -91,7 +100,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
     // LOCAL: the last segment in the order of the walk is not needed.
     const int per = LOCAL ? p.nseg - 1 : p.nseg;
-    const int bh = uniform(blockIdx.x / per), seg = blockIdx.x - bh * per + (LOCAL && REV ? 1 : 0), b = uniform(bh / p.H), h = bh - b * p.H;
+    const int bh = uniform(block / per), seg = block - bh * per + (LOCAL && REV ? 1 : 0), b = uniform(bh / p.H), h = bh - b * p.H;
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
     const int end = uniform(p.lens ? min(max(p.lens[b], 0), p.T) : p.T);
     const int live = end / C + (end % C != 0), steps = max(min(c1, live) - c0, 0);  // chunks that hold a token
@@ -136,16 +145,12 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     };
     Chunk f;
     // The wavefronts take turns at a chunk's decays.
-    auto fetch = [&](int it, bool first, bool second) {
+    auto fetch = [&](int it) {
         const int t0 = (REV ? c0 + steps - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
-        if (first) {
-            if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
-            if (wv == it % NW) f.a = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
-        }
-        if (second) {
-            f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
-            f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
-        }
+        if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
+        f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
+        f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
+        if (wv == it % NW) f.a = lane >= rows ? 1.f : p.a_fixed ? a_h : p.a[(bT + t0 + lane) * p.H + h];
     };
     // KEEP: <S, A> at the end of every ANCHOR-th chunk. The pass in order leaves S there before it takes the next chunk,
     // the reversed one takes the product.
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             }
         }
     };
-    if (steps > 0) fetch(0, true, true);
+    if (steps > 0) fetch(0);
     if constexpr (REV) behind();
 
     for (int it = 0; it < steps; ++it) {
@@ -207,7 +212,7 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             sh_upd[lane] = REV ? to_start : to_end;
         }
         if constexpr (KEEP) anchor(c);
-        if (it + 1 < steps) fetch(it + 1, true, !KEEP);
+        if (it + 1 < steps) fetch(it + 1);
         lds_barrier();
         const f32x2_t Lc = sh_L[C - 1];
         const float carry = exp2_f(Lc[0] + Lc[1]);
@@ -231,6 +236,8 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
                     const frag fx = O::template row<DX>(lx, 16 * ib, k0, lane);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) acc[u] = O::mma(O::template row<DX>(ly, 32 * pr + 16 * u, k0, lane), fx, acc[u]);
+                    // Not all operands at once: next to the state and the chunk on its way there are not the registers.
+                    if (ES == 2 && k0 % 64 == 32) __builtin_amdgcn_sched_barrier(0);
                 }
                 const f32x2_t Li = sh_L[i];
 #pragma unroll
@@ -323,9 +330,6 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
             }
         }
 
-        // KEEP has no registers for a whole chunk on its way while it multiplies with the state: y and z follow here. (All of
-        // it early, a part kept in memory: 211 and 232 us at B8 T4096 H16 d128; all of it here: 216 and 229; this: 206 and 216.)
-        if (KEEP && it + 1 < steps) fetch(it + 1, false, true);
         // The state: decayed over the chunk, then y^T (decayed z).
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
@@ -388,18 +392,42 @@ __global__ __launch_bounds__(4 * DZ, DZ / 64 * (sizeof(T) == 2 ? 2 : 1)) void pa
     }
 }
 
+// bf16: two workgroups of eight (or four of four) wavefronts to a compute unit.
+template <typename K> constexpr int pass_waves() { return K::DZ / 64 * (sizeof(typename K::T) == 2 ? 2 : 1); }
+
+template <typename K>
+__global__ __launch_bounds__(4 * K::DZ, pass_waves<K>()) void pass_kernel(PassArgs p) {
+    pass<K>(p, blockIdx.x);
+}
+
+// Two passes over the same segments in one launch, `n` workgroups each. Workgroups go to the eight dies in turn: the two
+// of one segment are eight apart, so the second finds in its die's cache what the first has read.
+template <typename K, typename M>
+__global__ __launch_bounds__(4 * K::DZ, pass_waves<K>()) void pair_kernel(PassArgs p, PassArgs q, int n) {
+    const int unit = (blockIdx.x >> 4 << 3) | (blockIdx.x & 7);
+    if (unit >= n) return;
+    if (blockIdx.x & 8) pass<M>(q, unit);
+    else pass<K>(p, unit);
+}
+
 // The state at each segment's start (reversed: end), in place of the segments' own contributions:
 // x <- s0 (or zeros); segment by segment: start = x, x <- dec x + contribution.
-template <bool REV>
-__global__ __launch_bounds__(256) void join_kernel(const float *s0, const float *dec, float *seg, int nseg, int n4) {
+struct JoinArgs {
+    const float *s0;
+    float *seg;
+    const float *dec;
+    bool rev;
+};
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs first, JoinArgs second, int nseg, int n4) {
+    const JoinArgs p = blockIdx.y ? second : first;
     const int blocks = (n4 + 255) / 256, bh = blockIdx.x / blocks, i = blockIdx.x % blocks * 256 + threadIdx.x;
     if (i >= n4) return;
-    f32x4_t x = s0 ? reinterpret_cast<const f32x4_t *>(s0)[static_cast<size_t>(bh) * n4 + i] : zero4();
-    f32x4_t *at = reinterpret_cast<f32x4_t *>(seg) + static_cast<size_t>(bh) * nseg * n4 + i;
-    const float *d = dec + static_cast<size_t>(bh) * nseg;
+    f32x4_t x = p.s0 ? reinterpret_cast<const f32x4_t *>(p.s0)[static_cast<size_t>(bh) * n4 + i] : zero4();
+    f32x4_t *at = reinterpret_cast<f32x4_t *>(p.seg) + static_cast<size_t>(bh) * nseg * n4 + i;
+    const float *d = p.dec + static_cast<size_t>(bh) * nseg;
 #pragma unroll 4
     for (int s = 0; s < nseg; ++s) {
-        const int k = REV ? nseg - 1 - s : s;
+        const int k = p.rev ? nseg - 1 - s : s;
         f32x4_t own = zero4();
         if (s + 1 < nseg) own = at[static_cast<size_t>(k) * n4];  // the last one's is not made: no segment starts behind it
         at[static_cast<size_t>(k) * n4] = x;
@@ -459,47 +487,46 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float *part, T *out
     store4(out + 4 * i, x);
 }
 
-template <typename T, int DX, int DZ, bool REV, bool LOCAL, bool KEEP, int NTP, int NTS, int NTU>
-hipError_t launch_pass(const PassArgs &p, hipStream_t stream) {
-    auto kern = pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>;
-    constexpr int bytes = PassLds<T, DX, DZ, LOCAL, NTP>::BYTES;
-    const hipError_t err = allow_lds<pass_kernel<T, DX, DZ, REV, LOCAL, KEEP, NTP, NTS, NTU>>(bytes);
+// The passes, by what their results need of each operand. P goes in as two terms (forward, dv) so that its rounding, which one token's
+// whole output shares where few tokens precede it, does not show; the state as one there: its roundings average out.
+template <typename T, int DK, int DV> struct Kinds {
+    static constexpr int N2 = sizeof(T) == 2 ? 2 : 1, N3 = sizeof(T) == 2 ? 3 : 1;
+    using Forward = Pass<T, DK, DV, false, false, false, N2, 1, N3>;
+    using LocalFwd = Pass<T, DK, DV, false, true, false, 1, 1, N3>;
+    using LocalRev = Pass<T, DK, DV, true, true, false, 1, 1, N3>;
+    using Dq = Pass<T, DV, DK, false, false, true, N3, N3, N3>;
+    using Dk = Pass<T, DV, DK, true, false, true, N3, N3, N3>;
+    using Dv = Pass<T, DK, DV, true, false, false, N2, 1, N3>;
+};
+
+template <typename K> unsigned pass_blocks(const PassArgs &p) {
+    return static_cast<unsigned>(p.B) * p.H * (K::LOCAL ? p.nseg - 1 : p.nseg);
+}
+
+template <typename K> hipError_t launch_pass(const PassArgs &p, hipStream_t s) {
+    const hipError_t err = allow_lds<pass_kernel<K>>(K::BYTES);
     if (err != hipSuccess) return err;
-    const unsigned grid = static_cast<unsigned>(p.B) * p.H * (LOCAL ? p.nseg - 1 : p.nseg);
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(4 * DZ), bytes, stream, p);
+    hipLaunchKernelGGL(pass_kernel<K>, dim3(pass_blocks<K>(p)), dim3(4 * K::DZ), K::BYTES, s, p);
     return hipGetLastError();
 }
 
-// The kinds of pass: terms of each operand by what its results need.
-enum class Kind { Forward, LocalFwd, LocalRev, Dq, Dk, Dv };
-
-template <typename T, int DX, int DZ> hipError_t launch_kind(Kind kind, const PassArgs &p, hipStream_t s) {
-    constexpr bool BF = sizeof(T) == 2;
-    constexpr int N3 = BF ? 3 : 1;
-    switch (kind) {
-        case Kind::Forward: return launch_pass<T, DX, DZ, false, false, false, 1, 1, N3>(p, s);
-        case Kind::LocalFwd: return launch_pass<T, DX, DZ, false, true, false, 1, 1, N3>(p, s);
-        case Kind::LocalRev: return launch_pass<T, DX, DZ, true, true, false, 1, 1, N3>(p, s);
-        case Kind::Dq: return launch_pass<T, DX, DZ, false, false, true, N3, N3, N3>(p, s);
-        case Kind::Dk: return launch_pass<T, DX, DZ, true, false, true, N3, N3, N3>(p, s);
-        case Kind::Dv: return launch_pass<T, DX, DZ, true, false, false, 1, 1, N3>(p, s);
+template <typename K, typename M> hipError_t launch_pair(const PassArgs &p, const PassArgs &q, hipStream_t s) {
+    if constexpr (K::DZ != M::DZ) {  // another number of threads
+        const hipError_t err = launch_pass<K>(p, s);
+        return err != hipSuccess ? err : launch_pass<M>(q, s);
+    } else {
+        constexpr int bytes = K::BYTES > M::BYTES ? K::BYTES : M::BYTES;
+        const hipError_t err = allow_lds<pair_kernel<K, M>>(bytes);
+        if (err != hipSuccess) return err;
+        const unsigned n = pass_blocks<K>(p);
+        hipLaunchKernelGGL((pair_kernel<K, M>), dim3((n + 7) / 8 * 16), dim3(4 * K::DZ), bytes, s, p, q, static_cast<int>(n));
+        return hipGetLastError();
     }
-    return hipErrorInvalidValue;
 }
 
-hipError_t launch_any(Kind kind, bool bf16, int dx, int dz, const PassArgs &p, hipStream_t s) {
-#define MUIR_HD(X, Z) \
-    if (dx == X && dz == Z) return bf16 ? launch_kind<bf16_t, X, Z>(kind, p, s) : launch_kind<float, X, Z>(kind, p, s);
-    MUIR_HD(64, 64) MUIR_HD(64, 128) MUIR_HD(128, 64) MUIR_HD(128, 128)
-#undef MUIR_HD
-    return hipErrorInvalidValue;
-}
-
-hipError_t launch_join(bool rev, const float *s0, const float *dec, float *seg, int bh, int nseg, int n,
-                       hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256) * bh);
-    if (rev) hipLaunchKernelGGL(join_kernel<true>, grid, dim3(256), 0, s, s0, dec, seg, nseg, n / 4);
-    else hipLaunchKernelGGL(join_kernel<false>, grid, dim3(256), 0, s, s0, dec, seg, nseg, n / 4);
+hipError_t launch_join(const JoinArgs &first, const JoinArgs *second, int bh, int nseg, int n, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256) * bh, second ? 2 : 1);
+    hipLaunchKernelGGL(join_kernel, grid, dim3(256), 0, s, first, second ? *second : first, nseg, n / 4);
     return hipGetLastError();
 }
 
@@ -527,9 +554,9 @@ PassArgs pass_args(const HeadDecayCall &c) {
     return p;
 }
 
-}  // namespace
-
-hipError_t launch_head_decay_fwd(const HeadDecayCall &c, void *o, float *s_out, void *workspace, hipStream_t stream) {
+template <typename T, int DK, int DV>
+hipError_t forward(const HeadDecayCall &c, void *o, float *s_out, void *workspace, hipStream_t stream) {
+    using Kind = Kinds<T, DK, DV>;
     PassArgs p = pass_args(c);
     p.x = c.q;
     p.y = c.k;
@@ -540,98 +567,113 @@ hipError_t launch_head_decay_fwd(const HeadDecayCall &c, void *o, float *s_out, 
     if (p.nseg > 1) {
         Carver w{static_cast<unsigned char *>(workspace)};
         const size_t bhs = static_cast<size_t>(c.B) * c.H * p.nseg;
-        float *seg = w.take<float>(bhs * c.dk * c.dv), *dec = w.take<float>(bhs);
+        float *seg = w.take<float>(bhs * DK * DV), *dec = w.take<float>(bhs);
         p.s_out = seg;
         p.dec = dec;
-        hipError_t err = launch_any(Kind::LocalFwd, c.bf16, c.dk, c.dv, p, stream);
+        hipError_t err = launch_pass<typename Kind::LocalFwd>(p, stream);
         if (err != hipSuccess) return err;
-        err = launch_join(false, c.s0, dec, seg, c.B * c.H, p.nseg, c.dk * c.dv, stream);
+        err = launch_join(JoinArgs{c.s0, seg, dec, false}, nullptr, c.B * c.H, p.nseg, DK * DV, stream);
         if (err != hipSuccess) return err;
         p.start = seg;
     }
     p.out = o;
     p.s_out = s_out;
-    return launch_any(Kind::Forward, c.bf16, c.dk, c.dv, p, stream);
+    return launch_pass<typename Kind::Forward>(p, stream);
 }
 
-hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g, void *workspace, hipStream_t stream) {
+template <typename T>
+hipError_t sum_heads(const float *part, void *out, size_t n4, int rep, int d4, hipStream_t stream) {
+    hipLaunchKernelGGL(head_sum_kernel<T>, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, stream, part,
+                       static_cast<T *>(out), n4, rep, d4);
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV>
+hipError_t backward(const HeadDecayCall &c, const HeadDecayGrads &g, void *workspace, hipStream_t stream) {
+    using Kind = Kinds<T, DK, DV>;
     const PassArgs p0 = pass_args(c);
     const int groups = groups_of(c.T), BH = c.B * c.H, rep = c.H / c.Hk;
-    const size_t bh = BH, tok = bh * c.T, st = static_cast<size_t>(c.dk) * c.dv;
+    const size_t bh = BH, tok = bh * c.T, st = static_cast<size_t>(DK) * DV;
     Carver w{static_cast<unsigned char *>(workspace)};
     float *rows = w.take<float>(tok), *cols = w.take<float>(tok);
-    float *anchors = w.take<float>(bh * groups * st), *edges = w.take<float>(bh * groups * (c.dk / 16));
+    float *anchors = w.take<float>(bh * groups * st), *edges = w.take<float>(bh * groups * (DK / 16));
     double *part = w.take<double>(bh * groups);
     const float *s_start = c.s0, *a_start = g.ds_out;
     hipError_t err;
     if (p0.nseg > 1) {
         float *seg[2] = {w.take<float>(bh * p0.nseg * st), w.take<float>(bh * p0.nseg * st)};
-        float *dec = w.take<float>(bh * p0.nseg);
+        float *dec[2] = {w.take<float>(bh * p0.nseg), w.take<float>(bh * p0.nseg)};
+        PassArgs p[2] = {p0, p0};
         for (int rev = 0; rev < 2; ++rev) {
-            PassArgs p = p0;
-            p.y = rev ? c.q : c.k;
-            p.z = rev ? g.dout : c.v;
-            p.hx = p.hy = c.Hk;
-            p.hz = c.H;
-            p.s_out = seg[rev];
-            p.dec = dec;
-            err = launch_any(rev ? Kind::LocalRev : Kind::LocalFwd, c.bf16, c.dk, c.dv, p, stream);
-            if (err != hipSuccess) return err;
-            err = launch_join(rev, rev ? g.ds_out : c.s0, dec, seg[rev], BH, p0.nseg, c.dk * c.dv, stream);
-            if (err != hipSuccess) return err;
+            p[rev].y = rev ? c.q : c.k;
+            p[rev].z = rev ? g.dout : c.v;
+            p[rev].hx = p[rev].hy = c.Hk;
+            p[rev].hz = c.H;
+            p[rev].s_out = seg[rev];
+            p[rev].dec = dec[rev];
         }
+        err = launch_pair<typename Kind::LocalFwd, typename Kind::LocalRev>(p[0], p[1], stream);
+        if (err != hipSuccess) return err;
+        const JoinArgs rev{g.ds_out, seg[1], dec[1], true};
+        err = launch_join(JoinArgs{c.s0, seg[0], dec[0], false}, &rev, BH, p0.nseg, DK * DV, stream);
+        if (err != hipSuccess) return err;
         s_start = seg[0];
         a_start = seg[1];
     }
-    float *shared = rep > 1 ? w.take<float>(tok * c.dk) : nullptr;
-    for (int pass = 0; pass < 2; ++pass) {  // dq in order, then dk reversed
-        PassArgs p = p0;
-        p.x = pass ? c.v : g.dout;
-        p.y = pass ? g.dout : c.v;
-        p.z = pass ? c.q : c.k;
-        p.hx = p.hy = c.H;
-        p.hz = c.Hk;
-        p.start = pass ? a_start : s_start;
-        p.start_t = true;
-        void *out = pass ? g.dk : g.dq;
-        p.out = shared ? shared : out;
-        p.out_f32 = shared != nullptr;
-        p.w = pass ? c.k : c.q;
-        p.hw = c.Hk;
-        p.dots = pass ? cols : rows;
-        p.anchors = anchors;
-        p.edges = edges;
-        if (c.T > 0) {
-            err = launch_any(pass ? Kind::Dk : Kind::Dq, c.bf16, c.dv, c.dk, p, stream);
-            if (err != hipSuccess) return err;
-            if (shared) {
-                const size_t n4 = tok / rep * c.dk / 4;
-                const dim3 grid(static_cast<unsigned>((n4 + 255) / 256));
-                if (c.bf16)
-                    hipLaunchKernelGGL(head_sum_kernel<bf16_t>, grid, dim3(256), 0, stream, shared,
-                                       static_cast<bf16_t *>(out), n4, rep, c.dk / 4);
-                else
-                    hipLaunchKernelGGL(head_sum_kernel<float>, grid, dim3(256), 0, stream, shared,
-                                       static_cast<float *>(out), n4, rep, c.dk / 4);
-                err = hipGetLastError();
-                if (err != hipSuccess) return err;
-            }
-        }
+    float *shared[2] = {nullptr, nullptr};  // dq and dk of every value head, where key heads are shared
+    if (rep > 1)
+        for (float *&x : shared) x = w.take<float>(tok * DK);
+    PassArgs p[2] = {p0, p0};  // dq in order, dk reversed
+    for (int pass = 0; pass < 2; ++pass) {
+        p[pass].x = pass ? c.v : g.dout;
+        p[pass].y = pass ? g.dout : c.v;
+        p[pass].z = pass ? c.q : c.k;
+        p[pass].hx = p[pass].hy = c.H;
+        p[pass].hz = c.Hk;
+        p[pass].start = pass ? a_start : s_start;
+        p[pass].start_t = true;
+        p[pass].out = shared[pass] ? shared[pass] : pass ? g.dk : g.dq;
+        p[pass].out_f32 = shared[pass] != nullptr;
+        p[pass].w = pass ? c.k : c.q;
+        p[pass].hw = c.Hk;
+        p[pass].dots = pass ? cols : rows;
+        p[pass].anchors = anchors;
+        p[pass].edges = edges;
     }
-    PassArgs p = p0;
-    p.x = c.k;
-    p.y = c.q;
-    p.z = g.dout;
-    p.hx = p.hy = c.Hk;
-    p.hz = c.H;
-    p.start = a_start;
-    p.out = g.dv;
-    p.s_out = g.ds0;
-    err = launch_any(Kind::Dv, c.bf16, c.dk, c.dv, p, stream);
-    if (err != hipSuccess) return err;
-    if (c.T > 0) {
-        hipLaunchKernelGGL(dla_kernel, dim3(static_cast<unsigned>(groups) * BH), dim3(ANCHOR * C), 0, stream, rows, cols, edges, c.lens,
-                           c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups, c.dk / 16);
+    PassArgs pv = p0;
+    pv.x = c.k;
+    pv.y = c.q;
+    pv.z = g.dout;
+    pv.hx = pv.hy = c.Hk;
+    pv.hz = c.H;
+    pv.start = a_start;
+    pv.out = g.dv;
+    pv.s_out = g.ds0;
+    if (c.T == 0) {  // ds0 = ds_out, and no token's gradient
+        err = launch_pass<typename Kind::Dv>(pv, stream);
+        if (err != hipSuccess) return err;
+    } else {
+        err = launch_pass<typename Kind::Dq>(p[0], stream);
+        if (err != hipSuccess) return err;
+        // Together where both fit the card at once: 34 us against 23 and 21 for 252 workgroups each (B3 T777 H12 d64, float32). Where
+        // they do not, they get in each other's way: 418 against 226 and 135 (B8 T4096 H16 d128, 512 each).
+        const unsigned room = 256 * std::max(1, 163840 / Kind::Dk::BYTES);
+        if (2 * pass_blocks<typename Kind::Dk>(p[1]) <= room) {
+            err = launch_pair<typename Kind::Dk, typename Kind::Dv>(p[1], pv, stream);
+        } else {
+            err = launch_pass<typename Kind::Dk>(p[1], stream);
+            if (err == hipSuccess) err = launch_pass<typename Kind::Dv>(pv, stream);
+        }
+        if (err != hipSuccess) return err;
+        if (rep > 1) {
+            const size_t n4 = tok / rep * DK / 4;
+            err = sum_heads<T>(shared[0], g.dq, n4, rep, DK / 4, stream);
+            if (err != hipSuccess) return err;
+            err = sum_heads<T>(shared[1], g.dk, n4, rep, DK / 4, stream);
+            if (err != hipSuccess) return err;
+        }
+        hipLaunchKernelGGL(dla_kernel, dim3(static_cast<unsigned>(groups) * BH), dim3(ANCHOR * C), 0, stream, rows, cols, edges,
+                           c.lens, c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups, DK / 16);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -641,5 +683,26 @@ hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g
     }
     return err;
 }
+
+}  // namespace
+
+#define MUIR_HD(K, V, F)                                                     \
+    if (c.dk == K && c.dv == V) return c.bf16 ? F(bf16_t, K, V) : F(float, K, V);
+
+hipError_t launch_head_decay_fwd(const HeadDecayCall &c, void *o, float *s_out, void *workspace, hipStream_t stream) {
+#define MUIR_F(T, K, V) forward<T, K, V>(c, o, s_out, workspace, stream)
+    MUIR_HD(64, 64, MUIR_F) MUIR_HD(64, 128, MUIR_F) MUIR_HD(128, 64, MUIR_F) MUIR_HD(128, 128, MUIR_F)
+#undef MUIR_F
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_head_decay_bwd(const HeadDecayCall &c, const HeadDecayGrads &g, void *workspace, hipStream_t stream) {
+#define MUIR_F(T, K, V) backward<T, K, V>(c, g, workspace, stream)
+    MUIR_HD(64, 64, MUIR_F) MUIR_HD(64, 128, MUIR_F) MUIR_HD(128, 64, MUIR_F) MUIR_HD(128, 128, MUIR_F)
+#undef MUIR_F
+    return hipErrorInvalidValue;
+}
+
+#undef MUIR_HD
 
 }  // namespace muir

@@ -26,8 +26,8 @@ size_t head_decay_bwd_workspace_bytes(int B, int T, int H, int Hk, int dk, int d
     const int nseg = head_decay_segments(B, T, H, bf16);
     const size_t bh = static_cast<size_t>(B) * H, tok = bh * T, groups = hd::groups_of(T);
     size_t n = 2 * up256(tok * 4) + up256(bh * groups * dk * dv * 4) + up256(bh * groups * (dk / 16) * 4) + up256(bh * groups * 8);
-    if (nseg > 1) n += 2 * up256(bh * nseg * dk * dv * 4) + up256(bh * nseg * 4);
-    if (Hk != H) n += up256(tok * dk * 4);
+    if (nseg > 1) n += 2 * up256(bh * nseg * dk * dv * 4) + 2 * up256(bh * nseg * 4);
+    if (Hk != H) n += 2 * up256(tok * dk * 4);
     return n;
 }
 
