@@ -82,6 +82,8 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     using L = PassLds<T, DX, DZ, LOCAL, NTP>;
     using frag = typename O::frag;
     constexpr int RT = DX / 16, ES = sizeof(T), THREADS = L::THREADS, NW = L::NW;
+    // LOCAL walks against the order of the pass that follows it, which then finds what was read last in the caches.
+    constexpr bool DOWN = REV != LOCAL;
     constexpr int SIDE = KEEP ? 2 : 4;  // sums that are added to in turn, so that a product does not wait for the one before
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char *const ly = smem + L::Y, *const lz = smem + L::Z, *const lx = smem + L::X, *const lp = smem + L::P;
@@ -146,7 +148,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     Chunk f;
     // The wavefronts take turns at a chunk's decays.
     auto fetch = [&](int it) {
-        const int t0 = (REV ? c0 + steps - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
+        const int t0 = (DOWN ? c0 + steps - 1 - it : c0 + it) * C, rows = uniform(min(max(end - t0, 0), C));
         if constexpr (!LOCAL) f.x.load(gx + static_cast<size_t>(t0) * sx, sx, rows, tid);
         f.y.load(gy + static_cast<size_t>(t0) * sy, sy, rows, tid);
         f.z.load(gz + static_cast<size_t>(t0) * sz, sz, rows, tid);
@@ -196,7 +198,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     if constexpr (REV) behind();
 
     for (int it = 0; it < steps; ++it) {
-        const int c = REV ? c0 + steps - 1 - it : c0 + it, t0 = c * C;
+        const int c = DOWN ? c0 + steps - 1 - it : c0 + it, t0 = c * C;
         // Addresses that follow from the lane are made anew in each chunk: kept over the loop they would take some forty
         // registers that the state and the tiles need.
         asm volatile("" : "+v"(lane), "+v"(m), "+v"(g));
@@ -206,7 +208,9 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
         f.z.put(lz, tid);
         if (wv == it % NW) {
             const double Lt = scan64(log2_decay(f.a));
-            const float to_start = exp2_f(static_cast<float>(Lt)), to_end = exp2_f(static_cast<float>(lane_value(Lt, 63) - Lt));
+            // LOCAL: decayed up to the segment's end at once, over the chunks walked before.
+            const double far = LOCAL ? seg_log : 0.0;
+            const float to_start = exp2_f(static_cast<float>(Lt + far)), to_end = exp2_f(static_cast<float>(lane_value(Lt, 63) - Lt + far));
             sh_L[lane] = f32x2_t{static_cast<float>(Lt), static_cast<float>(Lt - static_cast<float>(Lt))};
             sh_out[lane] = REV ? to_end : to_start;
             sh_upd[lane] = REV ? to_start : to_end;
@@ -331,8 +335,10 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
         }
 
         // The state: decayed over the chunk, then y^T (decayed z).
+        if constexpr (!LOCAL) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
+            for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
+        }
 #pragma unroll
         for (int pr = 0; pr < 2; ++pr) {
             frag zs[NTU];
@@ -653,17 +659,17 @@ hipError_t backward(const HeadDecayCall &c, const HeadDecayGrads &g, void *works
         err = launch_pass<typename Kind::Dv>(pv, stream);
         if (err != hipSuccess) return err;
     } else {
-        err = launch_pass<typename Kind::Dq>(p[0], stream);
-        if (err != hipSuccess) return err;
-        // Together where both fit the card at once: 34 us against 23 and 21 for 252 workgroups each (B3 T777 H12 d64, float32). Where
-        // they do not, they get in each other's way: 418 against 226 and 135 (B8 T4096 H16 d128, 512 each).
-        const unsigned room = 256 * std::max(1, 163840 / Kind::Dk::BYTES);
-        if (2 * pass_blocks<typename Kind::Dk>(p[1]) <= room) {
-            err = launch_pair<typename Kind::Dk, typename Kind::Dv>(p[1], pv, stream);
+        // dv and dq together where both fit the card at once: B3 T777 H12 d64, float32, 252 workgroups each, 34 us against
+        // 23 and 21 (measured on dk and dv). Where they do not, they get in each other's way: 418 us against 226 and 135 for
+        // dk and dv of B8 T4096 H16 d128, 512 each. In turn, each walks against the one before, whose last tokens the caches hold.
+        const unsigned room = 256 * std::max(1, 163840 / Kind::Dq::BYTES);
+        if (2 * pass_blocks<typename Kind::Dq>(p[0]) <= room) {
+            err = launch_pair<typename Kind::Dq, typename Kind::Dv>(p[0], pv, stream);
         } else {
-            err = launch_pass<typename Kind::Dk>(p[1], stream);
-            if (err == hipSuccess) err = launch_pass<typename Kind::Dv>(pv, stream);
+            err = launch_pass<typename Kind::Dv>(pv, stream);
+            if (err == hipSuccess) err = launch_pass<typename Kind::Dq>(p[0], stream);
         }
+        if (err == hipSuccess) err = launch_pass<typename Kind::Dk>(p[1], stream);
         if (err != hipSuccess) return err;
         if (rep > 1) {
             const size_t n4 = tok / rep * DK / 4;
