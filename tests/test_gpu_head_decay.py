@@ -123,6 +123,9 @@ CASES = [
     (2, 1111, 2, 2, 64, 128, "bf16", False, [1111, 500], True, "slow"),
     (1, 1100, 1, 1, 128, 128, "bf16", True, None, True, "slow"),
     (1, 1025, 2, 2, 128, 128, "f32", False, None, True, "slow"),
+    # More workgroups than run at once: each pass in a launch of its own.
+    (20, 70, 30, 15, 64, 64, "bf16", False, [70] * 10 + [3] * 10, True, "mixed"),
+    (9, 66, 30, 30, 64, 64, "f32", True, None, True, "slow"),
 ]
 
 
@@ -268,6 +271,44 @@ def test_other_stream_and_graph_replays(device):
         eg = backward(x)
         assert torch.equal(o3, eo) and torch.equal(s3, es) and all(torch.equal(g3[n], eg[n]) for n in eg)
         x["v"].copy_(keep)
+
+
+def test_two_calls_at_once(device):
+    """Calls on two streams share nothing: each has its own workspace and outputs."""
+    xs = [inputs(device, 1, 2000, 4, 2, 128, 128, torch.bfloat16, seed=i) for i in range(2)]
+    want = [(*forward(x), backward(x)) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(device) for _ in xs]
+    got = [[], []]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append((*forward(xs[i]), backward(xs[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, s, g in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(s, want[i][1])
+            assert all(torch.equal(g[n], want[i][2][n]) for n in g)
+
+
+def test_offsets_past_32_bits(device):
+    """Rows behind element 2^32 of v and o: the last tokens of the last sequence equal those of that sequence alone."""
+    B, T, H, Hk = 3, 90000, 128, 1
+    g = torch.Generator(device=device).manual_seed(0)
+    q, k = (0.1 * torch.randn(B, T, Hk, 64, device=device, generator=g, dtype=torch.bfloat16) for _ in range(2))
+    v = torch.randn(B, T, H, 128, device=device, generator=g, dtype=torch.bfloat16)
+    a = 0.5 + 0.5 * torch.rand(B, T, H, device=device, generator=g)
+    assert v.numel() > 2 ** 32
+    o, s = muir.chunk_fwd_head_decay(q, k, v, a)
+    one = [t[2:].clone() for t in (q, k, v, a)]
+    state = None
+    for t0 in range(0, T, 30016):  # whole chunks, the state carried
+        part = [t[:, t0:t0 + 30016].contiguous() for t in one]
+        po, state = muir.chunk_fwd_head_decay(*part, state)
+        # Other segment borders: the states differ by float32 roundings, an output by at most one bf16 step beside them.
+        d = (po.float() - o[2:, t0:t0 + 30016].float()).abs()
+        assert (d <= 2.0 ** -7 * po.float().abs() + 1e-4 * po.float().abs().max()).all()
+    assert (state - s[2:]).abs().max() <= 1e-4 * s.abs().max()
 
 
 def test_gradients_against_differences(device):
