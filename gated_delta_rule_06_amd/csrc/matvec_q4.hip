@@ -7,11 +7,12 @@
 // sum is a product with ones, shared by the NT weight tiles of a wavefront. float32 x goes in as three bf16
 // terms (to its last bit or two).
 //
-// A workgroup walks K in tiles of 1024 columns, 128 to each of its eight wavefronts, whose sums meet in LDS in a fixed
-// order. A tile's weights, x and scales come as whole cache lines through LDS, the next tile's in flight. Reading
-// them straight into the lanes that multiply them (16 rows, 64 bytes each, the scales one by one) took 51 us at
-// M = 16, N = 16384, K = 8192, G = 64 where this takes 24: the vector cache looks up every row of a load on its own.
-// Fetching two or three tiles ahead changed nothing. A lane takes 16 bytes, 32 weights of one row, from
+// A workgroup walks K in tiles of 1024 columns, 128 to each of eight wavefronts (or pairs of them, half of the weight rows
+// each), whose sums meet in LDS in a fixed order. A tile's weights, x and scales come as whole cache lines through LDS, the
+// next tile's in flight. Reading them straight into the lanes that multiply them (16 rows, 64 bytes each, the scales one by
+// one) took 51 us at M = 16, N = 16384, K = 8192, G = 64 where this takes 23 (3.1 TB/s; a plain sum over memory reads 3.9 on
+// this card): the vector cache looks up every row of a load on its own. Fetching two or three tiles ahead changed nothing.
+// A lane takes 16 bytes, 32 weights of one row, from
 // LDS, and the four lanes of a row exchange them (4x4 transpose in registers) so that each product's contraction
 // is 32 consecutive columns.
 #include "common.hpp"
@@ -67,24 +68,24 @@ template <typename XT, int NT, int WAVES, int GROUP> constexpr int q4_tile_bytes
     return 16 * NT * (WAVES * 64 + 16) + (sizeof(XT) == 2 ? 16 * (WAVES * 256 + 16) : 0) + (sc + 15) / 16 * 16;
 }
 
-template <typename XT, typename ST, int NT, int WAVES, int GROUP, bool ZERO>
-__global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restrict__ x, const uint8_t *__restrict__ w,
+template <typename XT, typename ST, int NT, int NH, int WAVES, int GROUP, bool ZERO>
+__global__ __launch_bounds__(WAVES *NH * 64) void matvec_q4_kernel(const XT *__restrict__ x, const uint8_t *__restrict__ w,
                                                                const ST *__restrict__ scale, const ST *__restrict__ zero,
                                                                XT *__restrict__ y, int M, int N, int K) {
     constexpr int NX = sizeof(XT) == 2 ? 1 : 3;
     constexpr bool XLDS = NX == 1;
     constexpr int PER = GROUP / 32, NG = 4 / PER;  // products of a group, groups of a step
-    constexpr int THREADS = WAVES * 64, KT = WAVES * 128;
+    constexpr int THREADS = WAVES * NH * 64, KT = WAVES * 128, NW = NT / NH;  // a wavefront has NW of the tiles of 16 rows
     constexpr int WC = KT / 32, XC = KT / 8;             // 16-byte chunks of a row of the tile
     constexpr int LW = WC * 16 + 16, LX = XC * 16 + 16;  // row strides, padded by 16 bytes: rows in different banks
     constexpr int NWL = 16 * NT * WC / THREADS, NXL = XLDS ? 16 * XC / THREADS : 1;
-    static_assert(16 * NT * WC % THREADS == 0 && 16 * XC % THREADS == 0, "whole chunks");
+    static_assert(16 * NT * WC % THREADS == 0 && 16 * XC % THREADS == 0 && THREADS % WC == 0 && THREADS % XC == 0, "whole chunks");
     constexpr int SC = WAVES * NG, NSCALE = 16 * NT * SC, NSL = (NSCALE + THREADS - 1) / THREADS;  // scales of the tile
     constexpr int LS = SC + 1;                                                                    // row stride, in pairs
     constexpr int XAT = 16 * NT * LW, SAT = XAT + (XLDS ? 16 * LX : 0), TILE = q4_tile_bytes<XT, NT, WAVES, GROUP>();
     static_assert(TILE >= SAT + 16 * NT * LS * 8, "tile");
     extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, m = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = (tid >> 6) % WAVES, nh = (tid >> 6) / WAVES, m = lane & 15, g = lane >> 4;
     const int mt = blockIdx.y * 16, n0 = blockIdx.x * (16 * NT), KG = K / GROUP;
     const int tiles = (K + KT - 1) / KT, live = min(M - mt, 16), rows = N - n0;
     // One base for the workgroup; a lane's own offsets fit 32 bits (64 rows of at most 2^25 bytes).
@@ -101,18 +102,29 @@ __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restr
         ST sc[NSL], zp[NSL];
     };
     Step ahead;
-    auto fetch = [&](Step &f, int t) {
+    // A lane's offsets in the first tile; rows behind the last are the last again, computed and not stored.
+    uint32_t at_w[NWL], at_s[NSL], at_x[NXL];
 #pragma unroll
-        for (int j = 0; j < NWL; ++j) {
-            const int i = tid + THREADS * j, k = t * KT + i % WC * 32;
-            // Rows behind the last are the last again, computed and not stored.
-            const uint32_t at = static_cast<uint32_t>(min(i / WC, rows - 1)) * (K / 2) + k / 2;
-            f.w[j] = k < K ? *reinterpret_cast<const uint4 *>(wb + at) : uint4{0, 0, 0, 0};
-        }
+    for (int j = 0; j < NWL; ++j) {
+        const int i = tid + THREADS * j;
+        at_w[j] = static_cast<uint32_t>(min(i / WC, rows - 1)) * (K / 2) + i % WC * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < NSL; ++j) at_s[j] = static_cast<uint32_t>(min((tid + THREADS * j) / SC, rows - 1)) * KG;
+#pragma unroll
+    for (int j = 0; j < NXL; ++j) {
+        const int i = tid + THREADS * j;
+        at_x[j] = static_cast<uint32_t>(i / XC) * K + i % XC * 8;
+    }
+    auto fetch = [&](Step &f, int t) {
+        const int kw = tid % WC * 32, kx = tid % XC * 8, left = K - t * KT;  // THREADS is a multiple of WC and XC
+#pragma unroll
+        for (int j = 0; j < NWL; ++j)
+            f.w[j] = kw < left ? *reinterpret_cast<const uint4 *>(wb + (at_w[j] + static_cast<uint32_t>(t) * (KT / 2))) : uint4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < NSL; ++j) {
             const int i = tid + THREADS * j;
-            const uint32_t at = static_cast<uint32_t>(min(i / SC, rows - 1)) * KG + min(t * SC + i % SC, KG - 1);
+            const uint32_t at = at_s[j] + min(t * SC + i % SC, KG - 1);
             if (NSCALE % THREADS == 0 || i < NSCALE) {
                 f.sc[j] = sb[at];
                 if constexpr (ZERO) f.zp[j] = zb[at];
@@ -120,18 +132,17 @@ __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restr
         }
         if constexpr (XLDS) {
 #pragma unroll
-            for (int j = 0; j < NXL; ++j) {
-                const int i = tid + THREADS * j, row = i / XC, k = t * KT + i % XC * 8;
-                f.x[j] = k < K && row < live ? *reinterpret_cast<const uint4 *>(xb + static_cast<size_t>(row) * K + k) : uint4{0, 0, 0, 0};
-            }
+            for (int j = 0; j < NXL; ++j)
+                f.x[j] = kx < left && (tid + THREADS * j) / XC < live ? *reinterpret_cast<const uint4 *>(xb + (at_x[j] + static_cast<uint32_t>(t) * KT))
+                                                                     : uint4{0, 0, 0, 0};
         }
     };
     bf16x8_t ones;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ones[j] = static_cast<__bf16>(1.0f);
-    f32x4_t sum[NT];
+    f32x4_t sum[NW];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sum[t] = zero4();
+    for (int t = 0; t < NW; ++t) sum[t] = zero4();
 
     auto step = [&](Step &f, int t) {
         unsigned char *lw = smem + (t & 1) * TILE, *lx = lw + XAT;
@@ -172,24 +183,24 @@ __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restr
                 if (m < live && k0 + k < K) fx[u] = x_frag(xb + static_cast<size_t>(m) * K + k0 + k);
             }
         }
-        uint4 d[NT];
+        uint4 d[NW];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            d[n] = *reinterpret_cast<const uint4 *>(lw + (16 * n + m) * LW + (4 * wv + g) * 16);
+        for (int n = 0; n < NW; ++n) {
+            d[n] = *reinterpret_cast<const uint4 *>(lw + (16 * (nh * NW + n) + m) * LW + (4 * wv + g) * 16);
             exchange(d[n]);
         }
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
-            f32x4_t xs = zero4(), acc[NT];
+            f32x4_t xs = zero4(), acc[NW];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n] = zero4();
+            for (int n = 0; n < NW; ++n) acc[n] = zero4();
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
                 const int u = q * PER + e;
 #pragma unroll
                 for (int c = NX - 1; c >= 0; --c) xs = Mma<bf16_t>::mma(fx[u].f[c], ones, xs);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < NW; ++n) {
                     const uint32_t dw[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
                     const bf16x8_t fw = nibbles(dw[u], base);
 #pragma unroll
@@ -197,8 +208,8 @@ __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restr
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 v = ls[(16 * n + m) * LS + wv * NG + q];
+            for (int n = 0; n < NW; ++n) {
+                const float2 v = ls[(16 * (nh * NW + n) + m) * LS + wv * NG + q];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[n][i] = fmaf(v.x, fmaf(-v.y, xs[i], acc[n][i]), sum[n][i]);
             }
@@ -209,31 +220,32 @@ __global__ __launch_bounds__(WAVES * 64) void matvec_q4_kernel(const XT *__restr
     __syncthreads();
     f32x4_t *sh = reinterpret_cast<f32x4_t *>(smem);  // [WAVES][NT][64]
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sh[(wv * NT + t) * 64 + lane] = sum[t];
+    for (int t = 0; t < NW; ++t) sh[(wv * NT + nh * NW + t) * 64 + lane] = sum[t];
     __syncthreads();
-    if (wv >= NT) return;
+    const int tile = tid >> 6;
+    if (tile >= NT) return;
     // Wavefront t finishes weight tile t: rows m = 4 g + i of x, column n = lane % 16.
-    f32x4_t r = sh[wv * 64 + lane];
+    f32x4_t r = sh[tile * 64 + lane];
 #pragma unroll
-    for (int i = 1; i < WAVES; ++i) r += sh[(i * NT + wv) * 64 + lane];
-    const int n = n0 + 16 * wv + m;
+    for (int i = 1; i < WAVES; ++i) r += sh[(i * NT + tile) * 64 + lane];
+    const int n = n0 + 16 * tile + m;
     if (n >= N) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (4 * g + i < live) elem<XT>::store(y, static_cast<size_t>(mt + 4 * g + i) * N + n, r[i]);
 }
 
-template <typename XT, typename ST, int NT, int WAVES>
+template <typename XT, typename ST, int NT, int NH, int WAVES>
 hipError_t go(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K, int group,
               hipStream_t s) {
     static_assert(WAVES >= NT, "a wavefront finishes each tile");
-    const dim3 grid((N + 16 * NT - 1) / (16 * NT), (M + 15) / 16), block(WAVES * 64);
+    const dim3 grid((N + 16 * NT - 1) / (16 * NT), (M + 15) / 16), block(WAVES * NH * 64);
 #define MUIR_Q4(G, Z)                                                                                               \
     if (group == G && (zero != nullptr) == Z) {                                                                     \
-        auto kern = matvec_q4_kernel<XT, ST, NT, WAVES, G, Z>;                                               \
+        auto kern = matvec_q4_kernel<XT, ST, NT, NH, WAVES, G, Z>;                                               \
         constexpr int two = 2 * q4_tile_bytes<XT, NT, WAVES, G>(), sums = WAVES * NT * 1024;                        \
         constexpr int bytes = two > sums ? two : sums;                                                              \
-        const hipError_t err = allow_lds<matvec_q4_kernel<XT, ST, NT, WAVES, G, Z>>(bytes);                            \
+        const hipError_t err = allow_lds<matvec_q4_kernel<XT, ST, NT, NH, WAVES, G, Z>>(bytes);                            \
         if (err != hipSuccess) return err;                                                                          \
         hipLaunchKernelGGL(kern, grid, block, bytes, s, static_cast<const XT *>(x),                                 \
                            static_cast<const uint8_t *>(w), static_cast<const ST *>(scale),                         \
@@ -249,13 +261,14 @@ template <typename XT, typename ST>
 hipError_t pick(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K, int group,
                 hipStream_t s) {
     // As many weight rows to a workgroup as leave one workgroup for each of the 256 compute units: x is read and unpacked
-    // once for them all. At M = 1 (us, for 16, 32 and 64 rows): N = 2048, K = 2048: 3.8, 4.3, 5.6; N = 8192, K = 2048:
-    // 6.8, 4.9, 6.0; N = 16384, K = 8192: 36.3, 26.4, 21.9; M = 64, N = K = 4096 (four times the workgroups): 22.2, 14.3, 10.4.
-    // Four wavefronts instead of eight were slower at each choice but N = 8192 with 16 rows.
+    // once for them all. At M = 1 (us, for 16, 32 and 64 rows): N = 2048, K = 2048: 3.8, 4.4, 5.3; N = 8192, K = 2048:
+    // 6.6, 4.8, 5.7; N = 16384, K = 8192: 34.7, 24.7, 19.9; M = 64, N = K = 4096 (four times the workgroups): 21.7, 13.9, 9.7.
+    // Sixteen wavefronts, half of the rows each, against eight with all of them: 23.3 and 24.3 us at M = 16, N = 16384, K = 8192;
+    // 19.9 and 21.9 at M = 1.
     const long long work = static_cast<long long>(N) * ((M + 15) / 16);
-    if (work >= 256 * 64) return go<XT, ST, 4, 8>(x, w, scale, zero, y, M, N, K, group, s);
-    if (work >= 256 * 32) return go<XT, ST, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);
-    return go<XT, ST, 1, 8>(x, w, scale, zero, y, M, N, K, group, s);
+    if (work >= 256 * 64) return go<XT, ST, 4, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);
+    if (work >= 256 * 32) return go<XT, ST, 2, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);
+    return go<XT, ST, 1, 1, 8>(x, w, scale, zero, y, M, N, K, group, s);
 }
 
 }  // namespace
