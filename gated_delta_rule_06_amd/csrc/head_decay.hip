@@ -27,7 +27,7 @@ struct PassArgs {
     void *out;              // [B, T, H, DZ] in the element type, or float32 with out_f32
     bool out_f32;
     float *s_out;           // state after the last token, [DX, DZ], or NULL; LOCAL: [B*H, nseg] states
-    float *dec;             // LOCAL: [B*H, nseg]
+    f32x2_t *dec;           // LOCAL: [B*H, nseg] decays, as a float32 and what it leaves
     const void *w;          // KEEP: [B, T, hw, DZ], dots [B, T, H] = out . w
     int hw;
     float *dots;
@@ -67,7 +67,7 @@ template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
     static constexpr int Y = 0, Z = Y + O::template tile_bytes<DX>(), X = Z + O::template tile_bytes<DZ>();
     static constexpr int P = X + (LOCAL ? 0 : O::template tile_bytes<DX>());
     static constexpr int TAIL = P + (LOCAL ? 0 : NTP * O::template tile_bytes<C>());
-    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + (LOCAL ? 0 : NW * C * 4);
+    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 16 + (LOCAL ? 0 : NW * C * 4);
 };
 
 // One wavefront owns 16 columns of the state and of the output; see head_decay.hpp for the operand order.
@@ -99,7 +99,8 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     f32x2_t *const sh_L = reinterpret_cast<f32x2_t *>(smem + L::TAIL);
     float *const sh_out = reinterpret_cast<float *>(sh_L + C);        // decay between a token and the start state
     float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
-    float *const sh_dot = sh_upd + C;                                 // [NW][C]
+    float *const sh_carry = sh_upd + C;                               // decay of the state over the chunk, and what it owes the next
+    float *const sh_dot = sh_carry + 4;                               // [NW][C]
 
     int tid = threadIdx.x;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -146,6 +147,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     }
     const float a_h = p.a_fixed && p.nchunks > 0 ? p.a[h] : 1.f;
     double seg_log = 0.0;
+    if (!LOCAL && tid == 0) sh_carry[1] = 0.f;
 
     struct Chunk {
         Tile<T, DX, THREADS> x, y;
@@ -226,7 +228,6 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
         if (it + 1 < steps) fetch(it + 1);
         lds_barrier();
         const f32x2_t Lc = sh_L[C - 1];
-        const float carry = exp2_f(Lc[0] + Lc[1]);
         if constexpr (LOCAL) seg_log += static_cast<double>(Lc[0]) + Lc[1];
         frag zf[2];
 #pragma unroll
@@ -262,6 +263,23 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                         v[e] = (REV ? j0 + e >= i : j0 + e <= i) ? w : 0.f;
                     }
                     O::template put4<C, NTP>(lp, i, j0 / 4, v);
+                }
+            }
+            // A wavefront with less to do here makes the state's decay over the chunk. A float32 near exp2(L) is off by up to
+            // 2^-24, and a fixed decay's by the same amount in every chunk: over 64 chunks that was 6e-6 in dla. So what a chunk's
+            // factor leaves of L goes into the next one's, and the product of the factors stays within one rounding.
+            if (wv == (REV ? NW / 8 * 4 + NW / 4 % 2 * 3 : NW / 8)) {
+                const float rest = Lc[1] + sh_carry[1], factor = exp2_f(Lc[0] + rest);
+                const float n = rintf(Lc[0]);
+                // 2^(L - n) in 64 bits by the exponential's series (|L - n| ln 2 < 0.35: eleven terms leave 2^-42).
+                const double y = (static_cast<double>(Lc[0] - n) + rest) * 0.6931471805599453;
+                double e = 1.0;
+#pragma unroll
+                for (int k = 10; k >= 1; --k) e = fma(e * y, 1.0 / k, 1.0);
+                const float off = static_cast<float>(ldexp(static_cast<double>(factor), -static_cast<int>(n)) - e) / static_cast<float>(e);
+                if (lane == 0) {
+                    sh_carry[0] = factor;
+                    sh_carry[1] = factor > 0.f ? -1.44269504f * off : 0.f;  // log2 of what the rounding took
                 }
             }
             lds_barrier();
@@ -343,6 +361,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
 
         // The state: decayed over the chunk, then y^T (decayed z).
         if constexpr (!LOCAL) {
+            const float carry = *sh_carry;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
         }
@@ -393,7 +412,10 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     float *st = nullptr;
     if (LOCAL) {
         st = p.s_out + static_cast<size_t>(bh * static_cast<size_t>(p.nseg) + seg) * DUMP;
-        if (tid == 0) p.dec[static_cast<size_t>(bh) * p.nseg + seg] = exp2_f(static_cast<float>(seg_log));
+        if (tid == 0) {
+            const double d = exp2(seg_log);
+            p.dec[static_cast<size_t>(bh) * p.nseg + seg] = f32x2_t{static_cast<float>(d), static_cast<float>(d - static_cast<float>(d))};
+        }
     } else if (p.s_out && seg == (REV ? 0 : p.nseg - 1)) {
         st = p.s_out + static_cast<size_t>(bh) * DUMP;
     }
@@ -428,7 +450,7 @@ __global__ __launch_bounds__(4 * K::DZ, pass_waves<K>()) void pair_kernel(PassAr
 struct JoinArgs {
     const float *s0;
     float *seg;
-    const float *dec;
+    const f32x2_t *dec;
     bool rev;
 };
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs first, JoinArgs second, int nseg, int n4) {
@@ -437,14 +459,14 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs first, JoinArgs seco
     if (i >= n4) return;
     f32x4_t x = p.s0 ? reinterpret_cast<const f32x4_t *>(p.s0)[static_cast<size_t>(bh) * n4 + i] : zero4();
     f32x4_t *at = reinterpret_cast<f32x4_t *>(p.seg) + static_cast<size_t>(bh) * nseg * n4 + i;
-    const float *d = p.dec + static_cast<size_t>(bh) * nseg;
+    const f32x2_t *d = p.dec + static_cast<size_t>(bh) * nseg;
 #pragma unroll 4
     for (int s = 0; s < nseg; ++s) {
         const int k = p.rev ? nseg - 1 - s : s;
         f32x4_t own = zero4();
         if (s + 1 < nseg) own = at[static_cast<size_t>(k) * n4];  // the last one's is not made: no segment starts behind it
         at[static_cast<size_t>(k) * n4] = x;
-        if (s + 1 < nseg) x = x * d[k] + own;
+        if (s + 1 < nseg) x = x * d[k][0] + (x * d[k][1] + own);
     }
 }
 
@@ -580,7 +602,8 @@ hipError_t forward(const HeadDecayCall &c, void *o, float *s_out, void *workspac
     if (p.nseg > 1) {
         Carver w{static_cast<unsigned char *>(workspace)};
         const size_t bhs = static_cast<size_t>(c.B) * c.H * p.nseg;
-        float *seg = w.take<float>(bhs * DK * DV), *dec = w.take<float>(bhs);
+        float *seg = w.take<float>(bhs * DK * DV);
+        f32x2_t *dec = w.take<f32x2_t>(bhs);
         p.s_out = seg;
         p.dec = dec;
         hipError_t err = launch_pass<typename Kind::LocalFwd>(p, stream);
@@ -615,7 +638,7 @@ hipError_t backward(const HeadDecayCall &c, const HeadDecayGrads &g, void *works
     hipError_t err;
     if (p0.nseg > 1) {
         float *seg[2] = {w.take<float>(bh * p0.nseg * st), w.take<float>(bh * p0.nseg * st)};
-        float *dec[2] = {w.take<float>(bh * p0.nseg), w.take<float>(bh * p0.nseg)};
+        f32x2_t *dec[2] = {w.take<f32x2_t>(bh * p0.nseg), w.take<f32x2_t>(bh * p0.nseg)};
         PassArgs p[2] = {p0, p0};
         for (int rev = 0; rev < 2; ++rev) {
             p[rev].y = rev ? c.q : c.k;

@@ -19,14 +19,14 @@ size_t head_decay_fwd_workspace_bytes(int B, int T, int H, int dk, int dv, bool 
     const int nseg = head_decay_segments(B, T, H, bf16);
     if (nseg == 1) return 0;
     const size_t bhs = static_cast<size_t>(B) * H * nseg;
-    return up256(bhs * dk * dv * 4) + up256(bhs * 4);
+    return up256(bhs * dk * dv * 4) + up256(bhs * 8);
 }
 
 size_t head_decay_bwd_workspace_bytes(int B, int T, int H, int Hk, int dk, int dv, bool bf16) {
     const int nseg = head_decay_segments(B, T, H, bf16);
     const size_t bh = static_cast<size_t>(B) * H, tok = bh * T, groups = hd::groups_of(T);
     size_t n = 2 * up256(tok * 4) + up256(bh * groups * dk * dv * 4) + up256(bh * groups * (dk / 16) * 4) + up256(bh * groups * 8);
-    if (nseg > 1) n += 2 * up256(bh * nseg * dk * dv * 4) + 2 * up256(bh * nseg * 4);
+    if (nseg > 1) n += 2 * up256(bh * nseg * dk * dv * 4) + 2 * up256(bh * nseg * 8);
     if (Hk != H) n += 2 * up256(tok * dk * 4);
     return n;
 }
