@@ -219,7 +219,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
             const double Lt = scan64(log2_decay(f.a));
             // LOCAL: decayed up to the segment's end at once, over the chunks walked before.
             const double far = LOCAL ? seg_log : 0.0;
-            const float to_start = exp2_f(static_cast<float>(Lt + far)), to_end = exp2_f(static_cast<float>(lane_value(Lt, 63) - Lt + far));
+            const float to_start = exp2_pair(Lt + far), to_end = exp2_pair(lane_value(Lt, 63) - Lt + far);
             sh_L[lane] = f32x2_t{static_cast<float>(Lt), static_cast<float>(Lt - static_cast<float>(Lt))};
             sh_out[lane] = REV ? to_end : to_start;
             sh_upd[lane] = REV ? to_start : to_end;
@@ -259,7 +259,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const f32x2_t d = REV ? sh_L[j0 + e] - Li : Li - sh_L[j0 + e];
-                        const float w = acc[u][e] * exp2_f(d[0] + d[1]);
+                        const float w = acc[u][e] * (KEEP || ES == 4 ? exp2_pair(d[0], d[1]) : exp2_f(d[0] + d[1]));
                         v[e] = (REV ? j0 + e >= i : j0 + e <= i) ? w : 0.f;
                     }
                     O::template put4<C, NTP>(lp, i, j0 / 4, v);
@@ -269,7 +269,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
             // 2^-24, and a fixed decay's by the same amount in every chunk: over 64 chunks that was 6e-6 in dla. So what a chunk's
             // factor leaves of L goes into the next one's, and the product of the factors stays within one rounding.
             if (wv == (REV ? NW / 8 * 4 + NW / 4 % 2 * 3 : NW / 8)) {
-                const float rest = Lc[1] + sh_carry[1], factor = exp2_f(Lc[0] + rest);
+                const float rest = Lc[1] + sh_carry[1], factor = exp2_pair(Lc[0], rest);
                 const float n = rintf(Lc[0]);
                 // 2^(L - n) in 64 bits by the exponential's series (|L - n| ln 2 < 0.35: eleven terms leave 2^-42).
                 const double y = (static_cast<double>(Lc[0] - n) + rest) * 0.6931471805599453;

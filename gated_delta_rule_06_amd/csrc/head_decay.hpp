@@ -185,5 +185,16 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// exp2(hi + lo) to the last bit or so: the sum as one float32 would be off by 2^-24 of itself, which a fixed decay repeats in
+// every chunk and the sum of its gradient over all tokens shows.
+__device__ __forceinline__ float exp2_pair(float hi, float lo) {
+    const float n = rintf(hi);
+    return __builtin_amdgcn_ldexpf(exp2_f((hi - n) + lo), static_cast<int>(n));
+}
+__device__ __forceinline__ float exp2_pair(double x) {
+    const float hi = static_cast<float>(x);
+    return exp2_pair(hi, static_cast<float>(x - hi));
+}
+
 }  // namespace hd
 }  // namespace muir
