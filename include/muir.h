@@ -426,7 +426,9 @@ size_t muir_state_bytes(int B, int H, int dk, int dv);
  * Layer operators around the chunk forward.
  *
  * They follow the conventions above. Buffers that are read and written one element at a time (a, lens, dla,
- * rstd, scale, zero, dweight, y of muir_matvec_q4) need only their element's alignment.
+ * rstd, scale, zero, dweight, y of muir_matvec_q4) need only their element's alignment. A workspace belongs to one
+ * call at a time: calls that may overlap (on two streams, or in two captured graphs that are replayed side by side) need
+ * one each.
  */
 
 /*
