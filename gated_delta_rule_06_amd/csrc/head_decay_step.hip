@@ -4,7 +4,8 @@
 // independent, so a workgroup takes COLS of a head's dv columns: all of them where the heads alone fill the
 // card, a quarter where they do not. A thread has four columns (16-byte loads) of four rows; the output sums over
 // rows first inside each wavefront, then over the wavefronts through LDS, in a fixed order. State loads and
-// stores are non-temporal: the state is not touched again before the next step.
+// stores are non-temporal: the state is not touched again before the next step. B256 H16 Hk4 128/128 bf16: 83 us for 541 MB, 6.5 TB/s;
+// B1 H16: 2.7 us.
 #include "common.hpp"
 #include "mfma.hpp"
 #include "op_kernels.hpp"

@@ -10,7 +10,7 @@
 // A workgroup walks K in tiles of 1024 columns, 128 to each of eight wavefronts (or pairs of them, half of the weight rows
 // each), whose sums meet in LDS in a fixed order. A tile's weights, x and scales come as whole cache lines through LDS, the
 // next tile's in flight. Reading them straight into the lanes that multiply them (16 rows, 64 bytes each, the scales one by
-// one) took 51 us at M = 16, N = 16384, K = 8192, G = 64 where this takes 23 (3.1 TB/s; a plain sum over memory reads 3.9 on
+// one) took 51 us at M = 16, N = 16384, K = 8192, G = 64 where this takes 21 (fastest of 20 calls, 3.4 TB/s; a plain sum over memory reads 3.9 on
 // this card): the vector cache looks up every row of a load on its own. Fetching two or three tiles ahead changed nothing.
 // A lane takes 16 bytes, 32 weights of one row, from
 // LDS, and the four lanes of a row exchange them (4x4 transpose in registers) so that each product's contraction
