@@ -332,3 +332,16 @@ def test_gradients_against_differences(device):
         scale = (mag[key].abs() * r.abs()).sum() if key != "la" else (backward64(x)["la"].abs() * r.abs()).sum() * 64
         print(f"  {n}: {got.item():.8f} against {want.item():.8f}", flush=True)
         assert abs(got - want) <= 2 * kf(90) * scale + 1e-7 * scale
+
+
+@pytest.mark.parametrize("T", [1, 64, 130, 1500])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_last_state_over_the_first(device, T, dtype):
+    """s_out may be s0, with one segment to a head and with several: the same bits as with two buffers."""
+    x = inputs(device, 2, T, 4, 2, 128, 64, dtype, seed=7)
+    want_o, want_s = forward(x)
+    s0 = x["s0"]
+    for _ in range(3):
+        x["s0"] = s0.clone()
+        o, s = forward(x, s_out=x["s0"])
+        assert s is x["s0"] and torch.equal(o, want_o) and torch.equal(s, want_s)
