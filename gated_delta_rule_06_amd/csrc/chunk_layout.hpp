@@ -215,7 +215,7 @@ template <int VC> struct RowV<float, VC> {
         if constexpr (VC == 4) {
             // The whole offset in the lane's register: with a scalar part the compiler lets the very next instruction
             // overwrite the stored registers, before a store of 16 bytes has read its last lanes.
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, int(voff + soff), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, int(whole_offset(voff, soff)), 0, 0);
         } else if constexpr (VC == 2) {
             const f32x2_t f = {v[0], v[1]};
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, f), r, int(voff), int(soff), 0);

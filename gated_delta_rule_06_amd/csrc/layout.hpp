@@ -4,10 +4,19 @@
 #pragma once
 
 #include <stddef.h>
+#include <stdint.h>
 
 namespace muir {
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// A lane's whole byte offset into a buffer from its own part and the part that all lanes share. Buffers reach to 4 GiB, so
+// the sum of a row behind the end can pass 32 bits: it then becomes an offset behind every buffer of whole token rows (they end
+// 256 bytes below 4 GiB at the latest), 16 bytes of which do not wrap either.
+constexpr uint32_t whole_offset(uint32_t lane, uint32_t shared) {
+    const uint32_t sum = lane + shared;
+    return sum < lane ? 0xfffffff0u : sum;
+}
 
 // Workspace slot of one (batch, head, chunk). M and P blocks are 16x16 row-major
 // (row = later token t, column = earlier token s), lower-triangular block order; the
