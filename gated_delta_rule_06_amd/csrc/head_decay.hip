@@ -285,7 +285,9 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                 const float off = static_cast<float>(ldexp(static_cast<double>(factor), -static_cast<int>(n)) - e) / static_cast<float>(e);
                 if (lane == 0) {
                     sh_carry[0] = factor;
-                    sh_carry[1] = factor > 0.f ? -1.44269504f * off : 0.f;  // log2 of what the rounding took
+                    // log2 of what the rounding took. Only of a normal factor: below that range the rounding is percents of it, up to
+                    // all, and the next factor also decays what this chunk itself added. (a = 0.2, 65 tokens: +27 % in the state.)
+                    sh_carry[1] = factor >= 1.17549435e-38f ? -1.44269504f * off : 0.f;
                 }
             }
             lds_barrier();
