@@ -55,6 +55,13 @@ __device__ __forceinline__ u32x2_t buf_load8(rsrc_t r, unsigned voff, unsigned s
 __device__ __forceinline__ u32x4_t buf_load16(rsrc_t r, unsigned voff, unsigned soff) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), 0);
 }
+// 16 bytes to a buffer, with the whole offset in the lane's register: every 16-byte store through a descriptor is this one. With a
+// part of the offset in a scalar register the compiler lets the very next instruction overwrite the stored registers, and the
+// store has not read the last four lanes of each sixteen by then (float32 outputs held a following instruction's integers).
+// Stores of 8 bytes read at once.
+__device__ __forceinline__ void buf_store16(rsrc_t r, unsigned off, u32x4_t v) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, int(off), 0, 0);
+}
 __device__ __forceinline__ f32x4_t buf_load_f4(rsrc_t r, unsigned voff, unsigned soff) {
     return __builtin_bit_cast(f32x4_t, buf_load16(r, voff, soff));
 }
@@ -213,9 +220,7 @@ template <int VC> struct RowV<float, VC> {
     static __device__ __forceinline__ float get(raw v, int i) { return v[i]; }
     static __device__ __forceinline__ void store(rsrc_t r, unsigned voff, unsigned soff, f32x4_t v) {
         if constexpr (VC == 4) {
-            // The whole offset in the lane's register: with a scalar part the compiler lets the very next instruction
-            // overwrite the stored registers, before a store of 16 bytes has read its last lanes.
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, int(whole_offset(voff, soff)), 0, 0);
+            buf_store16(r, whole_offset(voff, soff), __builtin_bit_cast(u32x4_t, v));
         } else if constexpr (VC == 2) {
             const f32x2_t f = {v[0], v[1]};
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, f), r, int(voff), int(soff), 0);

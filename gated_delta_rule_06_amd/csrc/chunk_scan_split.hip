@@ -169,8 +169,7 @@ __global__ __launch_bounds__(256) void chunk_scan_split_kernel(
     auto rd_put = [&](int ci, int frag, f8 val) {
         if constexpr (SAVE) return;  // no readout: nothing to hand over
         if (col_ok)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, val), rrd, int(lo_rd),
-                                                   int(size_t(ci) * RCB + size_t(frag) * 1024), 0);
+            buf_store16(rrd, lo_rd + unsigned(size_t(ci) * RCB + size_t(frag) * 1024), __builtin_bit_cast(u32x4_t, val));
     };
 
     // ------------------------------------------------------------------------------------

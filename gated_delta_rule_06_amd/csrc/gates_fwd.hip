@@ -136,7 +136,7 @@ __global__ __launch_bounds__(256) void lowrank_gates_kernel(
                                                               4u * unsigned(G & 1)) * 4u
                                                            : 0xfffffff0u)
                                         : (t * unsigned(HD) + unsigned(16 * c + 4 * G)) * 4u;
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y), ro, int(off), 0, 0);
+                buf_store16(ro, off, __builtin_bit_cast(u32x4_t, y));
             }
         }
     };

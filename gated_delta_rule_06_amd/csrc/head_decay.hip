@@ -42,13 +42,6 @@ struct PassArgs {
     int B, T, H, nseg, seg_chunks, nchunks;
 };
 
-// 16 bytes to a buffer, with the whole offset in the lane's register. With a part of it in a scalar register the compiler lets the next
-// instruction overwrite the stored registers, and the store has not read the last four lanes of each sixteen by then (seen
-// here: float32 outputs with a following instruction's integers in them). Stores of 8 bytes read at once.
-__device__ __forceinline__ void store16(u32x4_t v, rsrc_t b, int off) {
-    __builtin_amdgcn_raw_buffer_store_b128(v, b, off, 0, 0);
-}
-
 // A tile of 64 rows of one head on its way from memory to LDS.
 template <typename T, int D, int THREADS> struct Tile {
     static constexpr int VEC = 16 / sizeof(T);
@@ -201,7 +194,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
             const rsrc_t bo = make_rsrc(go + static_cast<size_t>(t0) * so, static_cast<unsigned>(uniform(min(p.T - t0, C))) * so);
             const int off = m * so + (col0 + 4 * g) * (p.out_f32 ? 4 : ES);
             for (int tb = 0; tb < 4; ++tb) {
-                if (ES == 4 || p.out_f32) store16(u32x4_t{0, 0, 0, 0}, bo, off + 16 * tb * so);
+                if (ES == 4 || p.out_f32) buf_store16(bo, off + 16 * tb * so, u32x4_t{0, 0, 0, 0});
                 else __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{0, 0}, bo, off, 16 * tb * so, 0);
             }
             if constexpr (KEEP) {
@@ -344,7 +337,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                 const int t = 16 * tb + m, col = col0 + 4 * g;
                 if (t0 + C > end && t0 + t >= end) acc[tb] = zero4();
                 if (ES == 4 || p.out_f32) {
-                    store16(__builtin_bit_cast(u32x4_t, acc[tb]), bo, (16 * tb + m) * so + 4 * col);
+                    buf_store16(bo, (16 * tb + m) * so + 4 * col, __builtin_bit_cast(u32x4_t, acc[tb]));
                 } else {
                     u16x4_t u;
 #pragma unroll

@@ -589,8 +589,8 @@ __global__ __launch_bounds__(2 * D) void wy_state_kernel(const float *__restrict
         const f8 mine = F::cat(F::pack(S[0]), F::pack(S[1]));
         sh_S[wave][lane] = mine;
         // The chunk's start state for the readout: [value tile][channel group][64][8].
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, mine), rx, int(lane * 16),
-                                               int(xoff(ci, XS::SC_OFF + size_t((vt * NKD + wave) * 64) * 16)), 0);
+        buf_store16(rx, unsigned(lane * 16) + xoff(ci, XS::SC_OFF + size_t((vt * NKD + wave) * 64) * 16),
+                    __builtin_bit_cast(u32x4_t, mine));
         lds_barrier();
         f8 sb[NKD];
 #pragma unroll
