@@ -449,8 +449,8 @@ size_t muir_state_bytes(int B, int H, int dk, int dv);
  *   H a multiple of Hk; dk and dv each 64 or 128; T >= 0 (T == 0 copies s0, or zeros, into s_out)
  *   workspace: muir_chunk_fwd_head_decay_workspace_size(...) bytes (0 where one segment a head is used)
  *
- * bf16: o is rounded once from float32 sums whose operands (q.k times its decay, the state) are bf16 terms;
- * s_out keeps float32 accuracy. Errors as for muir_chunk_fwd, and MUIR_ERR_UNSUPPORTED for H above 2^15,
+ * bf16: o is rounded once from float32 sums whose operands (q.k times its decay, the state) are two bf16 terms each, 2^-16
+ * of them left out; s_out keeps float32 accuracy. Errors as for muir_chunk_fwd, and MUIR_ERR_UNSUPPORTED for H above 2^15,
  * B * H above 2^21 or B * (T + 64) * H above 2^31.
  */
 size_t muir_chunk_fwd_head_decay_workspace_size(int B, int T, int H, int Hk, int dk, int dv,
