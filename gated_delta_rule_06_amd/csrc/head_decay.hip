@@ -34,7 +34,7 @@ struct PassArgs {
     bool out_f32;
     float *s_out;           // state after the last token, [DX, DZ], or NULL; LOCAL: [B*H, nseg] states
     f32x2_t *dec;           // LOCAL: [B*H, nseg] decays, as a float32 and what it leaves
-    const void *w;          // KEEP: [B, T, hw, DZ], dots [B, T, H] = out . w
+    const void *w;          // KEEP: [B, T, hw, DZ], dots [B, T, H] = out . w but for the token's own z in out
     int hw;
     float *dots;
     float *anchors;         // KEEP: [B*H, groups] states, written in order and read reversed
@@ -66,7 +66,7 @@ template <typename T, int DX, int DZ, bool LOCAL, int NTP> struct PassLds {
     static constexpr int Y = 0, Z = Y + O::template tile_bytes<DX>(), X = Z + O::template tile_bytes<DZ>();
     static constexpr int P = X + (LOCAL ? 0 : O::template tile_bytes<DX>());
     static constexpr int TAIL = P + (LOCAL ? 0 : NTP * O::template tile_bytes<C>());
-    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 16 + (LOCAL ? 0 : NW * C * 4);
+    static constexpr int BYTES = TAIL + C * 8 + C * 4 * 2 + 16 + (LOCAL ? 0 : NW * C * 4 + C * 4);
 };
 
 // One wavefront owns 16 columns of the state and of the output; see head_decay.hpp for the operand order.
@@ -101,6 +101,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     float *const sh_upd = sh_out + C;                                 // decay of a token's z in the update
     float *const sh_carry = sh_upd + C;                               // decay of the state over the chunk, and what it owes the next
     float *const sh_dot = sh_carry + 4;                               // [NW][C]
+    float *const sh_diag = sh_dot + NW * C;                           // KEEP: x_i . y_i
 
     int tid = threadIdx.x;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -251,6 +252,14 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                     // Not all operands at once: next to the state and the chunk on its way there are not the registers.
                     if (ES == 2 && k0 % 64 == 32) __builtin_amdgcn_sched_barrier(0);
                 }
+                // KEEP: the diagonal is added to the outputs by itself, behind their dots. A token's own product is in q.dq and in k.dk
+                // alike; where the decay is strong it is far above what is left of their difference, and so were its roundings.
+                if constexpr (KEEP) {
+                    if (pr == ib / 2 && m >> 2 == g) {
+                        const f32x4_t own = ib & 1 ? acc[1] : acc[0];
+                        sh_diag[i] = m & 2 ? (m & 1 ? own[3] : own[2]) : (m & 1 ? own[1] : own[0]);
+                    }
+                }
                 const f32x2_t Li = sh_L[i];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -260,7 +269,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                     for (int e = 0; e < 4; ++e) {
                         const f32x2_t d = REV ? sh_L[j0 + e] - Li : Li - sh_L[j0 + e];
                         const float w = acc[u][e] * (KEEP || ES == 4 ? exp2_pair(d[0], d[1]) : exp2_f(d[0] + d[1]));
-                        v[e] = (REV ? j0 + e >= i : j0 + e <= i) ? w : 0.f;
+                        v[e] = (KEEP ? REV ? j0 + e > i : j0 + e < i : REV ? j0 + e >= i : j0 + e <= i) ? w : 0.f;
                     }
                     O::template put4<C, NTP>(lp, i, j0 / 4, v);
                 }
@@ -299,6 +308,8 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                     s8[e] = S[2 * k][e];
                     s8[4 + e] = S[2 * k + 1][e];
                 }
+                // (Loads moved across here cost the dk pass of 128/64 a tile's vector, spilled while on its way.)
+                if constexpr (KEEP && ES == 2 && DX < DZ) __builtin_amdgcn_sched_barrier(0);
                 O::template split<NTS>(s8, sf);
 #pragma unroll
                 for (int t0b = 0; t0b < 4; t0b += OSIDE) {
@@ -337,14 +348,6 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                 }
                 const int t = 16 * tb + m, col = col0 + 4 * g;
                 if (t0 + C > end && t0 + t >= end) acc[tb] = zero4();
-                if (ES == 4 || p.out_f32) {
-                    buf_store16(bo, (16 * tb + m) * so + 4 * col, __builtin_bit_cast(u32x4_t, acc[tb]));
-                } else {
-                    u16x4_t u;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16(acc[tb][e]);
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, u), bo, m * so + 2 * col, 16 * tb * so, 0);
-                }
                 if constexpr (KEEP) {
                     float dot = 0.f;
 #pragma unroll
@@ -357,6 +360,17 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
                     if (g == 0) sh_dot[wv * C + t] = dot;
+                    const f32x4_t z4 = O::template quad<DZ>(lz, t, col / 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[tb][e] = fmaf(sh_diag[t], z4[e], acc[tb][e]);
+                }
+                if (ES == 4 || p.out_f32) {
+                    buf_store16(bo, (16 * tb + m) * so + 4 * col, __builtin_bit_cast(u32x4_t, acc[tb]));
+                } else {
+                    u16x4_t u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16(acc[tb][e]);
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, u), bo, m * so + 2 * col, 16 * tb * so, 0);
                 }
             }
         }
@@ -472,11 +486,12 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs first, JoinArgs seco
     }
 }
 
-// dla of one group of ANCHOR chunks: sums of q.dq - k.dk from each token to the group's end, plus <S, A> there.
-// In 64 bits: the terms cancel where the decay is strong.
+// dla of one group of ANCHOR chunks, from the nearer of its two ends: <S, A> at its end plus the sum of q.dq - k.dk from the token on, or
+// <S, A> at its start less the sum over the tokens before. In 64 bits: the terms cancel where the decay is strong. What q.dq and k.dk
+// were rounded by adds up with the distance; a fixed decay's gradient sums it over all tokens.
 __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const float *cols, const float *edges,
                                                         const int *lens, float *dla, double *part, int T, int H,
-                                                        int groups, int parts) {
+                                                        int groups, int parts, bool zero_start) {
     __shared__ double sh[ANCHOR];
     const int grp = blockIdx.x % groups, bh = blockIdx.x / groups, b = bh / H, h = bh % H;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -487,9 +502,18 @@ __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const
     x = scan64(x);
     if (lane == 63) sh[wv] = x;
     __syncthreads();
-    for (int w = 0; w < wv; ++w) x += sh[w];
-    const float *e = edges + (static_cast<size_t>(bh) * groups + grp) * parts;
-    for (int i = 0; i < parts; ++i) x += e[i];
+    double total = 0.0;
+    for (int w = 0; w < ANCHOR; ++w) {
+        if (w < wv) x += sh[w];
+        total += sh[w];
+    }
+    // The first group's start: zero where the state there is, else its end serves all.
+    const bool from_start = static_cast<int>(threadIdx.x) >= ANCHOR * C / 2 && (grp > 0 || zero_start);
+    if (from_start) x -= total;
+    if (!from_start || grp > 0) {
+        const float *e = edges + (static_cast<size_t>(bh) * groups + grp - (from_start ? 1 : 0)) * parts;
+        for (int i = 0; i < parts; ++i) x += e[i];
+    }
     if (t >= end) x = 0.0;
     if (dla) {
         if (t < T) dla[at] = static_cast<float>(x);
@@ -499,7 +523,9 @@ __global__ __launch_bounds__(ANCHOR *C) void dla_kernel(const float *rows, const
     for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
     if (lane == 0) sh[wv] = x;
     __syncthreads();
-    if (threadIdx.x == 0) part[static_cast<size_t>(bh) * groups + grp] = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < ANCHOR; ++w) x += sh[w];
+    part[static_cast<size_t>(bh) * groups + grp] = x;
 }
 
 // A fixed decay's gradient: one wavefront per head sums its groups over the batch, in a fixed order.
@@ -712,7 +738,7 @@ hipError_t backward(const HeadDecayCall &c, const HeadDecayGrads &g, void *works
             if (err != hipSuccess) return err;
         }
         hipLaunchKernelGGL(dla_kernel, dim3(static_cast<unsigned>(groups) * BH), dim3(ANCHOR * C), 0, stream, rows, cols, edges,
-                           c.lens, c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups, DK / 16);
+                           c.lens, c.a_fixed ? nullptr : g.dla, part, c.T, c.H, groups, DK / 16, c.s0 == nullptr);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }

@@ -61,6 +61,11 @@ template <> struct Op<bf16_t> {
     template <int D> static __device__ __forceinline__ void put16(unsigned char *t, int r, int c, u32x4_t v) {
         *reinterpret_cast<u32x4_t *>(t + at<D>(r, 2 * c)) = v;
     }
+    // Four elements of row r from column 4 c on.
+    template <int D> static __device__ __forceinline__ f32x4_t quad(const unsigned char *t, int r, int c) {
+        const u16x4_t u = *reinterpret_cast<const u16x4_t *>(t + at<D>(r, c));
+        return f32x4_t{bf16_to_f32(u[0]), bf16_to_f32(u[1]), bf16_to_f32(u[2]), bf16_to_f32(u[3])};
+    }
     static __device__ __forceinline__ void floats(frag f, float (&x)[8]) {
         const u16x8_t u = __builtin_bit_cast(u16x8_t, f);
 #pragma unroll
@@ -126,6 +131,9 @@ template <> struct Op<float> {
     }
     template <int D> static __device__ __forceinline__ void put16(unsigned char *t, int r, int c, u32x4_t v) {
         *reinterpret_cast<u32x4_t *>(const_cast<float *>(elem<D>(t, r, 4 * c))) = v;
+    }
+    template <int D> static __device__ __forceinline__ f32x4_t quad(const unsigned char *t, int r, int c) {
+        return *reinterpret_cast<const f32x4_t *>(elem<D>(t, r, 4 * c));
     }
     static __device__ __forceinline__ void floats(const frag &f, float (&x)[8]) {
 #pragma unroll
