@@ -193,8 +193,8 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// exp2(hi + lo) to the last bit or so: the sum as one float32 would be off by 2^-24 of itself, which a fixed decay repeats in
-// every chunk and the sum of its gradient over all tokens shows.
+// exp2(hi + lo) to the last bit or so, for the decays of a whole chunk, which go into states. Those between two tokens of a chunk do
+// without: their last bits show in no output (float32 outputs and gradients are off by the same 2e-7 to 3e-7 with and without).
 __device__ __forceinline__ float exp2_pair(float hi, float lo) {
     const float n = rintf(hi);
     return __builtin_amdgcn_ldexpf(exp2_f((hi - n) + lo), static_cast<int>(n));
