@@ -646,7 +646,8 @@ def chunk_fwd_head_decay(q, k, v, a, s0=None, *, lens=None, o=None, s_out=None,
     float32 or None; lens [B] int32 or None: the tokens of each sequence, those behind
     are not read and their rows of o are zeros. Returns (o, s_out): o [B,T,H,dv] and the
     state after each sequence's last token (None with ``return_state=False``). ``s_out``
-    may be ``s0`` itself.
+    may be ``s0`` itself. A NaN or infinity in a token can reach every output of its chunk of
+    64 tokens, earlier ones too.
     """
     import torch
     sizes, per_token, code, i = _head_decay_inputs(q, k, v, a, s0, lens)

@@ -450,7 +450,8 @@ size_t muir_state_bytes(int B, int H, int dk, int dv);
  *   workspace: muir_chunk_fwd_head_decay_workspace_size(...) bytes (0 where one segment a head is used)
  *
  * bf16: o is rounded once from float32 sums whose operands (q.k times its decay, the state) are two bf16 terms each, 2^-16
- * of them left out; s_out keeps float32 accuracy. Errors as for muir_chunk_fwd, and MUIR_ERR_UNSUPPORTED for H above 2^15,
+ * of them left out; s_out keeps float32 accuracy. A NaN or infinity in a token can reach every output of its chunk of 64 tokens,
+ * earlier ones too (as 0 times it), and gradients likewise. Errors as for muir_chunk_fwd, and MUIR_ERR_UNSUPPORTED for H above 2^15,
  * B * H above 2^21 or B * (T + 64) * H above 2^31.
  */
 size_t muir_chunk_fwd_head_decay_workspace_size(int B, int T, int H, int Hk, int dk, int dv,
