@@ -91,6 +91,7 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
     // LOCAL walks against the order of the pass that follows it, which then finds what was read last in the caches.
     constexpr bool DOWN = REV != LOCAL;
     constexpr int SIDE = KEEP ? 2 : 4;  // sums that are added to in turn, so that a product does not wait for the one before
+    constexpr int PAIRS = ES == 4 ? 2 : 1;  // blocks of 32 tokens that the state takes at once
     constexpr int OSIDE = NTS > 1 ? 2 : 4;  // in the products with the state, whose terms take registers too
     extern __shared__ __align__(16) unsigned char smem[];
     unsigned char *const ly = smem + L::Y, *const lz = smem + L::Z, *const lx = smem + L::X, *const lp = smem + L::P;
@@ -276,9 +277,9 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
             }
             // A wavefront with less to do here makes the state's decay over the chunk. A float32 near exp2(L) is off by up to
             // 2^-24, and a fixed decay's by the same amount in every chunk, which adds up in a state that lives long. So what a chunk's
-            // factor leaves of L goes into the next one's, and the product of the factors stays within one rounding. Float32 state, H16 d64,
-            // half-life 1e5 tokens: 3.8e-6 off after 262144 tokens against 6.8e-6, 1.38e-6 against 1.55e-6 after 32768, nothing below
-            // 4096 and nothing in time.
+            // factor leaves of L goes into the next one's, and the product of the factors stays within one rounding. Float32 state, H16 d64: 5.0e-7 off
+            // after 262144 tokens of half-life 1e5 against 5.6e-6 without, 2.4e-7 against 7.6e-7 after 32768, 1.9e-7 against 3.9e-7 there at
+            // half-life 1000; nothing in time.
             if (wv == (REV ? NW / 8 * 4 + NW / 4 % 2 * 3 : NW / 8)) {
                 const float rest = Lc[1] + sh_carry[1], factor = exp2_pair(Lc[0], rest);
                 const float n = rintf(Lc[0]);
@@ -377,34 +378,51 @@ template <typename K> __device__ __forceinline__ void pass(const PassArgs &p, in
             }
         }
 
-        // The state: decayed over the chunk, then y^T (decayed z).
-        if constexpr (!LOCAL) {
-            const float carry = *sh_carry;
+        // The state: decayed over the chunk, plus y^T (decayed z). In float32 the chunk's own sum is made first, so that the state is
+        // rounded once a chunk and not with each product of four tokens: 3.8e-6 -> 5e-7 off after 262144 tokens of half-life 1e5, in the same
+        // time. bf16 adds straight to the state, three times for 32 tokens: the same there took 748 -> 976 us for the backward of
+        // B8 T4096 H16 d128 (registers), where ds0 is 4.5e-7 off.
+        const float carry = LOCAL ? 1.f : *sh_carry;
+        if constexpr (!LOCAL && ES == 2) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) S[rt] *= carry;
         }
 #pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
-            frag zs[NTU];
-            const f32x4_t ulo = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 4 * g);
-            const f32x4_t uhi = *reinterpret_cast<const f32x4_t *>(sh_upd + 32 * pr + 16 + 4 * g);
-            float z8[8];
-            O::floats(zf[pr], z8);
+        for (int p0 = 0; p0 < 2; p0 += PAIRS) {
+            frag zs[PAIRS][NTU];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z8[e] *= ulo[e];
-                z8[4 + e] *= uhi[e];
+            for (int u = 0; u < PAIRS; ++u) {
+                const int j0 = 32 * (p0 + u) + 4 * g;
+                const f32x4_t ulo = *reinterpret_cast<const f32x4_t *>(sh_upd + j0);
+                const f32x4_t uhi = *reinterpret_cast<const f32x4_t *>(sh_upd + j0 + 16);
+                float z8[8];
+                O::floats(zf[p0 + u], z8);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z8[e] *= ulo[e];
+                    z8[4 + e] *= uhi[e];
+                }
+                O::template split<NTU>(z8, zs[u]);
             }
-            O::template split<NTU>(z8, zs);
 #pragma unroll
             for (int r0 = 0; r0 < RT; r0 += SIDE) {
-                frag fy[SIDE];
+                f32x4_t sum[SIDE];
 #pragma unroll
-                for (int r = 0; r < SIDE; ++r) fy[r] = O::template col<DX>(ly, 32 * pr, 16 * (r0 + r), lane);
+                for (int r = 0; r < SIDE; ++r) sum[r] = ES == 2 ? S[r0 + r] : zero4();
 #pragma unroll
-                for (int n = NTU - 1; n >= 0; --n)
+                for (int u = 0; u < PAIRS; ++u) {
+                    frag fy[SIDE];
 #pragma unroll
-                    for (int r = 0; r < SIDE; ++r) S[r0 + r] = O::mma(fy[r], zs[n], S[r0 + r]);
+                    for (int r = 0; r < SIDE; ++r) fy[r] = O::template col<DX>(ly, 32 * (p0 + u), 16 * (r0 + r), lane);
+#pragma unroll
+                    for (int n = NTU - 1; n >= 0; --n)
+#pragma unroll
+                        for (int r = 0; r < SIDE; ++r) sum[r] = O::mma(fy[r], zs[u][n], sum[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < SIDE; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[r0 + r][e] = ES == 2 ? sum[r][e] : fmaf(carry, S[r0 + r][e], sum[r][e]);
             }
         }
         lds_barrier();

@@ -6,6 +6,7 @@ of the float32 sums (kf, test_gpu_head_decay)."""
 import pytest
 import torch
 
+import gated_delta_rule_06_amd as muir
 from test_gpu_head_decay import (CASES, F, U, absolute, backward, backward64, forward, forward64, ids, inputs, kf, within)
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,24 @@ def test_decay_gradients_keep_their_relative_accuracy(device, a, B, T, H, Hk, dk
         torch.cuda.synchronize()
         want = backward64(x)["la"]
         within(g["la"], want, dla_bound(x) + U[torch.float32] * want.abs(), f"dla, {'fixed' if fixed else 'per token'}")
+
+
+def test_a_long_float32_state_is_rounded_once_a_chunk(device):
+    """512 chunks of a state that hardly decays, one walk to a head. Each chunk rounds the state twice at most (its decay, and its
+    sum with the chunk's own), by F / sqrt(3) of it in the mean square, and it grows as the root of the chunks: together
+    F sqrt(512 / 3) in the 2-norm; a chunk's own sum of 64 products adds F sqrt(64 / 3)."""
+    B, T, H, d = 4, 32768, 64, 64
+    g = torch.Generator(device=device).manual_seed(3)
+    q, k, v = (torch.randn(B, T, H, d, device=device, generator=g) for _ in range(3))
+    a = torch.exp2(-1e-5 * (1 + torch.arange(H, device=device) / H))
+    assert muir.chunk_fwd_head_decay_workspace_size(B, T, H, H, d, d, muir.MUIR_F32) == 0
+    _, s = muir.chunk_fwd_head_decay(q, k, v, a)
+    want = torch.zeros(B, H, d, d, dtype=torch.float64, device=device)
+    log = torch.log2(a.double())[None, :, None]
+    to_end = torch.exp2(log * (63 - torch.arange(64, device=device)))
+    for c in range(0, T, 64):
+        kc = k[:, c:c + 64].double().permute(0, 2, 3, 1).contiguous() * to_end[:, :, None]
+        want = want * torch.exp2(64 * log)[..., None] + torch.matmul(kc, v[:, c:c + 64].double().transpose(1, 2).contiguous())
+    off = ((s.double() - want).norm() / want.norm()).item()
+    print(f"  state off by {off:.3e}", flush=True)
+    assert off <= F * ((512 / 3) ** 0.5 + (64 / 3) ** 0.5)
