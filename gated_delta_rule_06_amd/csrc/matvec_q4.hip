@@ -5,7 +5,8 @@
 // numbers 16 + nib (exact, a shift and a mask-or for two of them: the nibble moves to mantissa bits 3..6 of
 // 16.0), and a group's sum is finished in float32 as scale (sum x (16 + nib) - (16 + zero) sum x). The second
 // sum is a product with ones, shared by the NT weight tiles of a wavefront. float32 x goes in as three bf16
-// terms (to its last bit or two).
+// terms (to its last bit or two), and there the nibbles become nib - 8 (sign extension, a conversion and half a packing each): the
+// terms of 16 + nib are up to five times as large as what is left of them, and float32 outputs showed their roundings.
 //
 // A workgroup walks K in tiles of 1024 columns, 128 to each of eight wavefronts (or pairs of them, half of the weight rows
 // each), whose sums meet in LDS in a fixed order. A tile's weights, x and scales come as whole cache lines through LDS, the
@@ -37,6 +38,16 @@ __device__ __forceinline__ bf16x8_t nibbles(uint32_t w, uint32_t base) {
     constexpr uint32_t M = 0x00780078u;
     const uint4 u{((w << 3) & M) | base, ((w >> 1) & M) | base, ((w >> 5) & M) | base, ((w >> 9) & M) | base};
     return __builtin_bit_cast(bf16x8_t, u);
+}
+
+// The same as nib - 8.
+__device__ __forceinline__ bf16x8_t signed_nibbles(uint32_t w) {
+    constexpr int ORDER[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+    w ^= 0x88888888u;  // two's complement of nib - 8
+    bf16x8_t f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = static_cast<__bf16>(static_cast<float>(static_cast<int>(w << (28 - 4 * ORDER[j])) >> 28));
+    return f;
 }
 
 // x of eight columns in that order, as NX bf16 terms.
@@ -74,6 +85,8 @@ __global__ __launch_bounds__(WAVES *NH * 64) void matvec_q4_kernel(const XT *__r
                                                                XT *__restrict__ y, int M, int N, int K) {
     constexpr int NX = sizeof(XT) == 2 ? 1 : 3;
     constexpr bool XLDS = NX == 1;
+    constexpr float OFFSET = NX == 1 ? 16.f : -8.f;  // what a nibble's bf16 number is more than it
+    constexpr bool XSUM = NX == 1 || ZERO;           // without it nib - 8 is the weight
     constexpr int PER = GROUP / 32, NG = 4 / PER;  // products of a group, groups of a step
     constexpr int THREADS = WAVES * NH * 64, KT = WAVES * 128, NW = NT / NH;  // a wavefront has NW of the tiles of 16 rows
     constexpr int WC = KT / 32, XC = KT / 8;             // 16-byte chunks of a row of the tile
@@ -162,8 +175,8 @@ __global__ __launch_bounds__(WAVES *NH * 64) void matvec_q4_kernel(const XT *__r
 #pragma unroll
         for (int j = 0; j < NSL; ++j) {
             const int i = tid + THREADS * j;
-            float2 v{to_f32(f.sc[j]), 24.f};
-            if constexpr (ZERO) v.y = 16.f + to_f32(f.zp[j]);
+            float2 v{to_f32(f.sc[j]), OFFSET + 8.f};
+            if constexpr (ZERO) v.y = OFFSET + to_f32(f.zp[j]);
             if (NSCALE % THREADS == 0 || i < NSCALE) ls[i / SC * LS + i % SC] = v;
         }
         if (t + 1 < tiles) fetch(f, t + 1);
@@ -198,11 +211,12 @@ __global__ __launch_bounds__(WAVES *NH * 64) void matvec_q4_kernel(const XT *__r
             for (int e = 0; e < PER; ++e) {
                 const int u = q * PER + e;
 #pragma unroll
-                for (int c = NX - 1; c >= 0; --c) xs = Mma<bf16_t>::mma(fx[u].f[c], ones, xs);
+                for (int c = NX - 1; c >= 0; --c)
+                    if constexpr (XSUM) xs = Mma<bf16_t>::mma(fx[u].f[c], ones, xs);
 #pragma unroll
                 for (int n = 0; n < NW; ++n) {
                     const uint32_t dw[4] = {d[n].x, d[n].y, d[n].z, d[n].w};
-                    const bf16x8_t fw = nibbles(dw[u], base);
+                    const bf16x8_t fw = NX == 1 ? nibbles(dw[u], base) : signed_nibbles(dw[u]);
 #pragma unroll
                     for (int c = NX - 1; c >= 0; --c) acc[n] = Mma<bf16_t>::mma(fx[u].f[c], fw, acc[n]);
                 }
@@ -211,7 +225,7 @@ __global__ __launch_bounds__(WAVES *NH * 64) void matvec_q4_kernel(const XT *__r
             for (int n = 0; n < NW; ++n) {
                 const float2 v = ls[(16 * (nh * NW + n) + m) * LS + wv * NG + q];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[n][i] = fmaf(v.x, fmaf(-v.y, xs[i], acc[n][i]), sum[n][i]);
+                for (int i = 0; i < 4; ++i) sum[n][i] = fmaf(v.x, XSUM ? fmaf(-v.y, xs[i], acc[n][i]) : acc[n][i], sum[n][i]);
             }
         }
     };

@@ -553,7 +553,7 @@ muir_status_t muir_rms_norm_8bit(
  *   group  32, 64 or 128; K a multiple of it
  *
  * Weights are exact; sums are float32 (float32 x is three bf16 terms, exact to its last bit or two). An
- * infinity in x makes that row of y NaN or infinite.
+ * infinity in x, or a float32 beyond the largest bf16, makes that row of y NaN or infinite.
  */
 muir_status_t muir_matvec_q4(
     const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K,
