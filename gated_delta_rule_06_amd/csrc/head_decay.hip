@@ -6,11 +6,11 @@
 //   dla_kernel, *_sum       the decay's gradient from the row sums of two passes; sums over shared heads
 // Where B * H workgroups fill the card there is one segment per head and the pass is the only launch of a forward.
 //
-// Measured in bf16, 128/128, 8192 chunks (fastest of 20, us): forward of B1 T32768 H16 61.5 local pass, 21 join, 132 pass; backward of
-// B8 T4096 H16 96 for both local passes, 19 both joins, 214 dq, 218 dk, 133 dv, 11 the decay's gradient. The local pass reads k and v
-// at 4.4 TB/s; in the others instructions issue in up to 76 to 84 % of the cycles, vector ones in half of them, and the matrix cores
-// are busy for 29 to 34 %. dq and dk keep three bf16 terms where the forward and dv keep two and one: 840 and 853 vector instructions
-// a wavefront and chunk against 498 and 497.
+// Measured in bf16, 128/128, 8192 chunks (fastest of 20, us): forward of B1 T32768 H16 65 local pass, 17 join, 149 pass; backward of
+// B8 T4096 H16 97 for both local passes, 18 both joins, 237 dq, 245 dk, 150 dv, 11 the decay's gradient. The local pass reads k and v
+// at 4.1 TB/s; in the others instructions issue in up to 72 to 86 % of the cycles, vector ones in 49 to 57 %, and the matrix cores
+// are busy for 26 to 37 %. dq and dk keep three bf16 terms where the forward and dv keep two, and write and read the states between groups
+// (268 MB each): 877 and 906 vector instructions a wavefront and chunk against 590.
 #include <algorithm>
 
 #include "head_decay.hpp"

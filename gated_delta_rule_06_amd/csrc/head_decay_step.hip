@@ -1,11 +1,11 @@
 // One token of linear attention with one decay per head: S <- a S + k v^T, o = S^T q, in place.
 //
 // The state is read and written once (8 dk dv bytes a head) and that is the whole cost. Columns are
-// independent, so a workgroup takes COLS of a head's dv columns: all of them where the heads alone fill the
-// card, a quarter where they do not. A thread has four columns (16-byte loads) of four rows; the output sums over
+// independent, so a workgroup takes COLS of a head's dv columns: all of them where there is a head for each compute
+// unit, 32 where there is not. A thread has four columns (16-byte loads) of four rows; the output sums over
 // rows first inside each wavefront, then over the wavefronts through LDS, in a fixed order. State loads and
-// stores are non-temporal: the state is not touched again before the next step. B256 H16 Hk4 128/128 bf16: 83 us for 541 MB, 6.5 TB/s;
-// B1 H16: 2.7 us.
+// stores are non-temporal: the state is not touched again before the next step. B256 H16 Hk4 128/128 bf16: 83 us for 541 MB, 6.5 TB/s,
+// on one state (some of its 268 MB may stay in the last-level cache from call to call); B1 H16: 2.8 us.
 #include "common.hpp"
 #include "mfma.hpp"
 #include "op_kernels.hpp"
@@ -75,7 +75,7 @@ hipError_t launch_cols(const void *q, const void *k, const void *v, const float 
 template <typename QT, int DK, int DV>
 hipError_t launch_sized(const void *q, const void *k, const void *v, const float *a, bool a_fixed, float *state,
                         void *o, int B, int H, int Hk, hipStream_t stream) {
-    // One workgroup per compute unit is enough to fill it (DK * DV / 16 threads); below that, split the columns.
+    // A workgroup of a whole head is DK * DV / 16 threads, 256 to 1024; with fewer heads than compute units, split the columns.
     if (static_cast<long long>(B) * H >= 256)
         return launch_cols<QT, DK, DV, DV>(q, k, v, a, a_fixed, state, o, B, H, Hk, stream);
     return launch_cols<QT, DK, DV, 32>(q, k, v, a, a_fixed, state, o, B, H, Hk, stream);

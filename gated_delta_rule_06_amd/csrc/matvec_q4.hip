@@ -11,8 +11,9 @@
 // A workgroup walks K in tiles of 1024 columns, 128 to each of eight wavefronts (or pairs of them, half of the weight rows
 // each), whose sums meet in LDS in a fixed order. A tile's weights, x and scales come as whole cache lines through LDS, the
 // next tile's in flight. Reading them straight into the lanes that multiply them (16 rows, 64 bytes each, the scales one by
-// one) took 51 us at M = 16, N = 16384, K = 8192, G = 64 where this takes 21 (fastest of 20 calls, 3.4 TB/s; a plain sum over memory reads 3.9 on
-// this card): the vector cache looks up every row of a load on its own. Fetching two or three tiles ahead changed nothing.
+// one) took 2.5 times as long at M = 16, N = 16384, K = 8192, G = 64 with zeros: the vector cache looks up every row of a load on its own.
+// Now 23.1 us a kernel there (3.1 TB/s) over eight sets of weights in turn, which no cache holds, and 19.1 on one set. Fetching two or three
+// tiles ahead changed nothing. float32 rows take 55.6 us: their x is read in the step that uses it, by each wavefront.
 // A lane takes 16 bytes, 32 weights of one row, from
 // LDS, and the four lanes of a row exchange them (4x4 transpose in registers) so that each product's contraction
 // is 32 consecutive columns.
@@ -275,10 +276,10 @@ template <typename XT, typename ST>
 hipError_t pick(const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K, int group,
                 hipStream_t s) {
     // As many weight rows to a workgroup as leave one workgroup for each of the 256 compute units: x is read and unpacked
-    // once for them all. At M = 1 (us, for 16, 32 and 64 rows): N = 2048, K = 2048: 3.8, 4.4, 5.3; N = 8192, K = 2048:
-    // 6.6, 4.8, 5.7; N = 16384, K = 8192: 34.7, 24.7, 19.9; M = 64, N = K = 4096 (four times the workgroups): 21.7, 13.9, 9.7.
-    // Sixteen wavefronts, half of the rows each, against eight with all of them: 23.3 and 24.3 us at M = 16, N = 16384, K = 8192;
-    // 19.9 and 21.9 at M = 1.
+    // once for them all. us a kernel for 16, 32 and 64 rows (bf16, eight sets of weights in turn): M = 1, N = 2048, K = 2048: 3.8, 4.4, 5.6;
+    // N = 8192, K = 2048: 6.8, 5.1, 5.9; N = 16384, K = 8192: 34.4, 23.7, 19.9; M = 64, N = K = 4096 (four times the workgroups): 22.0,
+    // 13.7, 10.1. Sixteen wavefronts, half of the rows each, against eight with all of them: 23.1 and 23.9 at M = 16, N = 16384, K = 8192,
+    // 19.8 and 21.6 at M = 1; float32 rows lose by it, 55.6 and 49.3.
     const long long work = static_cast<long long>(N) * ((M + 15) / 16);
     if (work >= 256 * 64) return go<XT, ST, 4, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);
     if (work >= 256 * 32) return go<XT, ST, 2, 2, 8>(x, w, scale, zero, y, M, N, K, group, s);

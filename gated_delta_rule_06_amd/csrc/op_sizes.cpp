@@ -5,8 +5,9 @@
 namespace muir {
 
 int head_decay_segments(int B, int T, int H, bool bf16) {
-    // As many workgroups as run at once (two to a compute unit in bf16, one in float32), of at least two
-    // chunks each: a segment costs a second reading of its keys and values and a state written and read.
+    // 512 workgroups in bf16 and 256 in float32, of at least two chunks each: a segment costs a second reading of its keys and
+    // values and a state written and read. At dk = dv = 128 that many run at once (LDS: two to a compute unit, one); narrower
+    // heads admit more, which the rule does not use.
     const long long heads = static_cast<long long>(B) * H, room = bf16 ? 512 : 256;
     const int n = hd::chunks_of(T);
     const int want = static_cast<int>(std::min<long long>(room / std::min(heads, room), n / 2));
