@@ -1,6 +1,7 @@
-"""Linear attention with one decay per head: bf16 outputs as exact as their one rounding.
+"""Linear attention with one decay per head: bf16 outputs as exact as their one rounding, decay gradients that keep their relative
+accuracy, float32 states that are rounded once a chunk.
 
-Beside that rounding (U of the output) the operands of the last products are two bf16 terms each, the decayed products and
+The outputs: beside that rounding (U of the output) the operands of the last products are two bf16 terms each, the decayed products and
 the state alike: the first term leaves at most U of a value and the second U of that, so U * U of each part's magnitudes, on top
 of the float32 sums (kf, test_gpu_head_decay)."""
 import pytest
