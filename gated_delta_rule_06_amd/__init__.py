@@ -24,6 +24,8 @@ __all__ = [
     "chunk_fwd_head_decay", "chunk_fwd_head_decay_workspace_size", "chunk_bwd_head_decay",
     "chunk_bwd_head_decay_workspace_size", "HEAD_DECAY_GRADS", "decode_step_head_decay",
     "rms_norm", "rms_norm_bwd", "rms_norm_bwd_workspace_size", "rms_norm_8bit", "matvec_q4",
+    "attention_fwd", "attention_bwd", "attention_bwd_workspace_size", "ATTENTION_GRADS", "cache_append",
+    "decode_step_attention", "decode_step_attention_workspace_size",
     "status_string", "last_error", "version", "MUIR_F32", "MUIR_BF16", "STATUS",
 ]
 
@@ -119,6 +121,18 @@ def lib():
         L.muir_rms_norm_8bit.restype = i
         L.muir_matvec_q4.argtypes = [vp] * 5 + [i] * 6 + [vp]
         L.muir_matvec_q4.restype = i
+        L.muir_attention_fwd.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp]
+        L.muir_attention_fwd.restype = i
+        L.muir_attention_bwd_workspace_size.argtypes = [i] * 6
+        L.muir_attention_bwd_workspace_size.restype = sz
+        L.muir_attention_bwd.argtypes = [vp] * 11 + [i] * 6 + [f, i, vp, sz, vp]
+        L.muir_attention_bwd.restype = i
+        L.muir_cache_append.argtypes = [vp] * 8 + [i] * 8 + [vp]
+        L.muir_cache_append.restype = i
+        L.muir_decode_step_attention_workspace_size.argtypes = [i] * 7
+        L.muir_decode_step_attention_workspace_size.restype = sz
+        L.muir_decode_step_attention.argtypes = [vp] * 8 + [i] * 8 + [f, i, vp, sz, vp]
+        L.muir_decode_step_attention.restype = i
         L.muir_status_string.argtypes = [i]
         L.muir_status_string.restype = ctypes.c_char_p
         L.muir_last_error.argtypes = []
@@ -860,3 +874,171 @@ def matvec_q4(x, w, scale, zero=None, *, group: int = 128, y=None):
     _call(lib().muir_matvec_q4, i, x.data_ptr(), w.data_ptr(), scale.data_ptr(), _at(zero),
           y.data_ptr(), x.numel() // K if K else 0, N, K, group, code, scode)
     return y
+
+
+def _sequences(x, name, offsets, lens, i):
+    """(rows N, sequences S) of [B, T, heads, d] or packed [N, heads, d] rows."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a torch.Tensor [B, T, heads, d], or [N, heads, d] with offsets")
+    if x.dim() == 4:
+        if offsets is not None:
+            raise ValueError("offsets go with packed rows [N, heads, d]")
+        S, N = x.shape[0], x.shape[0] * x.shape[1]
+    else:
+        if offsets is None:
+            raise ValueError("packed rows [N, heads, d] need offsets")
+        _rank(offsets, "offsets", 1)
+        S, N = offsets.shape[0] - 1, x.shape[0]
+        _is(offsets, "offsets", torch.int32, (S + 1,), i)
+    if lens is not None:
+        _is(lens, "lens", torch.int32, (S,), i)
+    return N, S
+
+
+def _attention_inputs(q, k, v, offsets, lens, window, scale):
+    i = q.get_device() if hasattr(q, "get_device") else -1
+    N, S = _sequences(q, "q", offsets, lens, i)
+    _rank(k, "k", q.dim())
+    H, d = q.shape[-2:]
+    kshape = q.shape[:-2] + (k.shape[-2], d)
+    _is(q, "q", q.dtype, q.shape, i)
+    _is(k, "k", q.dtype, kshape, i)
+    _is(v, "v", q.dtype, kshape, i)
+    return (N, S, H, kshape[-2], d), int(window), d ** -0.5 if scale is None else float(scale), _dtype_code(q), i
+
+
+def attention_fwd(q, k, v, offsets=None, *, lens=None, window: int = 0, scale=None, o=None, lse=None):
+    """Causal softmax attention over whole prompts (``muir_attention_fwd``): a token sees itself and
+    the tokens before it in its sequence, all of them (``window=0``) or the last ``window``.
+
+    q [B,T,H,d] and k, v [B,T,Hk,d], each key head shared by H / Hk query heads, with ``lens``
+    [B] int32 or None, the tokens of each sequence; or packed rows q [N,H,d], k, v [N,Hk,d] with
+    ``offsets`` [S + 1] int32, the first row of each sequence and the end of the last. float32 or
+    bfloat16, d 64 or 128; ``scale`` defaults to d ** -0.5. Returns (o, lse): o like q, and the
+    logarithm of each row's sum of exponentials, float32 [..., H], which :func:`attention_bwd`
+    takes. Rows that are no token have o = 0 and lse = -infinity. A NaN or infinity in a token's v
+    can reach the o of up to 127 tokens before it.
+    """
+    import torch
+    sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _is(o, "o", q.dtype, q.shape, i)
+    lse = _out(lse, "lse", torch.float32, q.shape[:-1], q)
+    _call(lib().muir_attention_fwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(offsets),
+          _at(lens), o.data_ptr(), lse.data_ptr(), *sizes, window, scale, code)
+    return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def attention_bwd_workspace_size(N: int, S: int, H: int, Hk: int, d: int, dtype_code: int) -> int:
+    return int(lib().muir_attention_bwd_workspace_size(N, S, H, Hk, d, dtype_code))
+
+
+ATTENTION_GRADS = ("q", "k", "v")
+
+
+def attention_bwd(q, k, v, o, lse, offsets=None, *, do, lens=None, window: int = 0, scale=None,
+                  workspace=None, out=None):
+    """Backward pass of :func:`attention_fwd` (``muir_attention_bwd``).
+
+    Inputs as for the forward, its o and lse, and ``do`` (dL/do, like q). Returns a dict keyed by
+    ``ATTENTION_GRADS``, shaped and typed as the inputs (shared heads summed); rows that are no
+    token have gradients 0. ``out`` may hold pre-allocated tensors under those keys.
+    """
+    import torch
+    sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)
+    _is(o, "o", q.dtype, q.shape, i)
+    _is(do, "do", q.dtype, q.shape, i)
+    _is(lse, "lse", torch.float32, q.shape[:-1], i)
+    out = dict(out) if out else {}
+    for n, x in (("q", q), ("k", k), ("v", v)):
+        out[n] = _out(out.get(n), "d" + n, x.dtype, x.shape, x)
+    workspace, size = _workspace(workspace, attention_bwd_workspace_size(*sizes, code), q)
+    _call(lib().muir_attention_bwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+          lse.data_ptr(), _at(offsets), _at(lens), do.data_ptr(),
+          *[out[n].data_ptr() for n in ATTENTION_GRADS], *sizes, window, scale, code,
+          _at(workspace), size)
+    return out
+
+
+def _cache_inputs(k_cache, v_cache, table, B, Hk, d, dtype, i):
+    import torch
+    _rank(k_cache, "k_cache", 4)
+    _rank(table, "table", 2)
+    pages, page, width = k_cache.shape[0], k_cache.shape[2], table.shape[1]
+    _is(k_cache, "k_cache", dtype, (pages, Hk, page, d), i)
+    _is(v_cache, "v_cache", dtype, (pages, Hk, page, d), i)
+    _is(table, "table", torch.int32, (B, width), i)
+    return pages, page, width
+
+
+def cache_append(k, v, k_cache, v_cache, table, offsets=None, *, lens=None, start=None) -> None:
+    """Keys and values of prompts into a paged cache (``muir_cache_append``), in place.
+
+    k, v [B,T,Hk,d] with ``lens``, or packed [N,Hk,d] with ``offsets``, as for
+    :func:`attention_fwd`; k_cache, v_cache [pages,Hk,page,d] in their dtype, page 16, 32, 64, 128
+    or 256; table [B,width] int32: row p % page of page ``table[s][p // page]`` holds token p of
+    sequence s; ``start`` [B] int32 or None (0): the place of each sequence's first token. Tokens
+    whose place lies behind the table, or where the table has no page (an entry outside
+    0..pages - 1), are left out.
+    """
+    import torch
+    i = k.get_device() if hasattr(k, "get_device") else -1
+    N, S = _sequences(k, "k", offsets, lens, i)
+    Hk, d = k.shape[-2:]
+    _is(k, "k", k.dtype, k.shape, i)
+    _is(v, "v", k.dtype, k.shape, i)
+    code = _dtype_code(k)
+    pages, page, width = _cache_inputs(k_cache, v_cache, table, S, Hk, d, k.dtype, i)
+    if start is not None:
+        _is(start, "start", torch.int32, (S,), i)
+    _call(lib().muir_cache_append, i, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), table.data_ptr(), _at(offsets), _at(lens), _at(start), N, S, Hk, d,
+          pages, page, width, code)
+
+
+@functools.lru_cache(maxsize=256)
+def decode_step_attention_workspace_size(B: int, H: int, Hk: int, d: int, page: int, width: int,
+                                         dtype_code: int) -> int:
+    return int(lib().muir_decode_step_attention_workspace_size(B, H, Hk, d, page, width, dtype_code))
+
+
+def decode_step_attention(q, k, v, k_cache, v_cache, table, lens, *, window: int = 0, scale=None,
+                          o=None, workspace=None):
+    """One new token of each sequence (``muir_decode_step_attention``): its key and value go into the
+    paged cache, in place, and its query attends to what the cache then holds, all of it
+    (``window=0``) or the last ``window`` tokens.
+
+    q [B,H,d]; k, v [B,Hk,d], or both None to append nothing; the cache and table [B,width] as for
+    :func:`cache_append`; lens [B] int32, the tokens in the cache before the call (not changed by
+    it). Returns o [B,H,d]. A sequence with a negative length, or without room in its table, takes
+    no part: its o is 0.
+    """
+    import torch
+    _rank(q, "q", 3)
+    _rank(k_cache, "k_cache", 4)
+    B, H, d = q.shape
+    Hk, i = k_cache.shape[1], q.get_device()
+    _is(q, "q", q.dtype, (B, H, d), i)
+    code = _dtype_code(q)
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    if k is not None:
+        _is(k, "k", q.dtype, (B, Hk, d), i)
+        _is(v, "v", q.dtype, (B, Hk, d), i)
+    pages, page, width = _cache_inputs(k_cache, v_cache, table, B, Hk, d, q.dtype, i)
+    _is(lens, "lens", torch.int32, (B,), i)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _is(o, "o", q.dtype, (B, H, d), i)
+    workspace, size = _workspace(
+        workspace, decode_step_attention_workspace_size(B, H, Hk, d, page, width, code), q)
+    _call(lib().muir_decode_step_attention, i, q.data_ptr(), _at(k), _at(v), k_cache.data_ptr(),
+          v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), o.data_ptr(), B, H, Hk, d, pages,
+          page, width, int(window), d ** -0.5 if scale is None else float(scale), code,
+          _at(workspace), size)
+    return o

@@ -19,15 +19,19 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuir.so")
 SOURCES = ["api.cpp", "sizes.cpp", "decode.hip", "chunk_fwd.hip", "chunk_bwd.hip", "wy_fwd.hip", "gates_fwd.hip",
            "noalloc.hip", "chunk_scan_split.hip", "op_api.cpp", "op_sizes.cpp", "head_decay.hip",
-           "head_decay_step.hip", "rms_norm.hip", "matvec_q4.hip"]
+           "head_decay_step.hip", "rms_norm.hip", "matvec_q4.hip", "attention_api.cpp", "attention_sizes.cpp",
+           "attention.hip", "attention_bwd.hip", "attention_step.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are kept out of every kernel. MFMA accumulators are kept
 # in ordinary VGPRs: the scan updates its fp32 state accumulators with vector
 # instructions between matrix-core products, and in AGPRs every such update costs a copy
 # out and back.
-HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-             "-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+# The attention backward's sums are touched by nothing but products until the end, and with them a wavefront needs more
+# than the 256 ordinary registers: there the compiler may choose AGPRs.
+AGPR_SOURCES = ("attention_bwd.hip",)
 
 
 def hipcc() -> str:
@@ -57,7 +61,8 @@ def build(verbose: bool = False, extra_flags=(), jobs: int | None = None) -> str
     for s in SOURCES:
         obj = os.path.join(objdir, s + ".o")
         objs.append(obj)
-        cmds.append([hipcc(), *flags, "-c", "-o", obj, os.path.join(CSRC, s)])
+        form = [] if s in AGPR_SOURCES else MFMA_FLAGS
+        cmds.append([hipcc(), *flags, *form, "-c", "-o", obj, os.path.join(CSRC, s)])
     t0 = time.time()
     if verbose:
         for c in cmds:

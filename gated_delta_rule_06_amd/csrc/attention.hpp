@@ -1,0 +1,177 @@
+// Operands, tiles and sequences shared by the kernels of causal softmax attention (attention.hip, attention_bwd.hip,
+// attention_step.hip).
+//
+// With s_ij = scale q_i . k_j over the keys j that query i sees (same sequence, i - window < j <= i):
+//   lse_i = log sum_j exp s_ij     p_ij = exp(s_ij - lse_i)     o_i = sum_j p_ij v_j
+// Exponentials are taken to base 2, with log2(e) folded into the scale.
+//
+// Every product over 32 rows is D[32 x 32] += A[32 x 16] B[32 x 16]^T on the matrix cores. Scores are made transposed where
+// the following product sums over their rows, so that their accumulators are the next operand as they are: a lane holds one
+// column, and eight consecutive accumulators are the eight contraction values of one product.
+#pragma once
+
+#include <type_traits>
+
+#include "attention_layout.hpp"
+#include "chunk_layout.hpp"
+#include "common.hpp"
+#include "mfma.hpp"
+
+namespace muir {
+namespace at {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// A running maximum before any key: below every score, and finite, so that differences from it stay numbers.
+constexpr float LOWEST = -1e30f;
+
+// Eight contraction values of one operand row: lane l has row l % 32, and its element j is contraction index 8 (l / 32) + j
+// of a product's 16. For float32 a product is eight instructions of two contraction values each, one element of every lane.
+template <typename T> struct Op;
+template <> struct Op<bf16_t> {
+    using frag = bf16x8_t;
+    static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    // Rounds to bf16, nearest even.
+    static __device__ __forceinline__ frag pack(float a, float b, float c, float d, float e, float f, float g, float h) {
+        return frag{static_cast<__bf16>(a), static_cast<__bf16>(b), static_cast<__bf16>(c), static_cast<__bf16>(d),
+                    static_cast<__bf16>(e), static_cast<__bf16>(f), static_cast<__bf16>(g), static_cast<__bf16>(h)};
+    }
+    static __device__ __forceinline__ float get(frag f, int j) { return static_cast<float>(f[j]); }
+};
+template <> struct Op<float> {
+    typedef float frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ frag pack(float a, float b, float c, float d, float e, float f, float g, float h) {
+        return frag{a, b, c, d, e, f, g, h};
+    }
+    static __device__ __forceinline__ float get(frag f, int j) { return f[j]; }
+};
+
+// Eight consecutive stored values (16-byte aligned).
+template <typename T> __device__ __forceinline__ typename Op<T>::frag load8(const void *p) {
+    return *static_cast<const typename Op<T>::frag *>(__builtin_assume_aligned(p, 16));
+}
+
+// A tile of token rows of D values in LDS, without padding, as the asynchronous loads write it: lane after lane 16 bytes. The
+// 16-byte pieces of a row are permuted by its number so that reading one piece of 16 rows (operand rows) and 64 bytes of
+// eight rows (the transposing reads) both take every bank evenly. The permutation repeats every 16 rows.
+template <typename T, int D> struct Tile {
+    static constexpr int ROWB = D * int(sizeof(T)), CH = ROWB / 16, RPI = 64 / CH;  // RPI: rows of one load of a wavefront
+    static __device__ __forceinline__ int swz(int r) {
+        return CH == 8 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+    }
+    static __device__ __forceinline__ int at(int r, int chunk) { return r * ROWB + ((chunk ^ swz(r)) << 4); }
+
+    // Operand rows r0 + l % R, contraction values 16 s + 8 (l / 32) + j (32 rows) or 32 s + 8 (l / 16) + j (16 rows).
+    template <int R> static __device__ __forceinline__ typename Op<T>::frag row(const unsigned char *t, int r0, int s, int lane) {
+        const int r = lane % R, c = (s * (64 / R) + lane / R) * int(sizeof(T)) / 2;  // its first 16-byte piece
+        const unsigned char *p = t + r0 * ROWB;
+        if constexpr (sizeof(T) == 2) {
+            return *reinterpret_cast<const bf16x8_t *>(p + at(r, c));
+        } else {
+            const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p + at(r, c)), b = *reinterpret_cast<const f32x4_t *>(p + at(r, c + 1));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+    // Operand rows are the tile's columns c0 + l % R; element j is tile row r0 + 4 (l / R) + j % 4, and 256 / R rows on
+    // for j >= 4: the order in which two 4-row groups of an accumulator lie in a lane. r0 is a multiple of 16.
+    template <int R> static __device__ __forceinline__ typename Op<T>::frag col(unsigned char *t, int r0, int c0, int lane) {
+        constexpr int NEXT = 256 / R;
+        const int g = lane / R;
+        unsigned char *p = t + r0 * ROWB;
+        if constexpr (sizeof(T) == 2) {
+            // The transposing read gives lane m of sixteen the column m of the four rows whose 32 bytes the lanes address.
+            const int m = lane % 16, r = 4 * g + (m >> 2), b = 2 * (c0 + (lane % R) / 16 * 16) + 8 * (m & 3);
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (at(r, b >> 4) + (b & 8))));
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (at(r + NEXT, b >> 4) + (b & 8))));
+            return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int c = c0 + lane % R;
+            typename Op<T>::frag f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = *reinterpret_cast<const float *>(p + at(4 * g + j % 4 + j / 4 * NEXT, c >> 2) + 4 * (c & 3));
+            return f;
+        }
+    }
+    // Four consecutive values from column c on (a multiple of 4) of row r.
+    static __device__ __forceinline__ void put4(unsigned char *t, int r, int c, f32x4_t v) {
+        unsigned char *p = t + at(r, c * int(sizeof(T)) >> 4);
+        store4(reinterpret_cast<T *>(p) + (c & (16 / int(sizeof(T)) - 1)), v);
+    }
+
+    // ROWS rows from `base` on into the tile, by WAVES wavefronts of which this is `wv`, straight to LDS. Rows from `live`
+    // on, and so what lies behind a sequence, come as zeros. `stride` is the bytes from row to row.
+    template <int ROWS, int WAVES> static __device__ __forceinline__ void fetch(unsigned char *t, const void *base, uint32_t stride, int live, int wv, int lane) {
+        const rsrc_t r = make_rsrc(base, live <= 0 ? 0u : uint32_t(min(live, ROWS) - 1) * stride + ROWB);
+#pragma unroll
+        for (int n = 0; n < ROWS / RPI / WAVES; ++n) {
+            const int r0 = (n * WAVES + wv) * RPI, i = lane / CH;
+            // Only the row's place in its 16 enters the permutation, so most loads of a wavefront share their lanes' offsets.
+            const uint32_t voff = i * stride + (((lane % CH) ^ swz((r0 & 15) + i)) << 4);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(t + r0 * ROWB), 16, voff, r0 * stride, 0, 0);
+        }
+    }
+};
+
+// Waits for every load of this wavefront; the barrier behind it makes all wavefronts' tiles visible.
+__device__ __forceinline__ void loads_done() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+}
+
+// Largest and sum over the two halves of a wavefront, which hold the same columns.
+__device__ __forceinline__ float halves_max(float x) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Row of accumulator element i (of 16) in a 32-row result.
+__device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i / 4) + 4 * (lane / 32) + i % 4; }
+// Eight accumulators as the operand of step s (of two).
+template <typename T> __device__ __forceinline__ typename Op<T>::frag acc_frag(const f32x16_t &x, int s) {
+    return Op<T>::pack(x[8 * s], x[8 * s + 1], x[8 * s + 2], x[8 * s + 3], x[8 * s + 4], x[8 * s + 5], x[8 * s + 6], x[8 * s + 7]);
+}
+
+struct Block {
+    int seq, lo, rows, n, at;  // the sequence, its first row, rows and tokens, and the block's first row in it
+};
+// Block `w` of `R` rows; one past its sequence's rows has at >= rows. All 64 lanes search together.
+template <int R> __device__ __forceinline__ Block find_block(const Sequences &q, int w) {
+    const int lane = threadIdx.x & 63;
+    const int s = search_sequence(q.S, [&](int lo, int step, int hi) {
+        const int i = lo + lane * step;
+        return __builtin_amdgcn_readfirstlane(static_cast<int>(__popcll(__ballot(i <= hi && q.first(i) / R + i <= w))));
+    });
+    Block b;
+    b.seq = __builtin_amdgcn_readfirstlane(s);
+    b.lo = __builtin_amdgcn_readfirstlane(q.first(s));
+    b.rows = __builtin_amdgcn_readfirstlane(q.rows(s));
+    b.n = __builtin_amdgcn_readfirstlane(q.tokens(s));
+    b.at = (w - b.lo / R - b.seq) * R;
+    return b;
+}
+
+}  // namespace at
+}  // namespace muir

@@ -1,0 +1,274 @@
+// Causal softmax attention, backward. With p_ij = exp(s_ij - lse_i) made again from q, k and the forward's lse,
+//   D_i = do_i . o_i     ds_ij = p_ij (do_i . v_j - D_i)
+//   dq_i = scale sum_j ds_ij k_j     dk_j = scale sum_i ds_ij q_i     dv_j = sum_i p_ij do_i
+// Two kernels, each with its sums in registers from the first to the last product, so no sum depends on an order and nothing is
+// added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
+// and do . v are made in both (7 products of which 5 are needed).
+// bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); D is taken from
+// the rounded o; everything else is float32.
+#include "attention.hpp"
+#include "attention_kernels.hpp"
+#include "launch.hpp"
+#include "op_layout.hpp"
+
+namespace muir {
+namespace {
+
+using namespace at;
+
+// Writes a wavefront's 32 rows, given transposed in accumulators, through its LDS room to rows of `stride` elements.
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(unsigned char *room, const f32x16_t (&acc)[D / 32], float f, bool live, T *out, size_t stride,
+                                           int rows, int lane) {
+    using Ti = Tile<T, D>;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4_t y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = live ? acc[n][4 * i + r] * f : 0.f;
+            Ti::put4(room, lane & 31, 32 * n + 8 * i + 4 * (lane >> 5), y);
+        }
+    wave_lds_sync();
+#pragma unroll
+    for (int n = 0; n < 32 / Ti::RPI; ++n) {
+        const int r = n * Ti::RPI + lane / Ti::CH, c = lane % Ti::CH;
+        if (r < rows)
+            *reinterpret_cast<u32x4_t *>(out + r * stride + c * (16 / sizeof(T))) = *reinterpret_cast<const u32x4_t *>(room + Ti::at(r, c));
+    }
+    wave_lds_sync();
+}
+
+template <typename T, int D> struct Bwd {
+    static constexpr int WAVES = 4, ROWS = 32 * WAVES, STEP = sizeof(T) == 2 ? 64 : 32;  // rows of the tiles walked over
+    static constexpr int TILE = STEP * D * int(sizeof(T)), STATS = 4 * 64 * 4;           // two of lse and of D
+    static_assert(ROWS == ATTENTION_ROWS && 4 * TILE >= ROWS * D * int(sizeof(T)), "the outputs pass through the tiles' room");
+};
+
+// dq, and for the next kernel lse in base 2 and D, [H][N] each; a row without keys gets an lse of +infinity, so its p are zero.
+template <typename T, int D>
+__global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention_dq_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ o, const T *__restrict__ dout,
+    const float *__restrict__ lse, Sequences seqs, T *__restrict__ dq, float *__restrict__ lse2, float *__restrict__ delta, int blocks,
+    int H, int Hk, int window, float scale) {
+    using C = Bwd<T, D>;
+    using Ti = Tile<T, D>;
+    using frag = typename Op<T>::frag;
+    constexpr int WAVES = C::WAVES, KEYS = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const Item it = find_item(blockIdx.x, blocks, H, Hk);
+    const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);
+    if (b.at >= b.rows) return;
+    const int hk = it.h / (H / Hk);
+    const uint32_t kv_stride = uint32_t(Hk) * Ti::ROWB;
+    const int r0 = b.at + 32 * wv, q_row = r0 + (lane & 31);
+    const float scale2 = scale * LOG2E;
+
+    const int end = min(b.at + C::ROWS, b.n);
+    const int first = window ? max(b.at - window + 1, 0) / KEYS : 0;
+    const int tiles = b.at < b.n ? (end + KEYS - 1) / KEYS : first;
+    const T *kb = k + (static_cast<size_t>(b.lo) * Hk + hk) * D, *vb = v + (static_cast<size_t>(b.lo) * Hk + hk) * D;
+    auto fetch = [&](int j, int buf) {
+        const size_t at = static_cast<size_t>(j) * KEYS * Hk * D;
+        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE, kb + at, kv_stride, b.n - j * KEYS, wv, lane);
+        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE + TILE, vb + at, kv_stride, b.n - j * KEYS, wv, lane);
+    };
+    if (first < tiles) fetch(first, 0);
+
+    const size_t own = (static_cast<size_t>(b.lo) + min(q_row, b.rows - 1)) * H + it.h;
+    frag qf[QS], df[QS];
+    float d = 0.f;
+#pragma unroll
+    for (int s = 0; s < QS; ++s) {
+        qf[s] = load8<T>(q + own * D + 16 * s + 8 * half);
+        df[s] = load8<T>(dout + own * D + 16 * s + 8 * half);
+        const frag of = load8<T>(o + own * D + 16 * s + 8 * half);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d = fmaf(Op<T>::get(of, j), Op<T>::get(df[s], j), d);
+    }
+    d = halves_sum(d);
+    const float l = lse[own] * LOG2E;
+    const bool live = q_row < b.n && l != -INFINITY;
+    const float top = live ? l : INFINITY;
+    if (half == 0 && q_row < b.rows) {
+        const size_t i = static_cast<size_t>(it.h) * seqs.N + b.lo + q_row;
+        lse2[i] = top;
+        delta[i] = live ? d : 0.f;
+    }
+    f32x16_t acc[NO] = {};
+
+    auto step = [&](auto masked, int j, unsigned char *kt, unsigned char *vt) {
+#pragma unroll
+        for (int t = 0; t < KEYS / 32; ++t) {
+            f32x16_t x = {}, y = {};
+#pragma unroll
+            for (int s = 0; s < QS; ++s) {
+                x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, lane), qf[s], x);
+                y = Op<T>::mma(Ti::template row<32>(vt, 32 * t, s, lane), df[s], y);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, -top));
+                x[i] = p * (y[i] - d);
+                if constexpr (decltype(masked)::value) {
+                    const int key = j * KEYS + 32 * t + acc_row(i, lane);
+                    const bool seen = key <= q_row && (window == 0 || q_row - key < window);
+                    x[i] = seen ? x[i] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const frag f = acc_frag<T>(x, s);
+#pragma unroll
+                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(kt, 32 * t + 16 * s, 32 * n, lane), f, acc[n]);
+            }
+        }
+    };
+    for (int j = first; j < tiles; ++j) {
+        const int buf = (j - first) & 1;
+        loads_done();
+        if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
+        unsigned char *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
+        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) continue;
+        if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window))
+            step(std::true_type{}, j, kt, vt);
+        else
+            step(std::false_type{}, j, kt, vt);
+    }
+    lds_barrier();
+    store_rows<T, D>(smem + wv * 32 * Ti::ROWB, acc, scale, live, dq + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D,
+                     static_cast<size_t>(H) * D, b.rows - r0, lane);
+}
+
+// dk and dv of 128 keys of a key head, 32 to a wavefront, whose keys and values stay in registers, over the queries of all its heads. Scores have
+// queries as rows, so p and ds are the operands of dv^T += do^T p and dk^T += q^T ds as they are.
+template <typename T, int D>
+__global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse2,
+    const float *__restrict__ delta, Sequences seqs, T *__restrict__ dk, T *__restrict__ dv, int blocks, int H, int Hk, int window,
+    float scale) {
+    using C = Bwd<T, D>;
+    using Ti = Tile<T, D>;
+    using frag = typename Op<T>::frag;
+    constexpr int WAVES = C::WAVES, QR = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *stats = reinterpret_cast<float *>(smem + 4 * TILE);
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const Item it = find_item(blockIdx.x, blocks, Hk, Hk);
+    const Block b = find_block<C::ROWS>(seqs, it.block);
+    if (b.at >= b.rows) return;
+    const int G = H / Hk, h0 = it.h * G;
+    const uint32_t q_stride = uint32_t(H) * Ti::ROWB;
+    const int k0 = b.at + 32 * wv, key = k0 + (lane & 31);
+    const float scale2 = scale * LOG2E;
+
+    // Tiles of queries that see the block's keys, for each head.
+    const int first = b.at / QR;
+    const int end = window ? static_cast<int>(min(static_cast<int64_t>(b.n), static_cast<int64_t>(b.at) + C::ROWS + window - 1)) : b.n;
+    const int per = b.at < b.n ? (end + QR - 1) / QR - first : 0, steps = per * G;
+    auto fetch = [&](int i, int buf) {
+        const int h = h0 + i / per, j = first + i % per, left = b.n - j * QR;
+        const size_t row = static_cast<size_t>(b.lo) + static_cast<size_t>(j) * QR;
+        Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE, q + (row * H + h) * D, q_stride, left, wv, lane);
+        Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE + TILE, dout + (row * H + h) * D, q_stride, left, wv, lane);
+        if (wv < 2) {
+            const rsrc_t r = make_rsrc((wv ? delta : lse2) + static_cast<size_t>(h) * seqs.N + row, min(left, QR) * 4u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stats + (buf * 2 + wv) * 64), 4, lane * 4, 0, 0, 0);
+        }
+    };
+    if (steps > 0) fetch(0, 0);
+
+    const size_t own = (static_cast<size_t>(b.lo) + min(key, b.rows - 1)) * Hk + it.h;
+    frag kf[QS], vf[QS];
+#pragma unroll
+    for (int s = 0; s < QS; ++s) {
+        kf[s] = load8<T>(k + own * D + 16 * s + 8 * half);
+        vf[s] = load8<T>(v + own * D + 16 * s + 8 * half);
+    }
+    f32x16_t dka[NO] = {}, dva[NO] = {};
+
+    auto step = [&](auto masked, int row0, unsigned char *qt, unsigned char *dt, const float *st) {
+        f32x16_t x = {}, y = {};
+#pragma unroll
+        for (int s = 0; s < QS; ++s) {
+            x = Op<T>::mma(Ti::template row<32>(qt, 0, s, lane), kf[s], x);
+            y = Op<T>::mma(Ti::template row<32>(dt, 0, s, lane), vf[s], y);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4_t l = *reinterpret_cast<const f32x4_t *>(st + 8 * i + 4 * half), d = *reinterpret_cast<const f32x4_t *>(st + 64 + 8 * i + 4 * half);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float p = __builtin_amdgcn_exp2f(fmaf(x[4 * i + r], scale2, -l[r])), ds = p * (y[4 * i + r] - d[r]);
+                if constexpr (decltype(masked)::value) {
+                    const int row = row0 + acc_row(4 * i + r, lane);
+                    const bool seen = key <= row && row < b.n && (window == 0 || row - key < window);
+                    p = seen ? p : 0.f;
+                    ds = seen ? ds : 0.f;
+                }
+                x[4 * i + r] = p;
+                y[4 * i + r] = ds;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const frag p = acc_frag<T>(x, s), ds = acc_frag<T>(y, s);
+#pragma unroll
+            for (int n = 0; n < NO; ++n) {
+                dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, lane), p, dva[n]);
+                dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, lane), ds, dka[n]);
+            }
+        }
+    };
+    for (int i = 0; i < steps; ++i) {
+        const int buf = i & 1, j = first + i % per;
+        loads_done();
+        if (i + 1 < steps) fetch(i + 1, buf ^ 1);
+        for (int t = 0; t < QR / 32; ++t) {
+            const int row0 = j * QR + 32 * t;
+            unsigned char *qt = smem + buf * 2 * TILE + t * 32 * Ti::ROWB, *dt = qt + TILE;
+            const float *st = stats + buf * 128 + 32 * t;
+            if (row0 + 31 < k0 || row0 >= b.n || (window && row0 - (k0 + 31) >= window)) continue;  // no query sees a key
+            if (row0 < k0 + 31 || row0 + 31 >= b.n || (window && row0 + 31 - k0 >= window))
+                step(std::true_type{}, row0, qt, dt, st);
+            else
+                step(std::false_type{}, row0, qt, dt, st);
+        }
+    }
+    lds_barrier();
+    unsigned char *room = smem + wv * 32 * Ti::ROWB;
+    const size_t out = ((static_cast<size_t>(b.lo) + k0) * Hk + it.h) * D, stride = static_cast<size_t>(Hk) * D;
+    store_rows<T, D>(room, dka, scale, key < b.n, dk + out, stride, b.rows - k0, lane);
+    store_rows<T, D>(room, dva, 1.f, key < b.n, dv + out, stride, b.rows - k0, lane);
+}
+
+template <typename T, int D> hipError_t launch(const AttentionCall &c, const AttentionGrads &g, void *workspace, hipStream_t stream) {
+    using B = Bwd<T, D>;
+    constexpr int LDS = 4 * B::TILE;
+    hipError_t err = allow_lds<&attention_dq_kernel<T, D>>(LDS);
+    if (err == hipSuccess) err = allow_lds<&attention_dkv_kernel<T, D>>(LDS + B::STATS);
+    if (err != hipSuccess) return err;
+    const int blocks = static_cast<int>(attention_blocks(c.N, c.S));
+    const Sequences s{c.offsets, c.lens, c.N, c.S};
+    const T *q = static_cast<const T *>(c.q), *k = static_cast<const T *>(c.k), *v = static_cast<const T *>(c.v), *d = static_cast<const T *>(g.dout);
+    float *lse2 = static_cast<float *>(workspace), *delta = lse2 + up256(static_cast<size_t>(c.N) * c.H * 4) / 4;
+    hipLaunchKernelGGL((attention_dq_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * B::WAVES), LDS, stream, q, k, v,
+                       static_cast<const T *>(g.o), d, g.lse, s, static_cast<T *>(g.dq), lse2, delta, blocks, c.H, c.Hk, c.window, c.scale);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((attention_dkv_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), LDS + B::STATS, stream,
+                       q, k, v, d, lse2, delta, s, static_cast<T *>(g.dk), static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_bwd(const AttentionCall &c, const AttentionGrads &g, void *workspace, hipStream_t stream) {
+    if (c.d == 64) return c.bf16 ? launch<bf16_t, 64>(c, g, workspace, stream) : launch<float, 64>(c, g, workspace, stream);
+    if (c.d == 128) return c.bf16 ? launch<bf16_t, 128>(c, g, workspace, stream) : launch<float, 128>(c, g, workspace, stream);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace muir

@@ -1,0 +1,47 @@
+// Internal launchers of causal softmax attention and its paged cache. Arguments are validated by the C ABI layer
+// (attention_api.cpp) before any of these is called; each returns the launch's hipError_t.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+namespace muir {
+
+// Rows q [N, H, d], k, v [N, Hk, d] of S sequences: offsets [S + 1] or NULL (N / S rows each), lens [S] or NULL.
+struct AttentionCall {
+    const void *q, *k, *v;
+    const int *offsets, *lens;
+    int N, S, H, Hk, d, window;
+    float scale;
+    bool bf16;
+};
+// Rows of a workgroup of the prompt kernels.
+constexpr int ATTENTION_ROWS = 128;
+inline long long attention_blocks(int N, int S) { return static_cast<long long>(N) / ATTENTION_ROWS + S + 1; }
+hipError_t launch_attention_fwd(const AttentionCall &c, void *o, float *lse, hipStream_t stream);
+
+size_t attention_bwd_workspace_bytes(int N, int H);
+struct AttentionGrads {
+    const void *o, *dout;
+    const float *lse;
+    void *dq, *dk, *dv;
+};
+hipError_t launch_attention_bwd(const AttentionCall &c, const AttentionGrads &g, void *workspace, hipStream_t stream);
+
+// Paged cache: k_cache, v_cache [pages, Hk, page, d], table [B, width].
+struct CacheCall {
+    void *k_cache, *v_cache;
+    const int *table;
+    int pages, page, width, Hk, d;
+    bool bf16;
+};
+hipError_t launch_cache_append(const CacheCall &c, const void *k, const void *v, const int *offsets, const int *lens,
+                               const int *start, int N, int S, hipStream_t stream);
+
+// Parts that a sequence's keys are split into, side by side (1: none, and no workspace).
+int attention_step_parts(int B, int H, int Hk, int d, int capacity, bool bf16);
+size_t attention_step_workspace_bytes(int B, int H, int Hk, int d, int capacity, bool bf16);
+hipError_t launch_attention_step(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o,
+                                 int B, int H, int window, float scale, void *workspace, hipStream_t stream);
+
+}  // namespace muir

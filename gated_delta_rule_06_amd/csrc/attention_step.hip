@@ -1,0 +1,274 @@
+// The paged cache of keys and values: rows appended to it, and one new token of each sequence attending over it.
+//
+// Step: a workgroup has up to 16 query heads that share a key head and one part of a sequence's keys, its wavefronts every WAVES-th tile of
+// 32 keys, each with its own running maximum, sum and output and its own two tiles of keys and values in LDS (loads straight to LDS, one tile
+// in flight); they meet in LDS at the end. Where sequences and key heads do not fill the card a sequence is cut into parts, which a second kernel
+// joins. Reading the cache once bounds it. Scores are made transposed (16 keys by 16 heads), so that two score tiles are the operand
+// of the product with the values, as in the prompt kernels; p is rounded to bf16 there in bf16.
+// Rows behind the last token, and pages that the table does not have, are never read: their keys come as zeros and are masked.
+#include "attention.hpp"
+#include "attention_kernels.hpp"
+#include "launch.hpp"
+
+namespace muir {
+namespace {
+
+using namespace at;
+
+// 64 rows of a sequence, all key heads: 16 bytes a thread and turn.
+constexpr int APPEND_ROWS = 64;
+template <int ROWB>
+__global__ __launch_bounds__(256) void cache_append_kernel(const unsigned char *__restrict__ k, const unsigned char *__restrict__ v,
+                                                           unsigned char *__restrict__ k_cache, unsigned char *__restrict__ v_cache, Pages pg,
+                                                           Sequences seqs, const int *__restrict__ start) {
+    constexpr int CH = ROWB / 16;
+    const Block b = find_block<APPEND_ROWS>(seqs, blockIdx.x);
+    if (b.at >= b.n) return;
+    const int s = b.seq, base = start ? start[s] : 0, n = min(b.n - b.at, APPEND_ROWS);
+    if (base < 0) return;
+    const size_t in = (static_cast<size_t>(b.lo) + b.at) * pg.Hk * ROWB;
+    for (int i = threadIdx.x; i < n * pg.Hk * CH; i += 256) {
+        const int c = i % CH, hk = i / CH % pg.Hk, r = i / CH / pg.Hk;
+        const int64_t pos = static_cast<int64_t>(base) + b.at + r;
+        if (pos >= pg.room()) continue;
+        const int id = pg.id(s, static_cast<int>(pos));
+        if (!pg.good(id)) continue;
+        const size_t to = pg.row(id, hk, static_cast<int>(pos)) * ROWB + c * 16, from = in + static_cast<size_t>(i) * 16;
+        *reinterpret_cast<u32x4_t *>(k_cache + to) = *reinterpret_cast<const u32x4_t *>(k + from);
+        *reinterpret_cast<u32x4_t *>(v_cache + to) = *reinterpret_cast<const u32x4_t *>(v + from);
+    }
+}
+
+template <typename T, int D> struct Step {
+    static constexpr int KEYS = 32, TILE = KEYS * D * int(sizeof(T)), WAVES = sizeof(T) * D == 512 ? 2 : 4;
+    static constexpr int RING = 4 * TILE, LDS = WAVES * RING;  // two tiles of keys and values a wavefront
+    static_assert(RING >= 16 * D * 4 + 128, "outputs, maxima and sums of 16 heads pass through the tiles' room");
+};
+
+template <typename T, int D>
+__global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kernel(
+    const T *__restrict__ q, const T *__restrict__ kn, const T *__restrict__ vn, T *k_cache, T *v_cache, Pages pg,
+    const int *__restrict__ lens, T *__restrict__ o, float *__restrict__ part_o, float *__restrict__ part_s, int H, int parts, int window,
+    float scale2) {
+    using C = Step<T, D>;
+    using Ti = Tile<T, D>;
+    using frag = typename Op<T>::frag;
+    constexpr int WAVES = C::WAVES, TILE = C::TILE, QS = D / 32, NO = D / 16;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+    const int G = H / pg.Hk, sets = (G + 15) / 16;
+    const int part = blockIdx.x % parts, set = blockIdx.x / parts % sets, bh = blockIdx.x / parts / sets, hk = bh % pg.Hk, b = bh / pg.Hk;
+    const int h0 = hk * G + set * 16, heads = min(G - set * 16, 16);
+    unsigned char *ring = smem + wv * C::RING;
+
+    const Span span = step_span(lens[b], kn != nullptr, window, pg.room());
+    const int old = span.old, n = span.n, begin = span.begin;
+    const int per = (span.t1 - span.t0 + parts - 1) / parts, from = span.t0 + part * per + wv, to = min(span.t0 + (part + 1) * per, span.t1);
+
+    // The wavefront's tiles are from, from + WAVES, ... Each lane keeps the page of one half (16 rows, which always lie in one page) of the
+    // 32 tiles that are fetched next.
+    int ids = -1;
+    auto fetch = [&](int tile, int buf) {
+        const int i = (tile - from) / WAVES % 32;
+        if (i == 0) {
+            const int64_t pos = static_cast<int64_t>(tile + lane / 2 * WAVES) * 32 + lane % 2 * 16;
+            ids = pos < n ? pg.table[static_cast<size_t>(b) * pg.width + (pos >> pg.log_page)] : -1;
+        }
+        int good = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int id = __builtin_amdgcn_readlane(ids, 2 * i + u), pos = tile * 32 + 16 * u;
+            const bool known = pg.good(id);
+            const int live = known ? min(old - pos, 16) : 0;
+            const size_t at = live > 0 ? pg.row(id, hk, pos) * D : 0;
+            unsigned char *t = ring + buf * 2 * TILE + u * 16 * Ti::ROWB;
+            Ti::template fetch<16, 1>(t, k_cache + at, Ti::ROWB, live, 0, lane);
+            Ti::template fetch<16, 1>(t + TILE, v_cache + at, Ti::ROWB, live, 0, lane);
+            good |= known << u;
+        }
+        return good;
+    };
+    int good_next = from < to ? fetch(from, 0) : 0;
+
+    frag qf[QS];
+#pragma unroll
+    for (int s = 0; s < QS; ++s) {
+        qf[s] = frag{};
+        if (col < heads) qf[s] = load8<T>(q + (static_cast<size_t>(b) * H + h0 + col) * D + 32 * s + 8 * g);
+    }
+    f32x4_t acc[NO] = {};
+    float m = LOWEST, l = 0.f;
+    for (int tile = from, buf = 0; tile < to; tile += WAVES, buf ^= 1) {
+        const bool more = tile + WAVES < to;
+        const int good = good_next;  // which halves lie in a page that the cache has
+        if (more) good_next = fetch(tile + WAVES, buf ^ 1);
+        // The tile's own loads are done when no more than the next one's are out.
+        if (more)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * 16 / Ti::RPI) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        unsigned char *kt = ring + buf * 2 * TILE, *vt = kt + TILE;
+        const int p0 = tile * 32;
+        if (kn && p0 <= old && old < p0 + 32 && n > old) {  // the new token's row
+            const int r = old - p0;
+            if (lane < Ti::CH) {
+                const size_t at = (static_cast<size_t>(b) * pg.Hk + hk) * D + lane * (16 / sizeof(T));
+                const u32x4_t ks = *reinterpret_cast<const u32x4_t *>(kn + at), vs = *reinterpret_cast<const u32x4_t *>(vn + at);
+                *reinterpret_cast<u32x4_t *>(kt + Ti::at(r, lane)) = ks;
+                *reinterpret_cast<u32x4_t *>(vt + Ti::at(r, lane)) = vs;
+                if (set == 0 && (good >> (r >> 4) & 1)) {
+                    const size_t to_row = pg.row(pg.id(b, old), hk, old) * D + lane * (16 / sizeof(T));
+                    *reinterpret_cast<u32x4_t *>(k_cache + to_row) = ks;
+                    *reinterpret_cast<u32x4_t *>(v_cache + to_row) = vs;
+                }
+            }
+        }
+        wave_lds_sync();
+        f32x4_t x[2] = {};
+#pragma unroll
+        for (int s = 0; s < QS; ++s)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) x[u] = Op<T>::mma16(Ti::template row<16>(kt, 16 * u, s, lane), qf[s], x[u]);
+        if (p0 < begin || p0 + 32 > n || good != 3) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = p0 + 16 * u + 4 * g + i;
+                    x[u][i] = (good >> u & 1) && pos >= begin && pos < n ? x[u][i] : -INFINITY;
+                }
+        }
+        float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = halves_max(top) * scale2;
+        if (__any(top > m + 8.f)) {
+            const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) acc[i] *= f;
+            m = now;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[u][i] = __builtin_amdgcn_exp2f(fmaf(x[u][i], scale2, -m));
+                l += x[u][i];
+            }
+        const frag p = Op<T>::pack(x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]);
+#pragma unroll
+        for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, lane), p, acc[i]);
+        wave_lds_sync();  // the tile is free
+    }
+    l += __shfl_xor(l, 16, 64);
+    l = halves_sum(l);
+
+    // The wavefronts' results: [16 heads][D] values (16-byte pieces of four, permuted by the head against bank conflicts), then maxima and sums.
+    auto place = [&](int w, int h, int c) { return reinterpret_cast<float *>(smem + w * C::RING) + h * D + ((c ^ h) & (D / 4 - 1)) * 4; };
+    auto stat = [&](int w) { return reinterpret_cast<float *>(smem + w * C::RING + 16 * D * 4); };
+#pragma unroll
+    for (int i = 0; i < NO; ++i) *reinterpret_cast<f32x4_t *>(place(wv, col, 4 * i + g)) = acc[i];
+    if (g == 0) {
+        stat(wv)[col] = m;
+        stat(wv)[16 + col] = l;
+    }
+    lds_barrier();
+    for (int i = threadIdx.x; i < heads * (D / 4); i += 64 * WAVES) {
+        const int h = i / (D / 4), c = i % (D / 4);
+        float all = LOWEST, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) all = fmaxf(all, stat(w)[h]);
+        f32x4_t y = zero4();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float f = __builtin_amdgcn_exp2f(stat(w)[h] - all);
+            sum = fmaf(stat(w)[16 + h], f, sum);
+            y += *reinterpret_cast<const f32x4_t *>(place(w, h, c)) * f;
+        }
+        const size_t row = static_cast<size_t>(b) * H + h0 + h;
+        if (parts == 1) {
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+            store4(o + row * D + 4 * c, y * inv);
+        } else {
+            *reinterpret_cast<f32x4_t *>(part_o + (row * parts + part) * D + 4 * c) = y;
+            if (c == 0) {
+                part_s[(row * parts + part) * 2] = all;
+                part_s[(row * parts + part) * 2 + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the parts of a head: D / 4 threads to a head, in the parts' order.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(const float *__restrict__ part_o, const float *__restrict__ part_s, T *__restrict__ o,
+                                                            int rows, int parts) {
+    const int row = blockIdx.x * (1024 / D) + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+    if (row >= rows) return;
+    const float *s = part_s + static_cast<size_t>(row) * parts * 2, *y = part_o + static_cast<size_t>(row) * parts * D + 4 * c;
+    float all = LOWEST, sum = 0.f;
+    for (int p = 0; p < parts; ++p) all = fmaxf(all, s[2 * p]);
+    f32x4_t x = zero4();
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float f = __builtin_amdgcn_exp2f(s[2 * p] - all);
+        sum = fmaf(s[2 * p + 1], f, sum);
+        x += *reinterpret_cast<const f32x4_t *>(y + static_cast<size_t>(p) * D) * f;
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    store4(o + static_cast<size_t>(row) * D + 4 * c, x * inv);
+}
+
+Pages pages_of(const CacheCall &c) {
+    return Pages{c.table, c.pages, __builtin_ctz(static_cast<unsigned>(c.page)), c.width, c.Hk};
+}
+
+template <typename T, int D>
+hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o, int B, int H, int window,
+                  float scale, void *workspace, hipStream_t stream) {
+    using S = Step<T, D>;
+    hipError_t err = allow_lds<&attention_step_kernel<T, D>>(S::LDS);
+    if (err != hipSuccess) return err;
+    const int parts = attention_step_parts(B, H, c.Hk, D, c.width * c.page, sizeof(T) == 2), sets = (H / c.Hk + 15) / 16;
+    float *part_o = static_cast<float *>(workspace), *part_s = part_o + static_cast<size_t>(B) * H * parts * D;
+    hipLaunchKernelGGL((attention_step_kernel<T, D>), dim3(static_cast<unsigned>(B) * c.Hk * sets * parts), dim3(64 * S::WAVES), S::LDS, stream,
+                       static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), static_cast<T *>(c.k_cache),
+                       static_cast<T *>(c.v_cache), pages_of(c), lens, static_cast<T *>(o), part_o, part_s, H, parts, window, scale * LOG2E);
+    err = hipGetLastError();
+    if (err != hipSuccess || parts == 1) return err;
+    const int rows = B * H, per = 1024 / D;
+    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((rows + per - 1) / per), dim3(256), 0, stream, part_o, part_s, static_cast<T *>(o),
+                       rows, parts);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_append(const CacheCall &c, const void *k, const void *v, const int *offsets, const int *lens, const int *start,
+                               int N, int S, hipStream_t stream) {
+    const int row = c.d * (c.bf16 ? 2 : 4), blocks = N / APPEND_ROWS + S + 1;
+    const Sequences s{offsets, lens, N, S};
+#define MUIR_APPEND(R)                                                                                                           \
+    if (row == R) {                                                                                                              \
+        hipLaunchKernelGGL((cache_append_kernel<R>), dim3(blocks), dim3(256), 0, stream, static_cast<const unsigned char *>(k), \
+                           static_cast<const unsigned char *>(v), static_cast<unsigned char *>(c.k_cache),                      \
+                           static_cast<unsigned char *>(c.v_cache), pages_of(c), s, start);                                     \
+        return hipGetLastError();                                                                                                \
+    }
+    MUIR_APPEND(128) MUIR_APPEND(256) MUIR_APPEND(512)
+#undef MUIR_APPEND
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_attention_step(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o, int B, int H,
+                                 int window, float scale, void *workspace, hipStream_t stream) {
+    if (c.d == 64)
+        return c.bf16 ? launch<bf16_t, 64>(c, q, k, v, lens, o, B, H, window, scale, workspace, stream)
+                      : launch<float, 64>(c, q, k, v, lens, o, B, H, window, scale, workspace, stream);
+    if (c.d == 128)
+        return c.bf16 ? launch<bf16_t, 128>(c, q, k, v, lens, o, B, H, window, scale, workspace, stream)
+                      : launch<float, 128>(c, q, k, v, lens, o, B, H, window, scale, workspace, stream);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace muir

@@ -559,6 +559,84 @@ muir_status_t muir_matvec_q4(
     const void *x, const void *w, const void *scale, const void *zero, void *y, int M, int N, int K,
     int group, muir_dtype_t x_type, muir_dtype_t scale_type, muir_stream_t stream);
 
+/*
+ * Causal softmax attention over whole prompts, as the layers of a hybrid stack between the recurrent ones have it (Muir pages: a local
+ * softmax window in front of the recurrent state). A token sees itself and the tokens before it in its sequence, all of
+ * them or the last `window`:
+ *     s_ij = scale q_i . k_j      lse_i = log sum_j exp s_ij      o_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ *   q, o     [N, H, d]   dtype `qkv`     N rows of S sequences, one behind the other
+ *   k, v     [N, Hk, d]  dtype `qkv`     shared by H / Hk consecutive query heads each
+ *   offsets  [S + 1] int32 or NULL       sequence s has the rows offsets[s] .. offsets[s + 1] (ascending from 0; values are cut to
+ *                                        0..N). NULL: N / S rows each, a padded batch [S, N / S, ...]
+ *   lens     [S] int32 or NULL           tokens of each sequence, from its first row on (clamped to its rows; NULL: all of them)
+ *   lse      [N, H] float32 or NULL      which muir_attention_bwd takes
+ *   H a multiple of Hk; d 64 or 128; window >= 0, 0 for no limit; scale finite and above 0 (usually d^(-1/2)); N >= 0
+ *
+ * Rows that are no token (behind a sequence's length, or behind the last sequence) have o = 0 and lse = -infinity, and what k and v hold
+ * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of up to 127 tokens before it (as 0 times it).
+ * bf16: exp(s_ij - m_i) is rounded to bf16 before it multiplies v_j; sums, maxima and lse are float32. Errors as for muir_chunk_fwd,
+ * and MUIR_ERR_UNSUPPORTED for H above 2^15, N above 2^30 or (N / 128 + S + 1) H above 2^24 - 1.
+ */
+muir_status_t muir_attention_fwd(
+    const void *q, const void *k, const void *v, const int *offsets, const int *lens, void *o, float *lse,
+    int N, int S, int H, int Hk, int d, int window, float scale, muir_dtype_t qkv, muir_stream_t stream);
+
+/*
+ * Its backward pass, given dL/do:
+ *     D_i = do_i . o_i      ds_ij = p_ij (do_i . v_j - D_i)
+ *     dq_i = scale sum_j ds_ij k_j      dk_j = scale sum_i ds_ij q_i      dv_j = sum_i p_ij do_i
+ *
+ *   q, k, v, offsets, lens, window, scale as for the forward, o and lse from it; dout [N, H, d] dtype `qkv`
+ *   dq [N, H, d], dk, dv [N, Hk, d] dtype `qkv`, dk and dv summed over the query heads that share them
+ *   workspace: muir_attention_bwd_workspace_size(...) bytes
+ *
+ * Rows that are no token have gradients 0, and dout and o are not looked at there. Every sum is float32, in a fixed order. In bf16 p and ds
+ * are rounded to bf16 before the products that sum them. A NaN or infinity in a token can reach the gradients of tokens up to 127 before and behind those that see it.
+ */
+size_t muir_attention_bwd_workspace_size(int N, int S, int H, int Hk, int d, muir_dtype_t qkv);
+muir_status_t muir_attention_bwd(
+    const void *q, const void *k, const void *v, const void *o, const float *lse, const int *offsets,
+    const int *lens, const void *dout, void *dq, void *dk, void *dv, int N, int S, int H, int Hk, int d,
+    int window, float scale, muir_dtype_t qkv, void *workspace, size_t workspace_bytes, muir_stream_t stream);
+
+/*
+ * Keys and values of prompts into a paged cache, which muir_decode_step_attention reads.
+ *
+ *   k, v              [N, Hk, d] dtype `type`, of S sequences with offsets and lens as for muir_attention_fwd
+ *   k_cache, v_cache  [pages, Hk, page, d] dtype `type`: row p % page of page table[s][p / page] holds token p of sequence s
+ *   table             [S, width] int32   pages of each sequence; an entry outside 0 .. pages - 1 is no page
+ *   start             [S] int32 or NULL  place of each sequence's first token (NULL: 0; below 0: the sequence is left out)
+ *   page 16, 32, 64, 128 or 256; width * page up to 2^30
+ *
+ * Tokens whose place lies behind the table or in no page are left out. Where a page occurs twice among the places written, either token may be kept.
+ */
+muir_status_t muir_cache_append(
+    const void *k, const void *v, void *k_cache, void *v_cache, const int *table, const int *offsets,
+    const int *lens, const int *start, int N, int S, int Hk, int d, int pages, int page, int width,
+    muir_dtype_t type, muir_stream_t stream);
+
+/*
+ * One new token of each sequence: its key and value are appended to the cache and its query attends to what the cache then holds,
+ * all of it or the last `window` tokens.
+ *
+ *   q, o     [B, H, d] dtype `type`
+ *   k, v     [B, Hk, d] dtype `type`, or both NULL: nothing is appended, and the query attends to the tokens that are there
+ *   k_cache, v_cache, table [B, width], page as for muir_cache_append
+ *   lens     [B] int32   tokens in the cache before the call; the new one is token lens[b]
+ *   workspace: muir_decode_step_attention_workspace_size(...) bytes (0 where no sequence is split)
+ *
+ * A sequence with lens[b] < 0, or whose table has no room for its tokens, takes no part: o is 0 and nothing is written. Tokens in no page are
+ * not seen (and a new one is not kept); where none is seen o is 0. What a page holds behind the last token reaches nothing. The page that a new token
+ * goes to must not be read by another sequence of the same call; pages before it may be shared.
+ */
+size_t muir_decode_step_attention_workspace_size(int B, int H, int Hk, int d, int page, int width,
+                                                 muir_dtype_t type);
+muir_status_t muir_decode_step_attention(
+    const void *q, const void *k, const void *v, void *k_cache, void *v_cache, const int *table,
+    const int *lens, void *o, int B, int H, int Hk, int d, int pages, int page, int width, int window,
+    float scale, muir_dtype_t type, void *workspace, size_t workspace_bytes, muir_stream_t stream);
+
 /* Static, never-NULL name of a status code ("MUIR_OK", ...). */
 const char *muir_status_string(muir_status_t s);
 
