@@ -27,11 +27,8 @@ ARCH = "gfx950"
 # in ordinary VGPRs: the scan updates its fp32 state accumulators with vector
 # instructions between matrix-core products, and in AGPRs every such update costs a copy
 # out and back.
-HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-MFMA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-# The attention backward's sums are touched by nothing but products until the end, and with them a wavefront needs more
-# than the 256 ordinary registers: there the compiler may choose AGPRs.
-AGPR_SOURCES = ("attention_bwd.hip",)
+HIP_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+             "-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
 def hipcc() -> str:
@@ -61,8 +58,7 @@ def build(verbose: bool = False, extra_flags=(), jobs: int | None = None) -> str
     for s in SOURCES:
         obj = os.path.join(objdir, s + ".o")
         objs.append(obj)
-        form = [] if s in AGPR_SOURCES else MFMA_FLAGS
-        cmds.append([hipcc(), *flags, *form, "-c", "-o", obj, os.path.join(CSRC, s)])
+        cmds.append([hipcc(), *flags, "-c", "-o", obj, os.path.join(CSRC, s)])
     t0 = time.time()
     if verbose:
         for c in cmds:

@@ -60,27 +60,28 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     f32x16_t acc[NO] = {};
     float m = LOWEST, l = 0.f;  // base 2, with the scale in
 
-    auto step = [&](auto masked, int j, unsigned char *kt, unsigned char *vt) {
+    const int r0 = b.at + 32 * wv;  // the wavefront's first query
+    auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
         f32x16_t x[NT] = {};
 #pragma unroll
         for (int s = 0; s < QS; ++s)
 #pragma unroll
             for (int t = 0; t < NT; ++t) x[t] = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, lane), qf[s], x[t]);
-        if constexpr (decltype(masked)::value) {
+        if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window)) {  // some key that some query does not see
+            const int last = q_row - j * KEYS - 4 * half, first_seen = window ? last - window : -1000;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int key = j * KEYS + 32 * t + acc_row(i, lane);
-                    const bool seen = key <= q_row && (window == 0 || q_row - key < window);
-                    x[t][i] = seen ? x[t][i] : -INFINITY;
+                    const int key = 32 * t + 8 * (i / 4) + i % 4;
+                    x[t][i] = key <= last && key > first_seen ? x[t][i] : -INFINITY;
                 }
         }
         float top = x[0][0];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, x[t][i]);
+            for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, x[t][i]), x[t][i + 1]);
         top = halves_max(top) * scale2;
         if (__any(top > m + 8.f)) {
             const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
@@ -91,12 +92,13 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 for (int i = 0; i < 16; ++i) acc[n][i] *= f;
             m = now;
         }
+        float sum[2] = {};
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], scale2, -m));
-                l += x[t][i];
+                sum[i & 1] += x[t][i];
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -105,18 +107,18 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(vt, 32 * t + 16 * s, 32 * n, lane), p, acc[n]);
             }
         }
+        l += sum[0] + sum[1];
     };
-    for (int j = first; j < tiles; ++j) {
-        const int buf = (j - first) & 1;
+    auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
+        constexpr int buf = decltype(buffer)::value;
         loads_done();  // tile j is there, and every wavefront has left the other one
         if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
-        unsigned char *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
-        const int r0 = b.at + 32 * wv;                                      // the wavefront's first query
-        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) continue;  // it sees nothing of the tile
-        if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window))
-            step(std::true_type{}, j, kt, vt);
-        else
-            step(std::false_type{}, j, kt, vt);
+        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;  // the wavefront sees nothing of the tile
+        step(j, smem + buf * 2 * TILE, smem + buf * 2 * TILE + TILE);
+    };
+    for (int j = first; j < tiles; j += 2) {
+        turn(j, std::integral_constant<int, 0>{});
+        if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
     }
 
     l = halves_sum(l);

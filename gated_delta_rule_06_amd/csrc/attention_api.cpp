@@ -74,7 +74,7 @@ muir_status_t muir_attention_fwd(const void *q, const void *k, const void *v, co
                         buf("lens", lens, static_cast<size_t>(S) * 4, 4)},
                        {buf("o", o, nq), buf("lse", lse, n * H * 4, 4)});
     if (st != MUIR_OK) return st;
-    const AttentionCall c{q, k, v, offsets, lens, N, S, H, Hk, d, window, scale, qkv == MUIR_BF16};
+    const AttentionCall c{q, k, v, offsets, lens, N, S, H, Hk, d, window < N ? window : 0, scale, qkv == MUIR_BF16};
     return check_hip(launch_attention_fwd(c, o, lse, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -106,7 +106,7 @@ muir_status_t muir_attention_bwd(const void *q, const void *k, const void *v, co
                         buf("offsets", offsets, offset_bytes(S), 4), buf("lens", lens, static_cast<size_t>(S) * 4, 4), buf("dout", dout, nq)},
                        {buf("dq", dq, nq), buf("dk", dk, nk), buf("dv", dv, nk), buf("workspace", workspace, need)});
     if (st != MUIR_OK) return st;
-    const AttentionCall c{q, k, v, offsets, lens, N, S, H, Hk, d, window, scale, qkv == MUIR_BF16};
+    const AttentionCall c{q, k, v, offsets, lens, N, S, H, Hk, d, window < N ? window : 0, scale, qkv == MUIR_BF16};
     return check_hip(launch_attention_bwd(c, AttentionGrads{o, dout, lse, dq, dk, dv}, workspace, static_cast<hipStream_t>(stream)), fn);
 }
 
@@ -115,7 +115,7 @@ muir_status_t muir_cache_append(const void *k, const void *v, void *k_cache, voi
                                 muir_dtype_t type, muir_stream_t stream) {
     const char *fn = "cache_append";
     muir_status_t st = check_heads(fn, Hk, Hk, d, type);
-    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, 64, 1);
+    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, 8, 1);
     if (st == MUIR_OK) st = check_cache(fn, pages, page, width);
     if (st != MUIR_OK) return st;
     if (N == 0) return ok();

@@ -99,7 +99,8 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     }
     f32x16_t acc[NO] = {};
 
-    auto step = [&](auto masked, int j, unsigned char *kt, unsigned char *vt) {
+    auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
+        const bool masked = (j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window);
 #pragma unroll
         for (int t = 0; t < KEYS / 32; ++t) {
             f32x16_t x = {}, y = {};
@@ -108,16 +109,16 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, lane), qf[s], x);
                 y = Op<T>::mma(Ti::template row<32>(vt, 32 * t, s, lane), df[s], y);
             }
+            if (masked) {
+                const int last = q_row - j * KEYS - 32 * t - 4 * half, first_seen = window ? last - window : -1000;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, -top));
-                x[i] = p * (y[i] - d);
-                if constexpr (decltype(masked)::value) {
-                    const int key = j * KEYS + 32 * t + acc_row(i, lane);
-                    const bool seen = key <= q_row && (window == 0 || q_row - key < window);
-                    x[i] = seen ? x[i] : 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    const int key = 8 * (i / 4) + i % 4;
+                    x[i] = key <= last && key > first_seen ? x[i] : -INFINITY;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, -top)) * (y[i] - d);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const frag f = acc_frag<T>(x, s);
@@ -126,16 +127,16 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
             }
         }
     };
-    for (int j = first; j < tiles; ++j) {
-        const int buf = (j - first) & 1;
+    auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
+        constexpr int buf = decltype(buffer)::value;
         loads_done();
         if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
-        unsigned char *kt = smem + buf * 2 * TILE, *vt = kt + TILE;
-        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) continue;
-        if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window))
-            step(std::true_type{}, j, kt, vt);
-        else
-            step(std::false_type{}, j, kt, vt);
+        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;
+        step(j, smem + buf * 2 * TILE, smem + buf * 2 * TILE + TILE);
+    };
+    for (int j = first; j < tiles; j += 2) {
+        turn(j, std::integral_constant<int, 0>{});
+        if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
     }
     lds_barrier();
     store_rows<T, D>(smem + wv * 32 * Ti::ROWB, acc, scale, live, dq + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D,
@@ -189,27 +190,28 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
     }
     f32x16_t dka[NO] = {}, dva[NO] = {};
 
-    auto step = [&](auto masked, int row0, unsigned char *qt, unsigned char *dt, const float *st) {
+    auto step = [&](int row0, unsigned char *qt, unsigned char *dt, const float *st) __attribute__((always_inline)) {
         f32x16_t x = {}, y = {};
 #pragma unroll
         for (int s = 0; s < QS; ++s) {
             x = Op<T>::mma(Ti::template row<32>(qt, 0, s, lane), kf[s], x);
             y = Op<T>::mma(Ti::template row<32>(dt, 0, s, lane), vf[s], y);
         }
+        if (row0 < k0 + 31 || row0 + 31 >= b.n || (window && row0 + 31 - k0 >= window)) {  // some query that does not see some key
+            const int from = key - row0 - 4 * half, to = min(b.n - row0 - 4 * half, window ? from + window : 1000);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int row = 8 * (i / 4) + i % 4;
+                x[i] = row >= from && row < to ? x[i] : -INFINITY;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x4_t l = *reinterpret_cast<const f32x4_t *>(st + 8 * i + 4 * half), d = *reinterpret_cast<const f32x4_t *>(st + 64 + 8 * i + 4 * half);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float p = __builtin_amdgcn_exp2f(fmaf(x[4 * i + r], scale2, -l[r])), ds = p * (y[4 * i + r] - d[r]);
-                if constexpr (decltype(masked)::value) {
-                    const int row = row0 + acc_row(4 * i + r, lane);
-                    const bool seen = key <= row && row < b.n && (window == 0 || row - key < window);
-                    p = seen ? p : 0.f;
-                    ds = seen ? ds : 0.f;
-                }
-                x[4 * i + r] = p;
-                y[4 * i + r] = ds;
+                x[4 * i + r] = __builtin_amdgcn_exp2f(fmaf(x[4 * i + r], scale2, -l[r]));
+                y[4 * i + r] = x[4 * i + r] * (y[4 * i + r] - d[r]);
             }
         }
 #pragma unroll
@@ -222,20 +224,22 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
             }
         }
     };
-    for (int i = 0; i < steps; ++i) {
-        const int buf = i & 1, j = first + i % per;
+    auto turn = [&](int i, auto buffer) __attribute__((always_inline)) {
+        constexpr int buf = decltype(buffer)::value;
         loads_done();
         if (i + 1 < steps) fetch(i + 1, buf ^ 1);
+        const int j = first + i % per;
+#pragma unroll
         for (int t = 0; t < QR / 32; ++t) {
             const int row0 = j * QR + 32 * t;
-            unsigned char *qt = smem + buf * 2 * TILE + t * 32 * Ti::ROWB, *dt = qt + TILE;
-            const float *st = stats + buf * 128 + 32 * t;
             if (row0 + 31 < k0 || row0 >= b.n || (window && row0 - (k0 + 31) >= window)) continue;  // no query sees a key
-            if (row0 < k0 + 31 || row0 + 31 >= b.n || (window && row0 + 31 - k0 >= window))
-                step(std::true_type{}, row0, qt, dt, st);
-            else
-                step(std::false_type{}, row0, qt, dt, st);
+            unsigned char *qt = smem + buf * 2 * TILE + t * 32 * Ti::ROWB;
+            step(row0, qt, qt + TILE, stats + buf * 128 + 32 * t);
         }
+    };
+    for (int i = 0; i < steps; i += 2) {
+        turn(i, std::integral_constant<int, 0>{});
+        if (i + 1 < steps) turn(i + 1, std::integral_constant<int, 1>{});
     }
     lds_barrier();
     unsigned char *room = smem + wv * 32 * Ti::ROWB;

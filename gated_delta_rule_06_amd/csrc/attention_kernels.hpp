@@ -11,7 +11,7 @@ namespace muir {
 struct AttentionCall {
     const void *q, *k, *v;
     const int *offsets, *lens;
-    int N, S, H, Hk, d, window;
+    int N, S, H, Hk, d, window;  // window 0 (no limit) or below N
     float scale;
     bool bf16;
 };

@@ -15,27 +15,40 @@ namespace {
 
 using namespace at;
 
-// 64 rows of a sequence, all key heads: 16 bytes a thread and turn.
-constexpr int APPEND_ROWS = 64;
+// A few rows of a sequence, all key heads: 16 bytes a thread and turn, four turns' loads on their way at once. Eight rows to a workgroup: with 64 a prompt of 100 tokens
+// in two workgroups took 15.7 us.
+constexpr int APPEND_ROWS = 8;
 template <int ROWB>
 __global__ __launch_bounds__(256) void cache_append_kernel(const unsigned char *__restrict__ k, const unsigned char *__restrict__ v,
                                                            unsigned char *__restrict__ k_cache, unsigned char *__restrict__ v_cache, Pages pg,
                                                            Sequences seqs, const int *__restrict__ start) {
-    constexpr int CH = ROWB / 16;
+    constexpr int CH = ROWB / 16, TURNS = 4;
     const Block b = find_block<APPEND_ROWS>(seqs, blockIdx.x);
     if (b.at >= b.n) return;
-    const int s = b.seq, base = start ? start[s] : 0, n = min(b.n - b.at, APPEND_ROWS);
+    const int base = start ? start[b.seq] : 0, pieces = min(b.n - b.at, APPEND_ROWS) * pg.Hk * CH;
     if (base < 0) return;
     const size_t in = (static_cast<size_t>(b.lo) + b.at) * pg.Hk * ROWB;
-    for (int i = threadIdx.x; i < n * pg.Hk * CH; i += 256) {
-        const int c = i % CH, hk = i / CH % pg.Hk, r = i / CH / pg.Hk;
-        const int64_t pos = static_cast<int64_t>(base) + b.at + r;
-        if (pos >= pg.room()) continue;
-        const int id = pg.id(s, static_cast<int>(pos));
-        if (!pg.good(id)) continue;
-        const size_t to = pg.row(id, hk, static_cast<int>(pos)) * ROWB + c * 16, from = in + static_cast<size_t>(i) * 16;
-        *reinterpret_cast<u32x4_t *>(k_cache + to) = *reinterpret_cast<const u32x4_t *>(k + from);
-        *reinterpret_cast<u32x4_t *>(v_cache + to) = *reinterpret_cast<const u32x4_t *>(v + from);
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += 256 * TURNS) {
+        u32x4_t ks[TURNS], vs[TURNS];
+        size_t to[TURNS];
+        bool keep[TURNS];
+#pragma unroll
+        for (int n = 0; n < TURNS; ++n) {
+            const int i = min(i0 + 256 * n, pieces - 1), hk = i / CH % pg.Hk, r = i / CH / pg.Hk;
+            const int64_t pos = static_cast<int64_t>(base) + b.at + r;
+            ks[n] = *reinterpret_cast<const u32x4_t *>(k + in + static_cast<size_t>(i) * 16);
+            vs[n] = *reinterpret_cast<const u32x4_t *>(v + in + static_cast<size_t>(i) * 16);
+            keep[n] = i0 + 256 * n < pieces && pos < pg.room();
+            const int id = keep[n] ? pg.id(b.seq, static_cast<int>(pos)) : -1;
+            keep[n] = pg.good(id);
+            to[n] = keep[n] ? pg.row(id, hk, static_cast<int>(pos)) * ROWB + i % CH * 16 : 0;
+        }
+#pragma unroll
+        for (int n = 0; n < TURNS; ++n)
+            if (keep[n]) {
+                *reinterpret_cast<u32x4_t *>(k_cache + to[n]) = ks[n];
+                *reinterpret_cast<u32x4_t *>(v_cache + to[n]) = vs[n];
+            }
     }
 }
 
@@ -199,24 +212,41 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     }
 }
 
-// Joins the parts of a head: D / 4 threads to a head, in the parts' order.
+// Joins the parts of a head, a workgroup to a head: its threads take every GROUPS-th part's four columns each, and meet in LDS, always in the same
+// order.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(const float *__restrict__ part_o, const float *__restrict__ part_s, T *__restrict__ o,
-                                                            int rows, int parts) {
-    const int row = blockIdx.x * (1024 / D) + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
-    if (row >= rows) return;
-    const float *s = part_s + static_cast<size_t>(row) * parts * 2, *y = part_o + static_cast<size_t>(row) * parts * D + 4 * c;
+                                                            int parts) {
+    constexpr int GROUPS = 1024 / D;
+    __shared__ float sums[GROUPS];
+    __shared__ f32x4_t sh[GROUPS][D / 4];
+    const size_t row = blockIdx.x;
+    const int group = threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+    const float *s = part_s + row * parts * 2, *y = part_o + row * parts * D + 4 * c;
     float all = LOWEST, sum = 0.f;
-    for (int p = 0; p < parts; ++p) all = fmaxf(all, s[2 * p]);
+    for (int p = threadIdx.x & 63; p < parts; p += 64) all = fmaxf(all, s[2 * p]);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) all = fmaxf(all, __shfl_xor(all, off, 64));
     f32x4_t x = zero4();
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
+    for (int p = group; p < parts; p += GROUPS) {
         const float f = __builtin_amdgcn_exp2f(s[2 * p] - all);
         sum = fmaf(s[2 * p + 1], f, sum);
         x += *reinterpret_cast<const f32x4_t *>(y + static_cast<size_t>(p) * D) * f;
     }
+    sh[group][c] = x;
+    if (c == 0) sums[group] = sum;
+    __syncthreads();
+    if (group != 0) return;
+    x = zero4();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+        x += sh[i][c];
+        sum += sums[i];
+    }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    store4(o + static_cast<size_t>(row) * D + 4 * c, x * inv);
+    store4(o + row * D + 4 * c, x * inv);
 }
 
 Pages pages_of(const CacheCall &c) {
@@ -236,9 +266,8 @@ hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *
                        static_cast<T *>(c.v_cache), pages_of(c), lens, static_cast<T *>(o), part_o, part_s, H, parts, window, scale * LOG2E);
     err = hipGetLastError();
     if (err != hipSuccess || parts == 1) return err;
-    const int rows = B * H, per = 1024 / D;
-    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((rows + per - 1) / per), dim3(256), 0, stream, part_o, part_s, static_cast<T *>(o),
-                       rows, parts);
+    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(static_cast<unsigned>(B) * H), dim3(256), 0, stream, part_o, part_s,
+                       static_cast<T *>(o), parts);
     return hipGetLastError();
 }
 
