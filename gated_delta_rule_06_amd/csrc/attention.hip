@@ -32,6 +32,7 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     constexpr int WAVES = C::WAVES, KEYS = C::KEYS, TILE = C::TILE, NT = KEYS / 32, QS = D / 16, NO = D / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, H, Hk);
     const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);  // late blocks of a sequence first: they see the most keys
     if (b.at >= b.rows) return;
@@ -62,12 +63,14 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
 
     const int r0 = b.at + 32 * wv;  // the wavefront's first query
     auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
+        ln.again();
         f32x16_t x[NT] = {};
 #pragma unroll
         for (int s = 0; s < QS; ++s)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) x[t] = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, lane), qf[s], x[t]);
+            for (int t = 0; t < NT; ++t) x[t] = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, ln), qf[s], x[t]);
         if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window)) {  // some key that some query does not see
+            KEEP_BRANCH;
             const int last = q_row - j * KEYS - 4 * half, first_seen = window ? last - window : -1000;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
             for (int s = 0; s < 2; ++s) {
                 const auto p = acc_frag<T>(x[t], s);
 #pragma unroll
-                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(vt, 32 * t + 16 * s, 32 * n, lane), p, acc[n]);
+                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(vt, 32 * t + 16 * s, 32 * n, ln), p, acc[n]);
             }
         }
         l += sum[0] + sum[1];

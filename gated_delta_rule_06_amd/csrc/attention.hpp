@@ -79,35 +79,51 @@ template <typename T, int D> struct Tile {
     }
     static __device__ __forceinline__ int at(int r, int chunk) { return r * ROWB + ((chunk ^ swz(r)) << 4); }
 
+    // A lane's place in the two kinds of operand below, for rows and columns 0 on; the others are an exclusive or with a constant and a constant
+    // offset away, since whole powers of two of pieces are. `again` makes the compiler form those anew where it is called: kept in
+    // registers they cost sixteen of them.
+    template <int R> struct Lane {
+        int row, col;
+        __device__ __forceinline__ explicit Lane(int lane) {
+            const int m = lane % 16, g = lane / R;
+            row = at(lane % R, g * int(sizeof(T)) / 2);
+            if constexpr (sizeof(T) == 2) {
+                const int b = 2 * (lane % R / 16 * 16) + 8 * (m & 3);
+                col = at(4 * g + (m >> 2), b >> 4) + (b & 8);
+            } else {
+                col = at(4 * g, lane % R >> 2) + 4 * (lane & 3);
+            }
+        }
+        __device__ __forceinline__ void again() { asm volatile("" : "+v"(row), "+v"(col)); }
+    };
+
     // Operand rows r0 + l % R, contraction values 16 s + 8 (l / 32) + j (32 rows) or 32 s + 8 (l / 16) + j (16 rows).
-    template <int R> static __device__ __forceinline__ typename Op<T>::frag row(const unsigned char *t, int r0, int s, int lane) {
-        const int r = lane % R, c = (s * (64 / R) + lane / R) * int(sizeof(T)) / 2;  // its first 16-byte piece
+    template <int R> static __device__ __forceinline__ typename Op<T>::frag row(const unsigned char *t, int r0, int s, const Lane<R> &ln) {
         const unsigned char *p = t + r0 * ROWB;
+        const int x = ln.row ^ (s * (64 / R) * int(sizeof(T)) / 2 << 4);
         if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const bf16x8_t *>(p + at(r, c));
+            return *reinterpret_cast<const bf16x8_t *>(p + x);
         } else {
-            const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p + at(r, c)), b = *reinterpret_cast<const f32x4_t *>(p + at(r, c + 1));
+            const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p + x), b = *reinterpret_cast<const f32x4_t *>(p + (x ^ 16));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
     // Operand rows are the tile's columns c0 + l % R; element j is tile row r0 + 4 (l / R) + j % 4, and 256 / R rows on
     // for j >= 4: the order in which two 4-row groups of an accumulator lie in a lane. r0 is a multiple of 16.
-    template <int R> static __device__ __forceinline__ typename Op<T>::frag col(unsigned char *t, int r0, int c0, int lane) {
-        constexpr int NEXT = 256 / R;
-        const int g = lane / R;
+    template <int R> static __device__ __forceinline__ typename Op<T>::frag col(unsigned char *t, int r0, int c0, const Lane<R> &ln) {
+        constexpr int NEXT = 256 / R, FLIP = R == 32 ? 2 << 4 : 0;  // of the permutation, eight rows on
         unsigned char *p = t + r0 * ROWB;
+        const int x = ln.col ^ (c0 * int(sizeof(T)) >> 4 << 4);
         if constexpr (sizeof(T) == 2) {
             // The transposing read gives lane m of sixteen the column m of the four rows whose 32 bytes the lanes address.
-            const int m = lane % 16, r = 4 * g + (m >> 2), b = 2 * (c0 + (lane % R) / 16 * 16) + 8 * (m & 3);
-            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (at(r, b >> 4) + (b & 8))));
-            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (at(r + NEXT, b >> 4) + (b & 8))));
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + x));
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + NEXT * ROWB + (x ^ FLIP)));
             return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const int c = c0 + lane % R;
             typename Op<T>::frag f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                f[j] = *reinterpret_cast<const float *>(p + at(4 * g + j % 4 + j / 4 * NEXT, c >> 2) + 4 * (c & 3));
+                f[j] = *reinterpret_cast<const float *>(p + (j % 4 + j / 4 * NEXT) * ROWB + (x ^ (j % 4 << 6) ^ (j / 4 * FLIP)));
             return f;
         }
     }
@@ -130,6 +146,9 @@ template <typename T, int D> struct Tile {
         }
     }
 };
+
+// Keeps what follows it in a branch there: the compiler would rather make selects of it for everybody.
+#define KEEP_BRANCH asm volatile("")
 
 // Waits for every load of this wavefront; the barrier behind it makes all wavefronts' tiles visible.
 __device__ __forceinline__ void loads_done() {

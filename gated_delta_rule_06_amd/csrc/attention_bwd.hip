@@ -46,11 +46,14 @@ template <typename T, int D> struct Bwd {
     static_assert(ROWS == ATTENTION_ROWS && 4 * TILE >= ROWS * D * int(sizeof(T)), "the outputs pass through the tiles' room");
 };
 
-// dq, and for the next kernel lse in base 2 and D, [H][N] each; a row without keys gets an lse of +infinity, so its p are zero.
+// Whether a score's sum begins at -lse / scale, or at 0 and -lse is added to the exponent.
+template <typename T> constexpr bool FROM_LSE = sizeof(T) == 2;
+
+// dq, and for the next kernel [H][N] of -lse (over the scale, or in base 2) and -D; a row without keys gets -infinity, so its p are zero.
 template <typename T, int D>
 __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention_dq_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ o, const T *__restrict__ dout,
-    const float *__restrict__ lse, Sequences seqs, T *__restrict__ dq, float *__restrict__ lse2, float *__restrict__ delta, int blocks,
+    const float *__restrict__ lse, Sequences seqs, T *__restrict__ dq, float *__restrict__ tops, float *__restrict__ deltas, int blocks,
     int H, int Hk, int window, float scale) {
     using C = Bwd<T, D>;
     using Ti = Tile<T, D>;
@@ -58,6 +61,7 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     constexpr int WAVES = C::WAVES, KEYS = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, H, Hk);
     const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);
     if (b.at >= b.rows) return;
@@ -89,27 +93,35 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
         for (int j = 0; j < 8; ++j) d = fmaf(Op<T>::get(of, j), Op<T>::get(df[s], j), d);
     }
     d = halves_sum(d);
-    const float l = lse[own] * LOG2E;
+    const float l = lse[own];
     const bool live = q_row < b.n && l != -INFINITY;
-    const float top = live ? l : INFINITY;
+    const float top = live ? FROM_LSE<T> ? -l / scale : -l * LOG2E : -INFINITY;
+    d = live ? d : 0.f;
     if (half == 0 && q_row < b.rows) {
         const size_t i = static_cast<size_t>(it.h) * seqs.N + b.lo + q_row;
-        lse2[i] = top;
-        delta[i] = live ? d : 0.f;
+        tops[i] = top;
+        deltas[i] = -d;
     }
     f32x16_t acc[NO] = {};
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
+        ln.again();
         const bool masked = (j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window);
 #pragma unroll
         for (int t = 0; t < KEYS / 32; ++t) {
-            f32x16_t x = {}, y = {};
+            f32x16_t x = {}, y;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if constexpr (FROM_LSE<T>) x[i] = top;
+                y[i] = -d;
+            }
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
-                x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, lane), qf[s], x);
-                y = Op<T>::mma(Ti::template row<32>(vt, 32 * t, s, lane), df[s], y);
+                x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, ln), qf[s], x);
+                y = Op<T>::mma(Ti::template row<32>(vt, 32 * t, s, ln), df[s], y);
             }
             if (masked) {
+                KEEP_BRANCH;
                 const int last = q_row - j * KEYS - 32 * t - 4 * half, first_seen = window ? last - window : -1000;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -118,12 +130,12 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, -top)) * (y[i] - d);
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(FROM_LSE<T> ? x[i] * scale2 : fmaf(x[i], scale2, top)) * y[i];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const frag f = acc_frag<T>(x, s);
 #pragma unroll
-                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(kt, 32 * t + 16 * s, 32 * n, lane), f, acc[n]);
+                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(kt, 32 * t + 16 * s, 32 * n, ln), f, acc[n]);
             }
         }
     };
@@ -146,9 +158,9 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
 // dk and dv of 128 keys of a key head, 32 to a wavefront, whose keys and values stay in registers, over the queries of all its heads. Scores have
 // queries as rows, so p and ds are the operands of dv^T += do^T p and dk^T += q^T ds as they are.
 template <typename T, int D>
-__global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
-    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse2,
-    const float *__restrict__ delta, Sequences seqs, T *__restrict__ dk, T *__restrict__ dv, int blocks, int H, int Hk, int window,
+__global__ __launch_bounds__(256, (sizeof(T) == 2 ? 2 : 1)) void attention_dkv_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ tops,
+    const float *__restrict__ deltas, Sequences seqs, T *__restrict__ dk, T *__restrict__ dv, int blocks, int H, int Hk, int window,
     float scale) {
     using C = Bwd<T, D>;
     using Ti = Tile<T, D>;
@@ -157,6 +169,7 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
     extern __shared__ __align__(16) unsigned char smem[];
     float *stats = reinterpret_cast<float *>(smem + 4 * TILE);
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, Hk, Hk);
     const Block b = find_block<C::ROWS>(seqs, it.block);
     if (b.at >= b.rows) return;
@@ -175,7 +188,7 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
         Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE, q + (row * H + h) * D, q_stride, left, wv, lane);
         Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE + TILE, dout + (row * H + h) * D, q_stride, left, wv, lane);
         if (wv < 2) {
-            const rsrc_t r = make_rsrc((wv ? delta : lse2) + static_cast<size_t>(h) * seqs.N + row, min(left, QR) * 4u);
+            const rsrc_t r = make_rsrc((wv ? deltas : tops) + static_cast<size_t>(h) * seqs.N + row, min(left, QR) * 4u);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stats + (buf * 2 + wv) * 64), 4, lane * 4, 0, 0, 0);
         }
     };
@@ -191,13 +204,26 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
     f32x16_t dka[NO] = {}, dva[NO] = {};
 
     auto step = [&](int row0, unsigned char *qt, unsigned char *dt, const float *st) __attribute__((always_inline)) {
-        f32x16_t x = {}, y = {};
+        ln.again();
+        // The sums begin at -lse / scale and -D of their rows, so that no subtraction is left. In float32 x begins at 0: its sum's
+        // roundings would be as large as lse makes them.
+        f32x16_t x = {}, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4_t l = *reinterpret_cast<const f32x4_t *>(st + 8 * i + 4 * half), d = *reinterpret_cast<const f32x4_t *>(st + 64 + 8 * i + 4 * half);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (FROM_LSE<T>) x[4 * i + r] = l[r];
+                y[4 * i + r] = d[r];
+            }
+        }
 #pragma unroll
         for (int s = 0; s < QS; ++s) {
-            x = Op<T>::mma(Ti::template row<32>(qt, 0, s, lane), kf[s], x);
-            y = Op<T>::mma(Ti::template row<32>(dt, 0, s, lane), vf[s], y);
+            x = Op<T>::mma(Ti::template row<32>(qt, 0, s, ln), kf[s], x);
+            y = Op<T>::mma(Ti::template row<32>(dt, 0, s, ln), vf[s], y);
         }
         if (row0 < k0 + 31 || row0 + 31 >= b.n || (window && row0 + 31 - k0 >= window)) {  // some query that does not see some key
+            KEEP_BRANCH;
             const int from = key - row0 - 4 * half, to = min(b.n - row0 - 4 * half, window ? from + window : 1000);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -206,21 +232,20 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4_t l = *reinterpret_cast<const f32x4_t *>(st + 8 * i + 4 * half), d = *reinterpret_cast<const f32x4_t *>(st + 64 + 8 * i + 4 * half);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[4 * i + r] = __builtin_amdgcn_exp2f(fmaf(x[4 * i + r], scale2, -l[r]));
-                y[4 * i + r] = x[4 * i + r] * (y[4 * i + r] - d[r]);
-            }
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (FROM_LSE<T>)
+                x[i] = __builtin_amdgcn_exp2f(x[i] * scale2);
+            else
+                x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, st[8 * (i / 4) + 4 * half + i % 4]));
+            y[i] *= x[i];
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const frag p = acc_frag<T>(x, s), ds = acc_frag<T>(y, s);
 #pragma unroll
             for (int n = 0; n < NO; ++n) {
-                dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, lane), p, dva[n]);
-                dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, lane), ds, dka[n]);
+                dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, ln), p, dva[n]);
+                dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, ln), ds, dka[n]);
             }
         }
     };
@@ -257,13 +282,13 @@ template <typename T, int D> hipError_t launch(const AttentionCall &c, const Att
     const int blocks = static_cast<int>(attention_blocks(c.N, c.S));
     const Sequences s{c.offsets, c.lens, c.N, c.S};
     const T *q = static_cast<const T *>(c.q), *k = static_cast<const T *>(c.k), *v = static_cast<const T *>(c.v), *d = static_cast<const T *>(g.dout);
-    float *lse2 = static_cast<float *>(workspace), *delta = lse2 + up256(static_cast<size_t>(c.N) * c.H * 4) / 4;
+    float *tops = static_cast<float *>(workspace), *deltas = tops + up256(static_cast<size_t>(c.N) * c.H * 4) / 4;
     hipLaunchKernelGGL((attention_dq_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * B::WAVES), LDS, stream, q, k, v,
-                       static_cast<const T *>(g.o), d, g.lse, s, static_cast<T *>(g.dq), lse2, delta, blocks, c.H, c.Hk, c.window, c.scale);
+                       static_cast<const T *>(g.o), d, g.lse, s, static_cast<T *>(g.dq), tops, deltas, blocks, c.H, c.Hk, c.window, c.scale);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     hipLaunchKernelGGL((attention_dkv_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), LDS + B::STATS, stream,
-                       q, k, v, d, lse2, delta, s, static_cast<T *>(g.dk), static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
+                       q, k, v, d, tops, deltas, s, static_cast<T *>(g.dk), static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
     return hipGetLastError();
 }
 

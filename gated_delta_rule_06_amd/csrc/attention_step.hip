@@ -72,6 +72,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     const int G = H / pg.Hk, sets = (G + 15) / 16;
     const int part = blockIdx.x % parts, set = blockIdx.x / parts % sets, bh = blockIdx.x / parts / sets, hk = bh % pg.Hk, b = bh / pg.Hk;
     const int h0 = hk * G + set * 16, heads = min(G - set * 16, 16);
+    const typename Ti::template Lane<16> ln(lane);
     unsigned char *ring = smem + wv * C::RING;
 
     const Span span = step_span(lens[b], kn != nullptr, window, pg.room());
@@ -141,7 +142,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
 #pragma unroll
         for (int s = 0; s < QS; ++s)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) x[u] = Op<T>::mma16(Ti::template row<16>(kt, 16 * u, s, lane), qf[s], x[u]);
+            for (int u = 0; u < 2; ++u) x[u] = Op<T>::mma16(Ti::template row<16>(kt, 16 * u, s, ln), qf[s], x[u]);
         if (p0 < begin || p0 + 32 > n || good != 3) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -170,7 +171,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
             }
         const frag p = Op<T>::pack(x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]);
 #pragma unroll
-        for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, lane), p, acc[i]);
+        for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, ln), p, acc[i]);
         wave_lds_sync();  // the tile is free
     }
     l += __shfl_xor(l, 16, 64);
