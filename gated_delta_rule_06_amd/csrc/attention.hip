@@ -17,17 +17,21 @@ namespace {
 
 using namespace at;
 
-template <typename T, int D> struct Fwd {
-    static constexpr int WAVES = 4, ROWS = 32 * WAVES, KEYS = sizeof(T) == 2 ? 64 : 32;
-    static constexpr int TILE = KEYS * D * int(sizeof(T)), LDS = 4 * TILE;
-    static_assert(ROWS == ATTENTION_ROWS && LDS >= ROWS * D * int(sizeof(T)), "the outputs pass through the tiles' room");
+// SPLIT: a workgroup has 32 rows, and its wavefronts every WAVES-th tile of their keys, each in tiles of its own; they meet at the end. There a wavefront has
+// one tile of keys and one of values, and loads the next keys while it multiplies values, the next values while it multiplies keys.
+template <typename T, int D, bool SPLIT> struct Fwd {
+    static constexpr int WAVES = 4, ROWS = SPLIT ? 32 : 128;
+    static constexpr int KEYS = D == 64 && !SPLIT ? 64 : 32, TILE = KEYS * D * int(sizeof(T));
+    static constexpr int STATS = SPLIT ? (2 * WAVES + 1) * 32 * 4 : 0, LDS = (SPLIT ? 2 * WAVES : 4) * TILE + STATS;
+    static constexpr int PER_CU = sizeof(T) * D == 512 ? 1 : SPLIT || KEYS == 64 ? 2 : 3;  // workgroups that registers are kept free for
+    static_assert(LDS - STATS >= ROWS * D * int(sizeof(T)) && (!SPLIT || 2 * TILE >= 32 * D * 4), "the outputs pass through the tiles' room");
 };
 
-template <typename T, int D>
-__global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention_fwd_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                                                            Sequences seqs, T *__restrict__ o, float *__restrict__ lse, int blocks,
-                                                            int H, int Hk, int window, float scale2) {
-    using C = Fwd<T, D>;
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__((64 * Fwd<T, D, SPLIT>::WAVES), (Fwd<T, D, SPLIT>::PER_CU)) void attention_fwd_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, Sequences seqs, T *__restrict__ o, float *__restrict__ lse,
+    int blocks, int H, int Hk, int window, float scale2) {
+    using C = Fwd<T, D, SPLIT>;
     using Ti = Tile<T, D>;
     constexpr int WAVES = C::WAVES, KEYS = C::KEYS, TILE = C::TILE, NT = KEYS / 32, QS = D / 16, NO = D / 32;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -37,38 +41,41 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);  // late blocks of a sequence first: they see the most keys
     if (b.at >= b.rows) return;
     const int hk = it.h / (H / Hk);
-    const size_t row0 = static_cast<size_t>(b.lo) + b.at;  // of the block
     const uint32_t kv_stride = uint32_t(Hk) * Ti::ROWB;
-    const int q_row = b.at + 32 * wv + (lane & 31);  // this lane's query, as a place in its sequence
+    const int r0 = b.at + (SPLIT ? 0 : 32 * wv), q_row = r0 + (lane & 31);  // the wavefront's first query and the lane's, as places in the sequence
 
     const int end = min(b.at + C::ROWS, b.n);                        // keys that the block's rows see
     const int first = window ? max(b.at - window + 1, 0) / KEYS : 0;  // tile of the first one
     const int tiles = b.at < b.n ? (end + KEYS - 1) / KEYS : first;   // none for rows that are no tokens
     const T *kb = k + (static_cast<size_t>(b.lo) * Hk + hk) * D, *vb = v + (static_cast<size_t>(b.lo) * Hk + hk) * D;
-    auto fetch = [&](int j, int buf) {
-        const size_t at = static_cast<size_t>(j) * KEYS * Hk * D;
-        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE, kb + at, kv_stride, b.n - j * KEYS, wv, lane);
-        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE + TILE, vb + at, kv_stride, b.n - j * KEYS, wv, lane);
+    unsigned char *tile = smem + (SPLIT ? wv * 2 * TILE : 0);
+    auto fetch_one = [&](const T *rows, int j, unsigned char *to) {
+        Ti::template fetch<KEYS, SPLIT ? 1 : WAVES>(to, rows + static_cast<size_t>(j) * KEYS * Hk * D, kv_stride, b.n - j * KEYS, SPLIT ? 0 : wv, lane);
     };
-    if (first < tiles) fetch(first, 0);
+    auto fetch = [&](int j, int buf) {
+        fetch_one(kb, j, tile + buf * 2 * TILE);
+        fetch_one(vb, j, tile + buf * 2 * TILE + TILE);
+    };
+    const int from = first + (SPLIT ? wv : 0);
+    if (from < tiles) fetch(from, 0);
 
     typename Op<T>::frag qf[QS];
     {
-        const T *p = q + (row0 + min(32 * wv + (lane & 31), b.rows - b.at - 1)) * H * D + static_cast<size_t>(it.h) * D + 8 * half;
+        const T *p = q + ((static_cast<size_t>(b.lo) + min(q_row, b.rows - 1)) * H + it.h) * D + 8 * half;
 #pragma unroll
         for (int s = 0; s < QS; ++s) qf[s] = load8<T>(p + 16 * s);
     }
     f32x16_t acc[NO] = {};
     float m = LOWEST, l = 0.f;  // base 2, with the scale in
 
-    const int r0 = b.at + 32 * wv;  // the wavefront's first query
-    auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
+    auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto keys_done, auto values_needed) __attribute__((always_inline)) {
         ln.again();
         f32x16_t x[NT] = {};
 #pragma unroll
         for (int s = 0; s < QS; ++s)
 #pragma unroll
             for (int t = 0; t < NT; ++t) x[t] = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, ln), qf[s], x[t]);
+        keys_done();
         if ((j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window)) {  // some key that some query does not see
             KEEP_BRANCH;
             const int last = q_row - j * KEYS - 4 * half, first_seen = window ? last - window : -1000;
@@ -103,6 +110,7 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], scale2, -m));
                 sum[i & 1] += x[t][i];
             }
+            if (t == 0) values_needed();
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const auto p = acc_frag<T>(x[t], s);
@@ -112,52 +120,91 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
         }
         l += sum[0] + sum[1];
     };
-    auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
-        constexpr int buf = decltype(buffer)::value;
-        loads_done();  // tile j is there, and every wavefront has left the other one
-        if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
-        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;  // the wavefront sees nothing of the tile
-        step(j, smem + buf * 2 * TILE, smem + buf * 2 * TILE + TILE);
-    };
-    for (int j = first; j < tiles; j += 2) {
-        turn(j, std::integral_constant<int, 0>{});
-        if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
+    if constexpr (SPLIT) {
+        constexpr int LOADS = KEYS / Ti::RPI;  // of one tile
+        for (int j = from; j < tiles; j += WAVES) {
+            const bool more = j + WAVES < tiles;
+            own_loads_done<LOADS>();  // the values were asked for after the keys
+            step(
+                j, tile, tile + TILE,
+                [&]() __attribute__((always_inline)) {
+                    own_reads_done();
+                    if (more) fetch_one(kb, j + WAVES, tile);
+                },
+                [&]() __attribute__((always_inline)) {
+                    if (more)
+                        own_loads_done<LOADS>();
+                    else
+                        own_loads_done<0>();
+                });
+            own_reads_done();
+            if (more) fetch_one(vb, j + WAVES, tile + TILE);
+        }
+    } else {
+        auto nothing = [] {};
+        auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
+            constexpr int buf = decltype(buffer)::value;
+            loads_done();  // tile j is there, and every wavefront has left the other one
+            if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
+            if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;  // the wavefront sees nothing of the tile
+            step(j, tile + buf * 2 * TILE, tile + buf * 2 * TILE + TILE, nothing, nothing);
+        };
+        for (int j = from; j < tiles; j += 2) {
+            turn(j, std::integral_constant<int, 0>{});
+            if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
+        }
     }
 
     l = halves_sum(l);
     const bool live = q_row < b.n;
-    const float inv = live && l != 0.f ? 1.f / l : 0.f;
-    if (half == 0 && q_row < b.rows && lse)
-        lse[(static_cast<size_t>(b.lo) + q_row) * H + it.h] = live && l != 0.f ? (m + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
-    lds_barrier();  // the tiles are free
-    unsigned char *out = smem + wv * 32 * Ti::ROWB;
-#pragma unroll
-    for (int n = 0; n < NO; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f32x4_t y;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = live ? acc[n][4 * i + r] * inv : 0.f;
-            Ti::put4(out, lane & 31, 32 * n + 8 * i + 4 * half, y);
+    float *stats = reinterpret_cast<float *>(smem + C::LDS - C::STATS);
+    if constexpr (SPLIT) {
+        if (half == 0) {
+            stats[64 * wv + lane] = m;
+            stats[64 * wv + 32 + lane] = l;
         }
-    wave_lds_sync();
+        lds_barrier();  // and all tiles are free
+        const float own = m;
+        l = 0.f;
 #pragma unroll
-    for (int n = 0; n < 32 / Ti::RPI; ++n) {
-        const int r = n * Ti::RPI + lane / Ti::CH, c = lane % Ti::CH;
-        if (b.at + 32 * wv + r < b.rows)
-            *reinterpret_cast<u32x4_t *>(o + ((row0 + 32 * wv + r) * H + it.h) * D + c * (16 / sizeof(T))) = *reinterpret_cast<const u32x4_t *>(out + Ti::at(r, c));
+        for (int w = 0; w < WAVES; ++w) m = fmaxf(m, stats[64 * w + (lane & 31)]);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) l = fmaf(stats[64 * w + 32 + (lane & 31)], __builtin_amdgcn_exp2f(stats[64 * w + (lane & 31)] - m), l);
+        const float f = __builtin_amdgcn_exp2f(own - m);
+#pragma unroll
+        for (int n = 0; n < NO; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[n][i] *= f;
+    }
+    const float inv = live && l != 0.f ? 1.f / l : 0.f;
+    if (half == 0 && q_row < b.rows && (!SPLIT || wv == 0)) {
+        if (lse) lse[(static_cast<size_t>(b.lo) + q_row) * H + it.h] = live && l != 0.f ? (m + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
+        if constexpr (SPLIT) stats[64 * WAVES + lane] = inv;
+    }
+    T *out = o + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D;
+    if constexpr (SPLIT) {
+        store_sums<T, D, WAVES>(smem, acc, [&](int r) { return stats[64 * WAVES + r]; }, out, static_cast<size_t>(H) * D, b.rows - r0, wv, lane);
+    } else {
+        lds_barrier();  // the tiles are free
+        store_rows<T, D>(smem + wv * 32 * Ti::ROWB, acc, inv, inv != 0.f, out, static_cast<size_t>(H) * D, b.rows - r0, lane);
     }
 }
 
-template <typename T, int D> hipError_t launch(const AttentionCall &c, void *o, float *lse, hipStream_t stream) {
-    using F = Fwd<T, D>;
-    const hipError_t err = allow_lds<&attention_fwd_kernel<T, D>>(F::LDS);
+template <typename T, int D, bool SPLIT> hipError_t launch(const AttentionCall &c, void *o, float *lse, hipStream_t stream) {
+    using F = Fwd<T, D, SPLIT>;
+    const hipError_t err = allow_lds<&attention_fwd_kernel<T, D, SPLIT>>(F::LDS);
     if (err != hipSuccess) return err;
-    const int blocks = static_cast<int>(attention_blocks(c.N, c.S));
-    hipLaunchKernelGGL((attention_fwd_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * F::WAVES), F::LDS, stream,
+    const int blocks = c.N / F::ROWS + c.S + 1;
+    hipLaunchKernelGGL((attention_fwd_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * F::WAVES), F::LDS, stream,
                        static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v),
                        Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(o), lse, blocks, c.H, c.Hk, c.window, c.scale * LOG2E);
     return hipGetLastError();
+}
+
+template <typename T, int D> hipError_t launch(const AttentionCall &c, void *o, float *lse, hipStream_t stream) {
+    if constexpr (sizeof(T) == 2)
+        if (!attention_split(c.N, c.S, c.H)) return launch<T, D, false>(c, o, lse, stream);
+    return launch<T, D, true>(c, o, lse, stream);
 }
 
 }  // namespace

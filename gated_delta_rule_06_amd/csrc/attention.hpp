@@ -156,6 +156,11 @@ __device__ __forceinline__ void loads_done() {
     lds_barrier();
 }
 
+// Waits until at most `LEFT` of this wavefront's loads are out: the ones before them, into a tile of its own, are done.
+template <int LEFT> __device__ __forceinline__ void own_loads_done() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory"); }
+// Before new loads into a tile of this wavefront's own: its reads of the old one are done.
+__device__ __forceinline__ void own_reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // Largest and sum over the two halves of a wavefront, which hold the same columns.
 __device__ __forceinline__ float halves_max(float x) {
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -171,6 +176,55 @@ __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i / 4) + 4
 // Eight accumulators as the operand of step s (of two).
 template <typename T> __device__ __forceinline__ typename Op<T>::frag acc_frag(const f32x16_t &x, int s) {
     return Op<T>::pack(x[8 * s], x[8 * s + 1], x[8 * s + 2], x[8 * s + 3], x[8 * s + 4], x[8 * s + 5], x[8 * s + 6], x[8 * s + 7]);
+}
+
+// A wavefront's 32 rows, given transposed in accumulators, through its own LDS room to `rows` rows of `stride` elements, times f; zeros where not live.
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(unsigned char *room, const f32x16_t (&acc)[D / 32], float f, bool live, T *out, size_t stride, int rows,
+                                           int lane) {
+    using Ti = Tile<T, D>;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4_t y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = live ? acc[n][4 * i + r] * f : 0.f;
+            Ti::put4(room, lane & 31, 32 * n + 8 * i + 4 * (lane >> 5), y);
+        }
+    wave_lds_sync();
+#pragma unroll
+    for (int n = 0; n < 32 / Ti::RPI; ++n) {
+        const int r = n * Ti::RPI + lane / Ti::CH, c = lane % Ti::CH;
+        if (r < rows)
+            *reinterpret_cast<u32x4_t *>(out + r * stride + c * (16 / sizeof(T))) = *reinterpret_cast<const u32x4_t *>(room + Ti::at(r, c));
+    }
+    wave_lds_sync();
+}
+// The same where the wavefronts of a workgroup have summands of the same 32 rows: they are added in the wavefronts' order. `factor` is of a row. The
+// room, which nobody else may be using, is 32 D floats a wavefront.
+template <typename T, int D, int WAVES, typename F>
+__device__ __forceinline__ void store_sums(unsigned char *room, const f32x16_t (&acc)[D / 32], F factor, T *out, size_t stride, int rows, int wv,
+                                           int lane) {
+    using Ti = Tile<float, D>;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            Ti::put4(room + wv * 32 * Ti::ROWB, lane & 31, 32 * n + 8 * i + 4 * (lane >> 5),
+                     f32x4_t{acc[n][4 * i], acc[n][4 * i + 1], acc[n][4 * i + 2], acc[n][4 * i + 3]});
+    lds_barrier();
+    for (int i = threadIdx.x; i < 32 * (D / 4); i += 64 * WAVES) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        f32x4_t y = zero4();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) y += *reinterpret_cast<const f32x4_t *>(room + w * 32 * Ti::ROWB + Ti::at(r, c));
+        const float f = factor(r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = f != 0.f ? y[e] * f : 0.f;
+        if (r < rows) store4(out + r * stride + 4 * c, y);
+    }
+    lds_barrier();
 }
 
 struct Block {

@@ -28,7 +28,7 @@ muir_status_t check_rows(const char *fn, int N, int S, const int *offsets, int p
     if (N < 0 || S < 1) return fail(MUIR_ERR_SHAPE, "%s: need N >= 0 and S >= 1 (got %d, %d)", fn, N, S);
     if (!offsets && N % S != 0) return fail(MUIR_ERR_SHAPE, "%s: without offsets N=%d must be a multiple of S=%d", fn, N, S);
     if (N > kMaxRows) return fail(MUIR_ERR_UNSUPPORTED, "%s: N above 2^30", fn);
-    if ((static_cast<long long>(N) / per_block + S + 1) * heads > kMaxBlocks)
+    if (attention_blocks(N, S, per_block) * heads > kMaxBlocks)
         return fail(MUIR_ERR_UNSUPPORTED, "%s: too many rows, sequences and heads for a call; split it", fn);
     return MUIR_OK;
 }
@@ -63,7 +63,7 @@ muir_status_t muir_attention_fwd(const void *q, const void *k, const void *v, co
                                  int N, int S, int H, int Hk, int d, int window, float scale, muir_dtype_t qkv, muir_stream_t stream) {
     const char *fn = "attention_fwd";
     muir_status_t st = check_heads(fn, H, Hk, d, qkv);
-    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, ATTENTION_ROWS, H);
+    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, qkv == MUIR_BF16 ? 128 : 32, H);
     if (st == MUIR_OK) st = check_scores(fn, window, scale);
     if (st != MUIR_OK) return st;
     if (N == 0) return ok();
@@ -80,7 +80,7 @@ muir_status_t muir_attention_fwd(const void *q, const void *k, const void *v, co
 
 size_t muir_attention_bwd_workspace_size(int N, int S, int H, int Hk, int d, muir_dtype_t qkv) {
     if (N < 0 || S < 1 || H < 1 || Hk < 1 || H % Hk != 0 || H > kMaxH || (d != 64 && d != 128) || !known(qkv) ||
-        N > kMaxRows || attention_blocks(N, S) * H > kMaxBlocks)
+        N > kMaxRows || attention_blocks(N, S, qkv == MUIR_BF16 ? 128 : 32) * H > kMaxBlocks)
         return 0;
     return attention_bwd_workspace_bytes(N, H);
 }
@@ -91,7 +91,7 @@ muir_status_t muir_attention_bwd(const void *q, const void *k, const void *v, co
                                  muir_stream_t stream) {
     const char *fn = "attention_bwd";
     muir_status_t st = check_heads(fn, H, Hk, d, qkv);
-    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, ATTENTION_ROWS, H);
+    if (st == MUIR_OK) st = check_rows(fn, N, S, offsets, qkv == MUIR_BF16 ? 128 : 32, H);
     if (st == MUIR_OK) st = check_scores(fn, window, scale);
     if (st != MUIR_OK) return st;
     if (N == 0) return ok();

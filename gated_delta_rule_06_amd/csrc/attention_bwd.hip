@@ -16,46 +16,26 @@ namespace {
 
 using namespace at;
 
-// Writes a wavefront's 32 rows, given transposed in accumulators, through its LDS room to rows of `stride` elements.
-template <typename T, int D>
-__device__ __forceinline__ void store_rows(unsigned char *room, const f32x16_t (&acc)[D / 32], float f, bool live, T *out, size_t stride,
-                                           int rows, int lane) {
-    using Ti = Tile<T, D>;
-#pragma unroll
-    for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f32x4_t y;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = live ? acc[n][4 * i + r] * f : 0.f;
-            Ti::put4(room, lane & 31, 32 * n + 8 * i + 4 * (lane >> 5), y);
-        }
-    wave_lds_sync();
-#pragma unroll
-    for (int n = 0; n < 32 / Ti::RPI; ++n) {
-        const int r = n * Ti::RPI + lane / Ti::CH, c = lane % Ti::CH;
-        if (r < rows)
-            *reinterpret_cast<u32x4_t *>(out + r * stride + c * (16 / sizeof(T))) = *reinterpret_cast<const u32x4_t *>(room + Ti::at(r, c));
-    }
-    wave_lds_sync();
-}
-
-template <typename T, int D> struct Bwd {
-    static constexpr int WAVES = 4, ROWS = 32 * WAVES, STEP = sizeof(T) == 2 ? 64 : 32;  // rows of the tiles walked over
-    static constexpr int TILE = STEP * D * int(sizeof(T)), STATS = 4 * 64 * 4;           // two of lse and of D
-    static_assert(ROWS == ATTENTION_ROWS && 4 * TILE >= ROWS * D * int(sizeof(T)), "the outputs pass through the tiles' room");
+// SPLIT: a workgroup has 32 rows, and its wavefronts every WAVES-th tile of what they walk over, each in two tiles of its own, which are loaded anew as
+// soon as their last product has read them; their sums meet at the end.
+template <typename T, int D, bool SPLIT> struct Bwd {
+    static constexpr int WAVES = 4, ROWS = SPLIT ? 32 : 128;
+    static constexpr int STEP = SPLIT ? 32 : 64, TILE = STEP * D * int(sizeof(T));  // rows of the tiles walked over
+    static constexpr int LDS = (SPLIT ? 2 * WAVES : 4) * TILE, STATS = (SPLIT ? 2 * WAVES : 4) * 64 * 4;  // lse and D, of as many tiles
+    static constexpr int DQ_PER_CU = sizeof(T) * D == 512 ? 1 : 2, DKV_PER_CU = sizeof(T) * D == 512 ? 1 : 2;
+    static_assert(LDS >= ROWS * D * int(sizeof(T)) && (!SPLIT || 2 * TILE >= 32 * D * 4), "the outputs pass through the tiles' room");
 };
 
 // Whether a score's sum begins at -lse / scale, or at 0 and -lse is added to the exponent.
 template <typename T> constexpr bool FROM_LSE = sizeof(T) == 2;
 
 // dq, and for the next kernel [H][N] of -lse (over the scale, or in base 2) and -D; a row without keys gets -infinity, so its p are zero.
-template <typename T, int D>
-__global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention_dq_kernel(
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::DQ_PER_CU)) void attention_dq_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ o, const T *__restrict__ dout,
     const float *__restrict__ lse, Sequences seqs, T *__restrict__ dq, float *__restrict__ tops, float *__restrict__ deltas, int blocks,
     int H, int Hk, int window, float scale) {
-    using C = Bwd<T, D>;
+    using C = Bwd<T, D, SPLIT>;
     using Ti = Tile<T, D>;
     using frag = typename Op<T>::frag;
     constexpr int WAVES = C::WAVES, KEYS = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
@@ -67,19 +47,23 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     if (b.at >= b.rows) return;
     const int hk = it.h / (H / Hk);
     const uint32_t kv_stride = uint32_t(Hk) * Ti::ROWB;
-    const int r0 = b.at + 32 * wv, q_row = r0 + (lane & 31);
+    const int r0 = b.at + (SPLIT ? 0 : 32 * wv), q_row = r0 + (lane & 31);
     const float scale2 = scale * LOG2E;
 
     const int end = min(b.at + C::ROWS, b.n);
     const int first = window ? max(b.at - window + 1, 0) / KEYS : 0;
     const int tiles = b.at < b.n ? (end + KEYS - 1) / KEYS : first;
     const T *kb = k + (static_cast<size_t>(b.lo) * Hk + hk) * D, *vb = v + (static_cast<size_t>(b.lo) * Hk + hk) * D;
-    auto fetch = [&](int j, int buf) {
-        const size_t at = static_cast<size_t>(j) * KEYS * Hk * D;
-        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE, kb + at, kv_stride, b.n - j * KEYS, wv, lane);
-        Ti::template fetch<KEYS, WAVES>(smem + buf * 2 * TILE + TILE, vb + at, kv_stride, b.n - j * KEYS, wv, lane);
+    unsigned char *tile = smem + (SPLIT ? wv * 2 * TILE : 0);
+    auto fetch_one = [&](const T *rows, int j, unsigned char *to) {
+        Ti::template fetch<KEYS, SPLIT ? 1 : WAVES>(to, rows + static_cast<size_t>(j) * KEYS * Hk * D, kv_stride, b.n - j * KEYS, SPLIT ? 0 : wv, lane);
     };
-    if (first < tiles) fetch(first, 0);
+    auto fetch = [&](int j, int buf) {
+        fetch_one(kb, j, tile + buf * 2 * TILE);
+        fetch_one(vb, j, tile + buf * 2 * TILE + TILE);
+    };
+    const int from = first + (SPLIT ? wv : 0);
+    if (from < tiles) fetch(from, 0);
 
     const size_t own = (static_cast<size_t>(b.lo) + min(q_row, b.rows - 1)) * H + it.h;
     frag qf[QS], df[QS];
@@ -97,14 +81,14 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
     const bool live = q_row < b.n && l != -INFINITY;
     const float top = live ? FROM_LSE<T> ? -l / scale : -l * LOG2E : -INFINITY;
     d = live ? d : 0.f;
-    if (half == 0 && q_row < b.rows) {
+    if (half == 0 && q_row < b.rows && (!SPLIT || wv == 0)) {
         const size_t i = static_cast<size_t>(it.h) * seqs.N + b.lo + q_row;
         tops[i] = top;
         deltas[i] = -d;
     }
     f32x16_t acc[NO] = {};
 
-    auto step = [&](int j, unsigned char *kt, unsigned char *vt) __attribute__((always_inline)) {
+    auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
         ln.again();
         const bool masked = (j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window);
 #pragma unroll
@@ -120,6 +104,7 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
                 x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, ln), qf[s], x);
                 y = Op<T>::mma(Ti::template row<32>(vt, 32 * t, s, ln), df[s], y);
             }
+            if (t == KEYS / 32 - 1) values_done();
             if (masked) {
                 KEEP_BRANCH;
                 const int last = q_row - j * KEYS - 32 * t - 4 * half, first_seen = window ? last - window : -1000;
@@ -139,35 +124,51 @@ __global__ __launch_bounds__(256, (sizeof(T) * D == 512 ? 1 : 2)) void attention
             }
         }
     };
-    auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
-        constexpr int buf = decltype(buffer)::value;
-        loads_done();
-        if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
-        if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;
-        step(j, smem + buf * 2 * TILE, smem + buf * 2 * TILE + TILE);
-    };
-    for (int j = first; j < tiles; j += 2) {
-        turn(j, std::integral_constant<int, 0>{});
-        if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
+    if constexpr (SPLIT) {
+        for (int j = from; j < tiles; j += WAVES) {
+            const bool more = j + WAVES < tiles;
+            own_loads_done<0>();
+            step(j, tile, tile + TILE, [&]() __attribute__((always_inline)) {
+                own_reads_done();
+                if (more) fetch_one(vb, j + WAVES, tile + TILE);
+            });
+            own_reads_done();
+            if (more) fetch_one(kb, j + WAVES, tile);
+        }
+    } else {
+        auto nothing = [] {};
+        auto turn = [&](int j, auto buffer) __attribute__((always_inline)) {
+            constexpr int buf = decltype(buffer)::value;
+            loads_done();
+            if (j + 1 < tiles) fetch(j + 1, buf ^ 1);
+            if (j * KEYS > r0 + 31 || (window && r0 + 1 - (j + 1) * KEYS >= window)) return;
+            step(j, tile + buf * 2 * TILE, tile + buf * 2 * TILE + TILE, nothing);
+        };
+        for (int j = from; j < tiles; j += 2) {
+            turn(j, std::integral_constant<int, 0>{});
+            if (j + 1 < tiles) turn(j + 1, std::integral_constant<int, 1>{});
+        }
     }
-    lds_barrier();
-    store_rows<T, D>(smem + wv * 32 * Ti::ROWB, acc, scale, live, dq + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D,
-                     static_cast<size_t>(H) * D, b.rows - r0, lane);
+    lds_barrier();  // the tiles are free
+    T *out = dq + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D;
+    if constexpr (SPLIT)
+        store_sums<T, D, WAVES>(smem, acc, [&](int r) { return r0 + r < b.n ? scale : 0.f; }, out, static_cast<size_t>(H) * D, b.rows - r0, wv, lane);
+    else
+        store_rows<T, D>(smem + wv * 32 * Ti::ROWB, acc, scale, live, out, static_cast<size_t>(H) * D, b.rows - r0, lane);
 }
 
 // dk and dv of 128 keys of a key head, 32 to a wavefront, whose keys and values stay in registers, over the queries of all its heads. Scores have
 // queries as rows, so p and ds are the operands of dv^T += do^T p and dk^T += q^T ds as they are.
-template <typename T, int D>
-__global__ __launch_bounds__(256, (sizeof(T) == 2 ? 2 : 1)) void attention_dkv_kernel(
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::DKV_PER_CU)) void attention_dkv_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ tops,
     const float *__restrict__ deltas, Sequences seqs, T *__restrict__ dk, T *__restrict__ dv, int blocks, int H, int Hk, int window,
     float scale) {
-    using C = Bwd<T, D>;
+    using C = Bwd<T, D, SPLIT>;
     using Ti = Tile<T, D>;
     using frag = typename Op<T>::frag;
     constexpr int WAVES = C::WAVES, QR = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    float *stats = reinterpret_cast<float *>(smem + 4 * TILE);
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
     typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, Hk, Hk);
@@ -175,24 +176,36 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? 2 : 1)) void attention_dkv_k
     if (b.at >= b.rows) return;
     const int G = H / Hk, h0 = it.h * G;
     const uint32_t q_stride = uint32_t(H) * Ti::ROWB;
-    const int k0 = b.at + 32 * wv, key = k0 + (lane & 31);
+    const int k0 = b.at + (SPLIT ? 0 : 32 * wv), key = k0 + (lane & 31);
+    unsigned char *tile = smem + (SPLIT ? wv * 2 * TILE : 0);
+    float *stats = reinterpret_cast<float *>(smem + C::LDS) + (SPLIT ? wv * 128 : 0);
     const float scale2 = scale * LOG2E;
 
     // Tiles of queries that see the block's keys, for each head.
     const int first = b.at / QR;
     const int end = window ? static_cast<int>(min(static_cast<int64_t>(b.n), static_cast<int64_t>(b.at) + C::ROWS + window - 1)) : b.n;
     const int per = b.at < b.n ? (end + QR - 1) / QR - first : 0, steps = per * G;
-    auto fetch = [&](int i, int buf) {
-        const int h = h0 + i / per, j = first + i % per, left = b.n - j * QR;
-        const size_t row = static_cast<size_t>(b.lo) + static_cast<size_t>(j) * QR;
-        Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE, q + (row * H + h) * D, q_stride, left, wv, lane);
-        Ti::template fetch<QR, WAVES>(smem + buf * 2 * TILE + TILE, dout + (row * H + h) * D, q_stride, left, wv, lane);
-        if (wv < 2) {
-            const rsrc_t r = make_rsrc((wv ? deltas : tops) + static_cast<size_t>(h) * seqs.N + row, min(left, QR) * 4u);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stats + (buf * 2 + wv) * 64), 4, lane * 4, 0, 0, 0);
+    auto fetch_one = [&](const T *rows, int i, unsigned char *to) {
+        const int h = h0 + i / per, j = first + i % per;
+        Ti::template fetch<QR, SPLIT ? 1 : WAVES>(to, rows + ((static_cast<size_t>(b.lo) + static_cast<size_t>(j) * QR) * H + h) * D, q_stride, b.n - j * QR,
+                                                  SPLIT ? 0 : wv, lane);
+    };
+    auto fetch_stats = [&](int i, int buf) {
+        const int h = h0 + i / per, j = first + i % per;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (!SPLIT && wv != x) continue;
+            const rsrc_t r = make_rsrc((x ? deltas : tops) + static_cast<size_t>(h) * seqs.N + b.lo + static_cast<size_t>(j) * QR, min(b.n - j * QR, QR) * 4u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(stats + (buf * 2 + x) * 64), 4, lane * 4, 0, 0, 0);
         }
     };
-    if (steps > 0) fetch(0, 0);
+    auto fetch = [&](int i, int buf) {
+        fetch_one(q, i, tile + buf * 2 * TILE);
+        fetch_one(dout, i, tile + buf * 2 * TILE + TILE);
+        fetch_stats(i, buf);
+    };
+    const int from = SPLIT ? wv : 0;
+    if (from < steps) fetch(from, 0);
 
     const size_t own = (static_cast<size_t>(b.lo) + min(key, b.rows - 1)) * Hk + it.h;
     frag kf[QS], vf[QS];
@@ -203,7 +216,7 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? 2 : 1)) void attention_dkv_k
     }
     f32x16_t dka[NO] = {}, dva[NO] = {};
 
-    auto step = [&](int row0, unsigned char *qt, unsigned char *dt, const float *st) __attribute__((always_inline)) {
+    auto step = [&](int row0, unsigned char *qt, unsigned char *dt, const float *st, auto dout_done) __attribute__((always_inline)) {
         ln.again();
         // The sums begin at -lse / scale and -D of their rows, so that no subtraction is left. In float32 x begins at 0: its sum's
         // roundings would be as large as lse makes them.
@@ -239,57 +252,113 @@ __global__ __launch_bounds__(256, (sizeof(T) == 2 ? 2 : 1)) void attention_dkv_k
                 x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, st[8 * (i / 4) + 4 * half + i % 4]));
             y[i] *= x[i];
         }
+        if constexpr (SPLIT) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const frag p = acc_frag<T>(x, s), ds = acc_frag<T>(y, s);
+            for (int s = 0; s < 2; ++s) {
+                const frag p = acc_frag<T>(x, s);
 #pragma unroll
-            for (int n = 0; n < NO; ++n) {
-                dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, ln), p, dva[n]);
-                dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, ln), ds, dka[n]);
+                for (int n = 0; n < NO; ++n) dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, ln), p, dva[n]);
+            }
+            dout_done();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const frag ds = acc_frag<T>(y, s);
+#pragma unroll
+                for (int n = 0; n < NO; ++n) dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, ln), ds, dka[n]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const frag p = acc_frag<T>(x, s), ds = acc_frag<T>(y, s);
+#pragma unroll
+                for (int n = 0; n < NO; ++n) {
+                    dva[n] = Op<T>::mma(Ti::template col<32>(dt, 16 * s, 32 * n, ln), p, dva[n]);
+                    dka[n] = Op<T>::mma(Ti::template col<32>(qt, 16 * s, 32 * n, ln), ds, dka[n]);
+                }
             }
         }
     };
-    auto turn = [&](int i, auto buffer) __attribute__((always_inline)) {
-        constexpr int buf = decltype(buffer)::value;
-        loads_done();
-        if (i + 1 < steps) fetch(i + 1, buf ^ 1);
-        const int j = first + i % per;
-#pragma unroll
-        for (int t = 0; t < QR / 32; ++t) {
-            const int row0 = j * QR + 32 * t;
-            if (row0 + 31 < k0 || row0 >= b.n || (window && row0 - (k0 + 31) >= window)) continue;  // no query sees a key
-            unsigned char *qt = smem + buf * 2 * TILE + t * 32 * Ti::ROWB;
-            step(row0, qt, qt + TILE, stats + buf * 128 + 32 * t);
+    if constexpr (SPLIT) {
+        for (int i = from; i < steps; i += WAVES) {
+            const bool more = i + WAVES < steps;
+            own_loads_done<0>();
+            step((first + i % per) * QR, tile, tile + TILE, stats, [&]() __attribute__((always_inline)) {
+                own_reads_done();
+                if (more) fetch_one(dout, i + WAVES, tile + TILE);
+            });
+            own_reads_done();
+            if (more) {
+                fetch_one(q, i + WAVES, tile);
+                fetch_stats(i + WAVES, 0);
+            }
         }
-    };
-    for (int i = 0; i < steps; i += 2) {
-        turn(i, std::integral_constant<int, 0>{});
-        if (i + 1 < steps) turn(i + 1, std::integral_constant<int, 1>{});
+    } else {
+        auto turn = [&](int i, auto buffer) __attribute__((always_inline)) {
+            constexpr int buf = decltype(buffer)::value;
+            loads_done();
+            if (i + 1 < steps) fetch(i + 1, buf ^ 1);
+            const int j = first + i % per;
+#pragma unroll
+            for (int t = 0; t < QR / 32; ++t) {
+                const int row0 = j * QR + 32 * t;
+                if (row0 + 31 < k0 || row0 >= b.n || (window && row0 - (k0 + 31) >= window)) continue;  // no query sees a key
+                unsigned char *qt = tile + buf * 2 * TILE + t * 32 * Ti::ROWB;
+                step(row0, qt, qt + TILE, stats + buf * 128 + 32 * t, [] {});
+            }
+        };
+        for (int i = 0; i < steps; i += 2) {
+            turn(i, std::integral_constant<int, 0>{});
+            if (i + 1 < steps) turn(i + 1, std::integral_constant<int, 1>{});
+        }
     }
-    lds_barrier();
-    unsigned char *room = smem + wv * 32 * Ti::ROWB;
+    lds_barrier();  // the tiles are free
     const size_t out = ((static_cast<size_t>(b.lo) + k0) * Hk + it.h) * D, stride = static_cast<size_t>(Hk) * D;
-    store_rows<T, D>(room, dka, scale, key < b.n, dk + out, stride, b.rows - k0, lane);
-    store_rows<T, D>(room, dva, 1.f, key < b.n, dv + out, stride, b.rows - k0, lane);
+    if constexpr (SPLIT) {
+        store_sums<T, D, WAVES>(smem, dka, [&](int r) { return k0 + r < b.n ? scale : 0.f; }, dk + out, stride, b.rows - k0, wv, lane);
+        store_sums<T, D, WAVES>(smem, dva, [&](int r) { return k0 + r < b.n ? 1.f : 0.f; }, dv + out, stride, b.rows - k0, wv, lane);
+    } else {
+        unsigned char *room = smem + wv * 32 * Ti::ROWB;
+        store_rows<T, D>(room, dka, scale, key < b.n, dk + out, stride, b.rows - k0, lane);
+        store_rows<T, D>(room, dva, 1.f, key < b.n, dv + out, stride, b.rows - k0, lane);
+    }
+}
+
+template <typename T, int D, bool SPLIT> hipError_t launch_dq(const AttentionCall &c, const AttentionGrads &g, float *tops, float *deltas, hipStream_t stream) {
+    using B = Bwd<T, D, SPLIT>;
+    const hipError_t err = allow_lds<&attention_dq_kernel<T, D, SPLIT>>(B::LDS);
+    if (err != hipSuccess) return err;
+    const int blocks = c.N / B::ROWS + c.S + 1;
+    hipLaunchKernelGGL((attention_dq_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * B::WAVES), B::LDS, stream,
+                       static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v), static_cast<const T *>(g.o),
+                       static_cast<const T *>(g.dout), g.lse, Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(g.dq), tops, deltas,
+                       blocks, c.H, c.Hk, c.window, c.scale);
+    return hipGetLastError();
+}
+
+template <typename T, int D, bool SPLIT> hipError_t launch_dkv(const AttentionCall &c, const AttentionGrads &g, float *tops, float *deltas, hipStream_t stream) {
+    using B = Bwd<T, D, SPLIT>;
+    const hipError_t err = allow_lds<&attention_dkv_kernel<T, D, SPLIT>>(B::LDS + B::STATS);
+    if (err != hipSuccess) return err;
+    const int blocks = c.N / B::ROWS + c.S + 1;
+    hipLaunchKernelGGL((attention_dkv_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), B::LDS + B::STATS,
+                       stream, static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v),
+                       static_cast<const T *>(g.dout), tops, deltas, Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(g.dk),
+                       static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
+    return hipGetLastError();
 }
 
 template <typename T, int D> hipError_t launch(const AttentionCall &c, const AttentionGrads &g, void *workspace, hipStream_t stream) {
-    using B = Bwd<T, D>;
-    constexpr int LDS = 4 * B::TILE;
-    hipError_t err = allow_lds<&attention_dq_kernel<T, D>>(LDS);
-    if (err == hipSuccess) err = allow_lds<&attention_dkv_kernel<T, D>>(LDS + B::STATS);
-    if (err != hipSuccess) return err;
-    const int blocks = static_cast<int>(attention_blocks(c.N, c.S));
-    const Sequences s{c.offsets, c.lens, c.N, c.S};
-    const T *q = static_cast<const T *>(c.q), *k = static_cast<const T *>(c.k), *v = static_cast<const T *>(c.v), *d = static_cast<const T *>(g.dout);
     float *tops = static_cast<float *>(workspace), *deltas = tops + up256(static_cast<size_t>(c.N) * c.H * 4) / 4;
-    hipLaunchKernelGGL((attention_dq_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * B::WAVES), LDS, stream, q, k, v,
-                       static_cast<const T *>(g.o), d, g.lse, s, static_cast<T *>(g.dq), tops, deltas, blocks, c.H, c.Hk, c.window, c.scale);
-    err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((attention_dkv_kernel<T, D>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), LDS + B::STATS, stream,
-                       q, k, v, d, tops, deltas, s, static_cast<T *>(g.dk), static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
-    return hipGetLastError();
+    hipError_t err;
+    if constexpr (sizeof(T) == 2) {
+        err = attention_split(c.N, c.S, c.H) ? launch_dq<T, D, true>(c, g, tops, deltas, stream) : launch_dq<T, D, false>(c, g, tops, deltas, stream);
+        if (err == hipSuccess)
+            err = attention_split(c.N, c.S, c.Hk) ? launch_dkv<T, D, true>(c, g, tops, deltas, stream) : launch_dkv<T, D, false>(c, g, tops, deltas, stream);
+    } else {
+        err = launch_dq<T, D, true>(c, g, tops, deltas, stream);
+        if (err == hipSuccess) err = launch_dkv<T, D, true>(c, g, tops, deltas, stream);
+    }
+    return err;
 }
 
 }  // namespace

@@ -15,9 +15,9 @@ struct AttentionCall {
     float scale;
     bool bf16;
 };
-// Rows of a workgroup of the prompt kernels.
-constexpr int ATTENTION_ROWS = 128;
-inline long long attention_blocks(int N, int S) { return static_cast<long long>(N) / ATTENTION_ROWS + S + 1; }
+// Workgroups of a prompt kernel have 128 rows of one head, or 32: in float32, and where 128 would make too few of them.
+inline long long attention_blocks(int N, int S, int rows) { return static_cast<long long>(N) / rows + S + 1; }
+bool attention_split(int N, int S, int heads);
 hipError_t launch_attention_fwd(const AttentionCall &c, void *o, float *lse, hipStream_t stream);
 
 size_t attention_bwd_workspace_bytes(int N, int H);

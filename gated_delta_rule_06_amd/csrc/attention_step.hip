@@ -118,9 +118,9 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
         if (more) good_next = fetch(tile + WAVES, buf ^ 1);
         // The tile's own loads are done when no more than the next one's are out.
         if (more)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * 16 / Ti::RPI) : "memory");
+            own_loads_done<4 * 16 / Ti::RPI>();
         else
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            own_loads_done<0>();
         unsigned char *kt = ring + buf * 2 * TILE, *vt = kt + TILE;
         const int p0 = tile * 32;
         if (kn && p0 <= old && old < p0 + 32 && n > old) {  // the new token's row
@@ -172,7 +172,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
         const frag p = Op<T>::pack(x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]);
 #pragma unroll
         for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, ln), p, acc[i]);
-        wave_lds_sync();  // the tile is free
+        own_reads_done();  // the tile is free
     }
     l += __shfl_xor(l, 16, 64);
     l = halves_sum(l);

@@ -576,7 +576,8 @@ muir_status_t muir_matvec_q4(
  * Rows that are no token (behind a sequence's length, or behind the last sequence) have o = 0 and lse = -infinity, and what k and v hold
  * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of up to 127 tokens before it (as 0 times it).
  * bf16: exp(s_ij - m_i) is rounded to bf16 before it multiplies v_j; sums, maxima and lse are float32. Errors as for muir_chunk_fwd,
- * and MUIR_ERR_UNSUPPORTED for H above 2^15, N above 2^30 or (N / 128 + S + 1) H above 2^24 - 1.
+ * and MUIR_ERR_UNSUPPORTED for H above 2^15, N above 2^30 or (N / 128 + S + 1) H
+ * above 2^24 - 1 (float32: N / 32).
  */
 muir_status_t muir_attention_fwd(
     const void *q, const void *k, const void *v, const int *offsets, const int *lens, void *o, float *lse,

@@ -87,7 +87,7 @@ static void check_layout() {
             offsets[s + 1] = offsets[s] + (pick(0, 2) ? pick(0, most) : 0);
             lens[s] = pick(-3, most + 3);
         }
-        const int N = offsets[S] + pick(0, 300), R = round % 2 ? 128 : 64;
+        const int N = offsets[S] + pick(0, 300), R = round % 3 == 0 ? 128 : round % 3 == 1 ? 32 : 8;
         check_blocks({offsets.data(), nullptr, N, S}, R, true);
         check_blocks({offsets.data(), lens.data(), N, S}, R, true);
         check_blocks({nullptr, lens.data(), S * most, S}, R, true);
