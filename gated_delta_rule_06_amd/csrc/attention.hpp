@@ -227,22 +227,19 @@ __device__ __forceinline__ void store_sums(unsigned char *room, const f32x16_t (
     lds_barrier();
 }
 
-struct Block {
-    int seq, lo, rows, n, at;  // the sequence, its first row, rows and tokens, and the block's first row in it
-};
-// Block `w` of `R` rows; one past its sequence's rows has at >= rows. All 64 lanes search together.
+// Block `w` of `R` rows. All 64 lanes search together.
 template <int R> __device__ __forceinline__ Block find_block(const Sequences &q, int w) {
     const int lane = threadIdx.x & 63;
     const int s = search_sequence(q.S, [&](int lo, int step, int hi) {
         const int i = lo + lane * step;
         return __builtin_amdgcn_readfirstlane(static_cast<int>(__popcll(__ballot(i <= hi && q.first(i) / R + i <= w))));
     });
-    Block b;
-    b.seq = __builtin_amdgcn_readfirstlane(s);
-    b.lo = __builtin_amdgcn_readfirstlane(q.first(s));
-    b.rows = __builtin_amdgcn_readfirstlane(q.rows(s));
-    b.n = __builtin_amdgcn_readfirstlane(q.tokens(s));
-    b.at = (w - b.lo / R - b.seq) * R;
+    Block b = block_in(q, R, w, s);
+    b.seq = __builtin_amdgcn_readfirstlane(b.seq);
+    b.lo = __builtin_amdgcn_readfirstlane(b.lo);
+    b.rows = __builtin_amdgcn_readfirstlane(b.rows);
+    b.n = __builtin_amdgcn_readfirstlane(b.n);
+    b.at = __builtin_amdgcn_readfirstlane(b.at);
     return b;
 }
 

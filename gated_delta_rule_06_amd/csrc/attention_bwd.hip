@@ -4,8 +4,11 @@
 // Two kernels, each with its sums in registers from the first to the last product, so no sum depends on an order and nothing is
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed).
-// bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); D is taken from
-// the rounded o; everything else is float32.
+// bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
+// float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
+// (2-norm, relative) where one rounding is 0.0017. But sum_j ds_ij = 0, so dq's kernel finds e_i as the sum of its own ds, hands the
+// exact D on to dk, and takes e_i sum_j p_ij k_j off dq, of that sum only the largest p of each of a wavefront's halves: the rest is
+// small, and is times e_i. 0.0024 and 0.0024 then.
 #include "attention.hpp"
 #include "attention_kernels.hpp"
 #include "launch.hpp"
@@ -23,11 +26,15 @@ template <typename T, int D, bool SPLIT> struct Bwd {
     static constexpr int STEP = SPLIT ? 32 : 64, TILE = STEP * D * int(sizeof(T));  // rows of the tiles walked over
     static constexpr int LDS = (SPLIT ? 2 * WAVES : 4) * TILE, STATS = (SPLIT ? 2 * WAVES : 4) * 64 * 4;  // lse and D, of as many tiles
     static constexpr int DQ_PER_CU = sizeof(T) * D == 512 ? 1 : 2, DKV_PER_CU = sizeof(T) * D == 512 ? 1 : 2;
+    static_assert(LDS == WAVES * 64 * D * int(sizeof(T)), "a wavefront has 64 rows of the tiles' room");
     static_assert(LDS >= ROWS * D * int(sizeof(T)) && (!SPLIT || 2 * TILE >= 32 * D * 4), "the outputs pass through the tiles' room");
 };
 
-// Whether a score's sum begins at -lse / scale, or at 0 and -lse is added to the exponent.
+// Whether a score's sum begins at -lse / scale where rows of accumulators are queries, or at 0 and -lse is added to the exponent.
 template <typename T> constexpr bool FROM_LSE = sizeof(T) == 2;
+
+// Whether D is corrected as above: what float32 rounds off o leaves nothing to correct.
+template <typename T> constexpr bool EXACT_D = sizeof(T) == 2;
 
 // dq, and for the next kernel [H][N] of -lse (over the scale, or in base 2) and -D; a row without keys gets -infinity, so its p are zero.
 template <typename T, int D, bool SPLIT>
@@ -79,14 +86,13 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     d = halves_sum(d);
     const float l = lse[own];
     const bool live = q_row < b.n && l != -INFINITY;
-    const float top = live ? FROM_LSE<T> ? -l / scale : -l * LOG2E : -INFINITY;
+    const float top = live ? -l * LOG2E : -INFINITY;
     d = live ? d : 0.f;
-    if (half == 0 && q_row < b.rows && (!SPLIT || wv == 0)) {
-        const size_t i = static_cast<size_t>(it.h) * seqs.N + b.lo + q_row;
-        tops[i] = top;
-        deltas[i] = -d;
-    }
     f32x16_t acc[NO] = {};
+    float e[2] = {};  // sums of ds
+    // The lane's largest p so far, its last four bits the accumulator element that it was, and the first key of its 32.
+    uint32_t best = 0;
+    int best_at = 0;
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
         ln.again();
@@ -95,10 +101,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
         for (int t = 0; t < KEYS / 32; ++t) {
             f32x16_t x = {}, y;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if constexpr (FROM_LSE<T>) x[i] = top;
-                y[i] = -d;
-            }
+            for (int i = 0; i < 16; ++i) y[i] = -d;
 #pragma unroll
             for (int s = 0; s < QS; ++s) {
                 x = Op<T>::mma(Ti::template row<32>(kt, 32 * t, s, ln), qf[s], x);
@@ -115,7 +118,25 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(FROM_LSE<T> ? x[i] * scale2 : fmaf(x[i], scale2, top)) * y[i];
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, top));
+            if constexpr (EXACT_D<T>) {
+                float most = x[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) most = fmaxf(most, x[i]);
+                if (__any(most > __uint_as_float(best))) {  // seldom, after the first few
+                    KEEP_BRANCH;
+                    uint32_t which = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) which = max(which, (__float_as_uint(x[i]) & ~15u) | static_cast<uint32_t>(i));
+                    best_at = which > best ? j * KEYS + 32 * t : best_at;
+                    best = max(best, which);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] *= y[i];
+                if constexpr (EXACT_D<T>) e[i & 1] += x[i];
+            }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const frag f = acc_frag<T>(x, s);
@@ -150,6 +171,50 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
         }
     }
     lds_barrier();  // the tiles are free
+    if constexpr (EXACT_D<T>) {
+        float off = halves_sum(e[0] + e[1]);
+        if constexpr (SPLIT) {
+            float *sums = reinterpret_cast<float *>(smem);
+            if (half == 0) sums[32 * wv + lane] = off;
+            lds_barrier();
+            off = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) off += sums[32 * w + (lane & 31)];
+            lds_barrier();
+        }
+        d += off;
+        // The keys come as two tiles of 32, one for each query and half, and the factors are a diagonal matrix: dq^T += k^T (-e p). A lane without
+        // a largest p takes its own token's key, times 0, and one whose query is no token, and may hold anything, some token's.
+        const int place = (best & 15u) / 4 * 8 + 4 * half + (best & 3u), mine = min(best >= 16u ? best_at + place : q_row, max(b.n - 1, 0));
+        const auto ps = __builtin_amdgcn_permlane32_swap(best & ~15u, best & ~15u, false, false);
+        unsigned char *room = smem + wv * 64 * Ti::ROWB;
+#pragma unroll
+        for (int n = 0; n < 64 / Ti::RPI; ++n) {
+            const int r = n * Ti::RPI + lane / Ti::CH, key = __shfl(mine, r, 64);
+            const T *from = kb + static_cast<size_t>(key) * Hk * D + ((lane % Ti::CH) ^ Ti::swz(r)) * (16 / int(sizeof(T)));
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (lds_void *)(room + n * 1024), 16, 0, 0);
+        }
+        own_loads_done<0>();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float f = -off * __uint_as_float(ps[x]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                float c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = acc_row(8 * s + i, lane) == (lane & 31) ? f : 0.f;
+                const frag diagonal = Op<T>::pack(c[0], c[1], c[2], c[3], c[4], c[5], c[6], c[7]);
+#pragma unroll
+                for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(room, 32 * x + 16 * s, 32 * n, ln), diagonal, acc[n]);
+            }
+        }
+        lds_barrier();  // the tiles are free again
+    }
+    if (half == 0 && q_row < b.rows && (!SPLIT || wv == 0)) {
+        const size_t i = static_cast<size_t>(it.h) * seqs.N + b.lo + q_row;
+        tops[i] = FROM_LSE<T> && live ? -l / scale : top;
+        deltas[i] = -d;
+    }
     T *out = dq + ((static_cast<size_t>(b.lo) + r0) * H + it.h) * D;
     if constexpr (SPLIT)
         store_sums<T, D, WAVES>(smem, acc, [&](int r) { return r0 + r < b.n ? scale : 0.f; }, out, static_cast<size_t>(H) * D, b.rows - r0, wv, lane);

@@ -48,6 +48,16 @@ template <typename Count> MUIR_HD int search_sequence(int S, Count count) {
     return lo;
 }
 
+// What block `w` of `R` rows has of sequence `s`, which it was found to be in: the sequence's first row, rows and tokens, and the block's first row in
+// it. A block without rows, past its sequence's or found by offsets that do not ascend, has at >= rows; at is never below 0.
+struct Block {
+    int seq, lo, rows, n, at;
+};
+MUIR_HD Block block_in(const Sequences &q, int R, int w, int s) {
+    const int lo = q.first(s), rows = q.rows(s), at = (w - lo / R - s) * R;
+    return Block{s, lo, rows, q.tokens(s), at < 0 ? rows : at};
+}
+
 // Work item of a workgroup: consecutive workgroups go round the eight XCDs, so that the heads of one key head, all their blocks, run on
 // one of them, whose L2 then holds that head's keys and values; what is left over eight key heads goes round by blocks. Blocks
 // come in rising order.

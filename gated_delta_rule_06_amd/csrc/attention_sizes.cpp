@@ -11,7 +11,7 @@ namespace muir {
 // 104 us; at B4 T1024 H16 (592) 46 and 133 against 43 and 101. In float32 the products take so long that rows are never too few for it: d64 is
 // faster at every size measured (B1 T128 H12 7.3 and 20 us against 15 and 43, B8 T4096 H16 2.24 and 7.38 ms against 2.38 and 7.82), d128 up to
 // B4 T1024 H16 (201 and 666 us against 218 and 830), and at B8 T4096 H16 7 and 3 % slower.
-bool attention_split(int N, int S, int heads) { return attention_blocks(N, S, 128) * heads <= 512; }
+bool attention_split(int N, int S, int heads) { return attention_blocks(N, S, 128) * heads <= 400; }
 
 size_t attention_bwd_workspace_bytes(int N, int H) { return 2 * up256(static_cast<size_t>(N) * H * 4); }
 

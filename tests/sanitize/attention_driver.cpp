@@ -62,13 +62,11 @@ static void check_blocks(const muir::at::Sequences &q, int R, bool ordered) {
             return n;
         });
         CHECK(s >= 0 && s <= q.S);
-        const int lo = q.first(s), rows = q.rows(s), n = q.tokens(s), start = (w - lo / R - s) * R;
-        CHECK(lo >= 0 && rows >= 0 && lo + rows <= q.N && n >= 0 && n <= rows);
-        if (start >= rows) continue;
-        CHECK(!ordered || start >= 0);
-        for (int r = start < 0 ? 0 : start; r < start + R && r < rows; ++r) {
-            ++taken[lo + r];
-            token[lo + r] += r < n;
+        const muir::at::Block x = muir::at::block_in(q, R, w, s);
+        CHECK(x.seq == s && x.lo >= 0 && x.rows >= 0 && x.lo + x.rows <= q.N && x.n >= 0 && x.n <= x.rows && x.at >= 0);
+        for (int r = x.at; r < x.at + R && r < x.rows; ++r) {
+            ++taken[x.lo + r];
+            token[x.lo + r] += r < x.n;
         }
     }
     if (!ordered) return;
