@@ -135,14 +135,16 @@ template <typename T, int D> struct Tile {
 
     // ROWS rows from `base` on into the tile, by WAVES wavefronts of which this is `wv`, straight to LDS. Rows from `live`
     // on, and so what lies behind a sequence, come as zeros. `stride` is the bytes from row to row.
-    template <int ROWS, int WAVES> static __device__ __forceinline__ void fetch(unsigned char *t, const void *base, uint32_t stride, int live, int wv, int lane) {
+    // AUX: the loads' cache policy, 0 or STREAM.
+    static constexpr int STREAM = 2;
+    template <int ROWS, int WAVES, int AUX = 0> static __device__ __forceinline__ void fetch(unsigned char *t, const void *base, uint32_t stride, int live, int wv, int lane) {
         const rsrc_t r = make_rsrc(base, live <= 0 ? 0u : uint32_t(min(live, ROWS) - 1) * stride + ROWB);
 #pragma unroll
         for (int n = 0; n < ROWS / RPI / WAVES; ++n) {
             const int r0 = (n * WAVES + wv) * RPI, i = lane / CH;
             // Only the row's place in its 16 enters the permutation, so most loads of a wavefront share their lanes' offsets.
             const uint32_t voff = i * stride + (((lane % CH) ^ swz((r0 & 15) + i)) << 4);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(t + r0 * ROWB), 16, voff, r0 * stride, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(t + r0 * ROWB), 16, voff, r0 * stride, 0, AUX);
         }
     }
 };

@@ -1,8 +1,8 @@
 // The paged cache of keys and values: rows appended to it, and one new token of each sequence attending over it.
 //
 // Step: a workgroup has up to 16 query heads that share a key head and one part of a sequence's keys, its wavefronts every WAVES-th tile of
-// 32 keys, each with its own running maximum, sum and output and its own two tiles of keys and values in LDS (loads straight to LDS, one tile
-// in flight); they meet in LDS at the end. Where sequences and key heads do not fill the card a sequence is cut into parts, which a second kernel
+// 32 keys, each with its own running maximum, sum and output and its own tiles of keys and values in LDS (loads straight to LDS: the next keys
+// while values are multiplied, the next values while keys are); they meet in LDS at the end. Where sequences and key heads do not fill the card a sequence is cut into parts, which a second kernel
 // joins. Reading the cache once bounds it. Scores are made transposed (16 keys by 16 heads), so that two score tiles are the operand
 // of the product with the values, as in the prompt kernels; p is rounded to bf16 there in bf16.
 // Rows behind the last token, and pages that the table does not have, are never read: their keys come as zeros and are masked.
@@ -53,12 +53,14 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const unsigned char *
 }
 
 template <typename T, int D> struct Step {
-    static constexpr int KEYS = 32, TILE = KEYS * D * int(sizeof(T)), WAVES = sizeof(T) * D == 512 ? 2 : 4;
-    static constexpr int RING = 4 * TILE, LDS = WAVES * RING;  // two tiles of keys and values a wavefront
-    static_assert(RING >= 16 * D * 4 + 128, "outputs, maxima and sums of 16 heads pass through the tiles' room");
+    static constexpr int KEYS = 32, TILE = KEYS * D * int(sizeof(T)), WAVES = sizeof(T) * D == 512 ? 4 : 8;
+    static constexpr int ROOM = 2 * TILE, LDS = WAVES * ROOM;  // a tile of keys and one of values for each wavefront
+    static_assert(ROOM >= 16 * D * 4 + 128, "outputs, maxima and sums of 16 heads pass through the tiles' room");
 };
 
-template <typename T, int D>
+// BIG: the cache is larger than the 256 MB that the last-level cache holds, so none of it is there when it comes to be read, and its loads go past the caches:
+// B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.3 GB, 207 us (6.3 TB/s) against 233. A cache of 190 MB read again and again takes 33 us with ordinary loads, 38 so.
+template <typename T, int D, bool BIG>
 __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kernel(
     const T *__restrict__ q, const T *__restrict__ kn, const T *__restrict__ vn, T *k_cache, T *v_cache, Pages pg,
     const int *__restrict__ lens, T *__restrict__ o, float *__restrict__ part_o, float *__restrict__ part_s, int H, int parts, int window,
@@ -73,7 +75,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     const int part = blockIdx.x % parts, set = blockIdx.x / parts % sets, bh = blockIdx.x / parts / sets, hk = bh % pg.Hk, b = bh / pg.Hk;
     const int h0 = hk * G + set * 16, heads = min(G - set * 16, 16);
     const typename Ti::template Lane<16> ln(lane);
-    unsigned char *ring = smem + wv * C::RING;
+    unsigned char *kt = smem + wv * C::ROOM, *vt = kt + TILE;
 
     const Span span = step_span(lens[b], kn != nullptr, window, pg.room());
     const int old = span.old, n = span.n, begin = span.begin;
@@ -82,27 +84,28 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     // The wavefront's tiles are from, from + WAVES, ... Each lane keeps the page of one half (16 rows, which always lie in one page) of the
     // 32 tiles that are fetched next.
     int ids = -1;
-    auto fetch = [&](int tile, int buf) {
-        const int i = (tile - from) / WAVES % 32;
-        if (i == 0) {
-            const int64_t pos = static_cast<int64_t>(tile + lane / 2 * WAVES) * 32 + lane % 2 * 16;
-            ids = pos < n ? pg.table[static_cast<size_t>(b) * pg.width + (pos >> pg.log_page)] : -1;
-        }
-        int good = 0;
+    auto look_up = [&](int tile) {
+        if ((tile - from) / WAVES % 32 != 0) return;
+        const int64_t pos = static_cast<int64_t>(tile + lane / 2 * WAVES) * 32 + lane % 2 * 16;
+        ids = pos < n ? pg.table[static_cast<size_t>(b) * pg.width + (pos >> pg.log_page)] : -1;
+    };
+    auto page_of = [&](int tile, int u) { return __builtin_amdgcn_readlane(ids, 2 * ((tile - from) / WAVES % 32) + u); };
+    // Which halves of a tile lie in a page that the cache has.
+    auto known = [&](int tile) { return (pg.good(page_of(tile, 0)) ? 1 : 0) | (pg.good(page_of(tile, 1)) ? 2 : 0); };
+    auto fetch = [&](const T *cache, int tile, unsigned char *to) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int id = __builtin_amdgcn_readlane(ids, 2 * i + u), pos = tile * 32 + 16 * u;
-            const bool known = pg.good(id);
-            const int live = known ? min(old - pos, 16) : 0;
-            const size_t at = live > 0 ? pg.row(id, hk, pos) * D : 0;
-            unsigned char *t = ring + buf * 2 * TILE + u * 16 * Ti::ROWB;
-            Ti::template fetch<16, 1>(t, k_cache + at, Ti::ROWB, live, 0, lane);
-            Ti::template fetch<16, 1>(t + TILE, v_cache + at, Ti::ROWB, live, 0, lane);
-            good |= known << u;
+            const int id = page_of(tile, u), pos = tile * 32 + 16 * u, live = pg.good(id) ? min(old - pos, 16) : 0;
+            Ti::template fetch<16, 1, BIG ? Ti::STREAM : 0>(to + u * 16 * Ti::ROWB, cache + (live > 0 ? pg.row(id, hk, pos) * D : 0), Ti::ROWB, live, 0, lane);
         }
-        return good;
     };
-    int good_next = from < to ? fetch(from, 0) : 0;
+    int good = 0;
+    if (from < to) {
+        look_up(from);
+        good = known(from);
+        fetch(k_cache, from, kt);
+        fetch(v_cache, from, vt);
+    }
 
     frag qf[QS];
 #pragma unroll
@@ -112,29 +115,22 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     }
     f32x4_t acc[NO] = {};
     float m = LOWEST, l = 0.f;
-    for (int tile = from, buf = 0; tile < to; tile += WAVES, buf ^= 1) {
+    constexpr int LOADS = 32 / Ti::RPI;  // of one tile
+    for (int tile = from; tile < to; tile += WAVES) {
         const bool more = tile + WAVES < to;
-        const int good = good_next;  // which halves lie in a page that the cache has
-        if (more) good_next = fetch(tile + WAVES, buf ^ 1);
-        // The tile's own loads are done when no more than the next one's are out.
-        if (more)
-            own_loads_done<4 * 16 / Ti::RPI>();
-        else
-            own_loads_done<0>();
-        unsigned char *kt = ring + buf * 2 * TILE, *vt = kt + TILE;
         const int p0 = tile * 32;
-        if (kn && p0 <= old && old < p0 + 32 && n > old) {  // the new token's row
-            const int r = old - p0;
-            if (lane < Ti::CH) {
-                const size_t at = (static_cast<size_t>(b) * pg.Hk + hk) * D + lane * (16 / sizeof(T));
-                const u32x4_t ks = *reinterpret_cast<const u32x4_t *>(kn + at), vs = *reinterpret_cast<const u32x4_t *>(vn + at);
-                *reinterpret_cast<u32x4_t *>(kt + Ti::at(r, lane)) = ks;
-                *reinterpret_cast<u32x4_t *>(vt + Ti::at(r, lane)) = vs;
-                if (set == 0 && (good >> (r >> 4) & 1)) {
-                    const size_t to_row = pg.row(pg.id(b, old), hk, old) * D + lane * (16 / sizeof(T));
-                    *reinterpret_cast<u32x4_t *>(k_cache + to_row) = ks;
-                    *reinterpret_cast<u32x4_t *>(v_cache + to_row) = vs;
-                }
+        own_loads_done<LOADS>();  // the values were asked for after the keys
+        u32x4_t new_value;
+        const bool has_new = kn && p0 <= old && old < p0 + 32 && n > old;
+        if (has_new && lane < Ti::CH) {  // the new token's row
+            const size_t at = (static_cast<size_t>(b) * pg.Hk + hk) * D + lane * (16 / sizeof(T));
+            const u32x4_t new_key = *reinterpret_cast<const u32x4_t *>(kn + at);
+            new_value = *reinterpret_cast<const u32x4_t *>(vn + at);
+            *reinterpret_cast<u32x4_t *>(kt + Ti::at(old - p0, lane)) = new_key;
+            if (set == 0 && (good >> ((old - p0) >> 4) & 1)) {
+                const size_t row = pg.row(pg.id(b, old), hk, old) * D + lane * (16 / sizeof(T));
+                *reinterpret_cast<u32x4_t *>(k_cache + row) = new_key;
+                *reinterpret_cast<u32x4_t *>(v_cache + row) = new_value;
             }
         }
         wave_lds_sync();
@@ -143,6 +139,13 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
         for (int s = 0; s < QS; ++s)
 #pragma unroll
             for (int u = 0; u < 2; ++u) x[u] = Op<T>::mma16(Ti::template row<16>(kt, 16 * u, s, ln), qf[s], x[u]);
+        own_reads_done();
+        int good_next = 0;
+        if (more) {
+            look_up(tile + WAVES);
+            good_next = known(tile + WAVES);
+            fetch(k_cache, tile + WAVES, kt);
+        }
         if (p0 < begin || p0 + 32 > n || good != 3) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -170,16 +173,24 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
                 l += x[u][i];
             }
         const frag p = Op<T>::pack(x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]);
+        if (more)
+            own_loads_done<LOADS>();
+        else
+            own_loads_done<0>();
+        if (has_new && lane < Ti::CH) *reinterpret_cast<u32x4_t *>(vt + Ti::at(old - p0, lane)) = new_value;
+        wave_lds_sync();
 #pragma unroll
         for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, ln), p, acc[i]);
-        own_reads_done();  // the tile is free
+        own_reads_done();
+        if (more) fetch(v_cache, tile + WAVES, vt);
+        good = good_next;
     }
     l += __shfl_xor(l, 16, 64);
     l = halves_sum(l);
 
     // The wavefronts' results: [16 heads][D] values (16-byte pieces of four, permuted by the head against bank conflicts), then maxima and sums.
-    auto place = [&](int w, int h, int c) { return reinterpret_cast<float *>(smem + w * C::RING) + h * D + ((c ^ h) & (D / 4 - 1)) * 4; };
-    auto stat = [&](int w) { return reinterpret_cast<float *>(smem + w * C::RING + 16 * D * 4); };
+    auto place = [&](int w, int h, int c) { return reinterpret_cast<float *>(smem + w * C::ROOM) + h * D + ((c ^ h) & (D / 4 - 1)) * 4; };
+    auto stat = [&](int w) { return reinterpret_cast<float *>(smem + w * C::ROOM + 16 * D * 4); };
 #pragma unroll
     for (int i = 0; i < NO; ++i) *reinterpret_cast<f32x4_t *>(place(wv, col, 4 * i + g)) = acc[i];
     if (g == 0) {
@@ -254,18 +265,27 @@ Pages pages_of(const CacheCall &c) {
     return Pages{c.table, c.pages, __builtin_ctz(static_cast<unsigned>(c.page)), c.width, c.Hk};
 }
 
+template <typename T, int D, bool BIG>
+hipError_t launch_parts(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o, int B, int H, int parts, int window,
+                        float scale, float *part_o, float *part_s, hipStream_t stream) {
+    using S = Step<T, D>;
+    const hipError_t err = allow_lds<&attention_step_kernel<T, D, BIG>>(S::LDS);
+    if (err != hipSuccess) return err;
+    const int sets = (H / c.Hk + 15) / 16;
+    hipLaunchKernelGGL((attention_step_kernel<T, D, BIG>), dim3(static_cast<unsigned>(B) * c.Hk * sets * parts), dim3(64 * S::WAVES), S::LDS, stream,
+                       static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), static_cast<T *>(c.k_cache),
+                       static_cast<T *>(c.v_cache), pages_of(c), lens, static_cast<T *>(o), part_o, part_s, H, parts, window, scale * LOG2E);
+    return hipGetLastError();
+}
+
 template <typename T, int D>
 hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o, int B, int H, int window,
                   float scale, void *workspace, hipStream_t stream) {
-    using S = Step<T, D>;
-    hipError_t err = allow_lds<&attention_step_kernel<T, D>>(S::LDS);
-    if (err != hipSuccess) return err;
-    const int parts = attention_step_parts(B, H, c.Hk, D, c.width * c.page, sizeof(T) == 2), sets = (H / c.Hk + 15) / 16;
+    const int parts = attention_step_parts(B, H, c.Hk, D, c.width * c.page, sizeof(T) == 2);
     float *part_o = static_cast<float *>(workspace), *part_s = part_o + static_cast<size_t>(B) * H * parts * D;
-    hipLaunchKernelGGL((attention_step_kernel<T, D>), dim3(static_cast<unsigned>(B) * c.Hk * sets * parts), dim3(64 * S::WAVES), S::LDS, stream,
-                       static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), static_cast<T *>(c.k_cache),
-                       static_cast<T *>(c.v_cache), pages_of(c), lens, static_cast<T *>(o), part_o, part_s, H, parts, window, scale * LOG2E);
-    err = hipGetLastError();
+    const bool big = 2 * static_cast<size_t>(c.pages) * c.Hk * c.page * D * sizeof(T) > size_t(256) << 20;
+    const hipError_t err = big ? launch_parts<T, D, true>(c, q, k, v, lens, o, B, H, parts, window, scale, part_o, part_s, stream)
+                               : launch_parts<T, D, false>(c, q, k, v, lens, o, B, H, parts, window, scale, part_o, part_s, stream);
     if (err != hipSuccess || parts == 1) return err;
     hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(static_cast<unsigned>(B) * H), dim3(256), 0, stream, part_o, part_s,
                        static_cast<T *>(o), parts);
