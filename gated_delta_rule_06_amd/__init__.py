@@ -876,36 +876,49 @@ def matvec_q4(x, w, scale, zero=None, *, group: int = 128, y=None):
     return y
 
 
-def _sequences(x, name, offsets, lens, i):
-    """(rows N, sequences S) of [B, T, heads, d] or packed [N, heads, d] rows."""
+def _sequences(x, name, offsets, lens):
+    """(rows N, sequences S, device index) of [B, T, heads, d] or packed [N, heads, d] rows."""
     import torch
-    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
-        raise ValueError(f"{name} must be a torch.Tensor [B, T, heads, d], or [N, heads, d] with offsets")
-    if x.dim() == 4:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape, i = x.shape, x.get_device()
+    if len(shape) == 4:
         if offsets is not None:
             raise ValueError("offsets go with packed rows [N, heads, d]")
-        S, N = x.shape[0], x.shape[0] * x.shape[1]
-    else:
+        S, N = shape[0], shape[0] * shape[1]
+    elif len(shape) == 3:
         if offsets is None:
             raise ValueError("packed rows [N, heads, d] need offsets")
         _rank(offsets, "offsets", 1)
-        S, N = offsets.shape[0] - 1, x.shape[0]
+        S, N = offsets.shape[0] - 1, shape[0]
         _is(offsets, "offsets", torch.int32, (S + 1,), i)
+    else:
+        raise ValueError(f"{name} must be [B, T, heads, d], or [N, heads, d] with offsets")
     if lens is not None:
         _is(lens, "lens", torch.int32, (S,), i)
-    return N, S
+    return N, S, i
 
 
 def _attention_inputs(q, k, v, offsets, lens, window, scale):
-    i = q.get_device() if hasattr(q, "get_device") else -1
-    N, S = _sequences(q, "q", offsets, lens, i)
-    _rank(k, "k", q.dim())
-    H, d = q.shape[-2:]
-    kshape = q.shape[:-2] + (k.shape[-2], d)
-    _is(q, "q", q.dtype, q.shape, i)
-    _is(k, "k", q.dtype, kshape, i)
-    _is(v, "v", q.dtype, kshape, i)
-    return (N, S, H, kshape[-2], d), int(window), d ** -0.5 if scale is None else float(scale), _dtype_code(q), i
+    N, S, i = _sequences(q, "q", offsets, lens)
+    shape, dt = q.shape, q.dtype
+    H, d = shape[-2:]
+    _rank(k, "k", len(shape))
+    Hk = k.shape[-2]
+    kshape = (*shape[:-2], Hk, d)
+    _is(q, "q", dt, shape, i)
+    _is(k, "k", dt, kshape, i)
+    _is(v, "v", dt, kshape, i)
+    return (N, S, H, Hk, d), int(window), d ** -0.5 if scale is None else float(scale), _dtype_code(q), i
+
+
+def _like(t, name, like, i):
+    """``t`` checked as an output shaped and typed as ``like``, or a new tensor."""
+    import torch
+    if t is None:
+        return torch.empty_like(like)
+    _is(t, name, like.dtype, like.shape, i)
+    return t
 
 
 def attention_fwd(q, k, v, offsets=None, *, lens=None, window: int = 0, scale=None, o=None, lse=None):
@@ -922,11 +935,11 @@ def attention_fwd(q, k, v, offsets=None, *, lens=None, window: int = 0, scale=No
     """
     import torch
     sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)
-    if o is None:
-        o = torch.empty_like(q)
+    o = _like(o, "o", q, i)
+    if lse is None:
+        lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
     else:
-        _is(o, "o", q.dtype, q.shape, i)
-    lse = _out(lse, "lse", torch.float32, q.shape[:-1], q)
+        _is(lse, "lse", torch.float32, q.shape[:-1], i)
     _call(lib().muir_attention_fwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(offsets),
           _at(lens), o.data_ptr(), lse.data_ptr(), *sizes, window, scale, code)
     return o, lse
@@ -953,24 +966,23 @@ def attention_bwd(q, k, v, o, lse, offsets=None, *, do, lens=None, window: int =
     _is(o, "o", q.dtype, q.shape, i)
     _is(do, "do", q.dtype, q.shape, i)
     _is(lse, "lse", torch.float32, q.shape[:-1], i)
-    out = dict(out) if out else {}
-    for n, x in (("q", q), ("k", k), ("v", v)):
-        out[n] = _out(out.get(n), "d" + n, x.dtype, x.shape, x)
+    out = out or {}
+    dq, dk, dv = (_like(out.get(n), "d" + n, x, i) for n, x in (("q", q), ("k", k), ("v", v)))
     workspace, size = _workspace(workspace, attention_bwd_workspace_size(*sizes, code), q)
     _call(lib().muir_attention_bwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-          lse.data_ptr(), _at(offsets), _at(lens), do.data_ptr(),
-          *[out[n].data_ptr() for n in ATTENTION_GRADS], *sizes, window, scale, code,
-          _at(workspace), size)
-    return out
+          lse.data_ptr(), _at(offsets), _at(lens), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+          dv.data_ptr(), *sizes, window, scale, code, _at(workspace), size)
+    return {**out, "q": dq, "k": dk, "v": dv}
 
 
 def _cache_inputs(k_cache, v_cache, table, B, Hk, d, dtype, i):
     import torch
     _rank(k_cache, "k_cache", 4)
     _rank(table, "table", 2)
-    pages, page, width = k_cache.shape[0], k_cache.shape[2], table.shape[1]
-    _is(k_cache, "k_cache", dtype, (pages, Hk, page, d), i)
-    _is(v_cache, "v_cache", dtype, (pages, Hk, page, d), i)
+    pages, _, page, _ = k_cache.shape
+    width, shape = table.shape[1], (pages, Hk, page, d)
+    _is(k_cache, "k_cache", dtype, shape, i)
+    _is(v_cache, "v_cache", dtype, shape, i)
     _is(table, "table", torch.int32, (B, width), i)
     return pages, page, width
 
@@ -986,13 +998,13 @@ def cache_append(k, v, k_cache, v_cache, table, offsets=None, *, lens=None, star
     0..pages - 1), are left out.
     """
     import torch
-    i = k.get_device() if hasattr(k, "get_device") else -1
-    N, S = _sequences(k, "k", offsets, lens, i)
-    Hk, d = k.shape[-2:]
-    _is(k, "k", k.dtype, k.shape, i)
-    _is(v, "v", k.dtype, k.shape, i)
+    N, S, i = _sequences(k, "k", offsets, lens)
+    shape, dt = k.shape, k.dtype
+    Hk, d = shape[-2:]
+    _is(k, "k", dt, shape, i)
+    _is(v, "v", dt, shape, i)
     code = _dtype_code(k)
-    pages, page, width = _cache_inputs(k_cache, v_cache, table, S, Hk, d, k.dtype, i)
+    pages, page, width = _cache_inputs(k_cache, v_cache, table, S, Hk, d, dt, i)
     if start is not None:
         _is(start, "start", torch.int32, (S,), i)
     _call(lib().muir_cache_append, i, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
@@ -1021,20 +1033,17 @@ def decode_step_attention(q, k, v, k_cache, v_cache, table, lens, *, window: int
     _rank(q, "q", 3)
     _rank(k_cache, "k_cache", 4)
     B, H, d = q.shape
-    Hk, i = k_cache.shape[1], q.get_device()
-    _is(q, "q", q.dtype, (B, H, d), i)
+    Hk, i, dt = k_cache.shape[1], q.get_device(), q.dtype
+    _is(q, "q", dt, (B, H, d), i)
     code = _dtype_code(q)
     if (k is None) != (v is None):
         raise ValueError("k and v come together")
     if k is not None:
-        _is(k, "k", q.dtype, (B, Hk, d), i)
-        _is(v, "v", q.dtype, (B, Hk, d), i)
-    pages, page, width = _cache_inputs(k_cache, v_cache, table, B, Hk, d, q.dtype, i)
+        _is(k, "k", dt, (B, Hk, d), i)
+        _is(v, "v", dt, (B, Hk, d), i)
+    pages, page, width = _cache_inputs(k_cache, v_cache, table, B, Hk, d, dt, i)
     _is(lens, "lens", torch.int32, (B,), i)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _is(o, "o", q.dtype, (B, H, d), i)
+    o = _like(o, "o", q, i)
     workspace, size = _workspace(
         workspace, decode_step_attention_workspace_size(B, H, Hk, d, page, width, code), q)
     _call(lib().muir_decode_step_attention, i, q.data_ptr(), _at(k), _at(v), k_cache.data_ptr(),
