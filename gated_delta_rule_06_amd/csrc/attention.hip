@@ -63,7 +63,7 @@ __global__ __launch_bounds__((64 * Fwd<T, D, SPLIT>::WAVES), (Fwd<T, D, SPLIT>::
     {
         const T *p = q + ((static_cast<size_t>(b.lo) + min(q_row, b.rows - 1)) * H + it.h) * D + 8 * half;
 #pragma unroll
-        for (int s = 0; s < QS; ++s) qf[s] = load8<T>(p + 16 * s);
+        for (int s = 0; s < QS; ++s) qf[s] = load8<T, 32>(p + 16 * s);
     }
     f32x16_t acc[NO] = {};
     float m = LOWEST, l = 0.f;  // base 2, with the scale in

@@ -29,44 +29,87 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -1e30f;
 
 // Eight contraction values of one operand row: lane l has row l % 32, and its element j is contraction index 8 (l / 32) + j
-// of a product's 16. For float32 a product is eight instructions of two contraction values each, one element of every lane.
+// of a product's 16 (frag), or row l % 16 and index 8 (l / 16) + j of 32 (frag16).
 template <typename T> struct Op;
 template <> struct Op<bf16_t> {
     using frag = bf16x8_t;
+    using frag16 = bf16x8_t;
     static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
-    static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
+    static __device__ __forceinline__ f32x4_t mma16(frag16 a, frag16 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
     // Rounds to bf16, nearest even.
-    static __device__ __forceinline__ frag pack(float a, float b, float c, float d, float e, float f, float g, float h) {
-        return frag{static_cast<__bf16>(a), static_cast<__bf16>(b), static_cast<__bf16>(c), static_cast<__bf16>(d),
-                    static_cast<__bf16>(e), static_cast<__bf16>(f), static_cast<__bf16>(g), static_cast<__bf16>(h)};
+    static __device__ __forceinline__ frag pack(const float (&x)[8]) {
+        return frag{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]), static_cast<__bf16>(x[2]), static_cast<__bf16>(x[3]),
+                    static_cast<__bf16>(x[4]), static_cast<__bf16>(x[5]), static_cast<__bf16>(x[6]), static_cast<__bf16>(x[7])};
     }
-    static __device__ __forceinline__ float get(frag f, int j) { return static_cast<float>(f[j]); }
+    static __device__ __forceinline__ frag16 pack16(const float (&x)[8]) { return pack(x); }
 };
+// float32 as three bf16 terms, each the next 8 bits of the value, so they hold all 24. A product is the six of nine whose terms are not
+// below 2^-24 of it: what is left out is as large as one float32 rounding. On the bf16 matrix cores that is 6 instructions of 32 cycles for
+// 16 contraction values, where float32's own take 8 of 64; splitting eight values costs 44 vector instructions beside.
 template <> struct Op<float> {
-    typedef float frag __attribute__((ext_vector_type(8)));
-    static __device__ __forceinline__ f32x16_t mma(frag a, frag b, f32x16_t c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
-        return c;
+    struct frag {
+        bf16x8_t t[3];
+    };
+    typedef float frag16 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x16_t mma(const frag &a, const frag &b, f32x16_t c) {
+        // Smallest first: they are added to a sum that the largest then makes large.
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[2], b.t[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[2], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[1], b.t[1], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[1], b.t[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[1], c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[0], c, 0, 0, 0);
     }
-    static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
+    static __device__ __forceinline__ f32x4_t mma16(frag16 a, frag16 b, f32x4_t c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ frag pack(float a, float b, float c, float d, float e, float f, float g, float h) {
-        return frag{a, b, c, d, e, f, g, h};
+    static __device__ __forceinline__ frag pack(const float (&x)[8]) {
+        float r[8];
+        frag f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            u32x4_t w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = __float_as_uint(r[2 * j]), hi = __float_as_uint(r[2 * j + 1]);
+                w[j] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);  // the upper halves of both
+                if (n < 2) {
+                    r[2 * j] -= __uint_as_float(lo & 0xffff0000u);
+                    r[2 * j + 1] -= __uint_as_float(hi & 0xffff0000u);
+                }
+            }
+            f.t[n] = __builtin_bit_cast(bf16x8_t, w);
+        }
+        return f;
     }
-    static __device__ __forceinline__ float get(frag f, int j) { return f[j]; }
+    static __device__ __forceinline__ frag16 pack16(const float (&x)[8]) { return frag16{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}; }
 };
+// What a lane of an R-row product takes.
+template <typename T, int R> using frag_of = std::conditional_t<R == 32, typename Op<T>::frag, typename Op<T>::frag16>;
+template <typename T, int R> __device__ __forceinline__ frag_of<T, R> make_frag(const float (&x)[8]) {
+    if constexpr (R == 32)
+        return Op<T>::pack(x);
+    else
+        return Op<T>::pack16(x);
+}
 
 // Eight consecutive stored values (16-byte aligned).
-template <typename T> __device__ __forceinline__ typename Op<T>::frag load8(const void *p) {
-    return *static_cast<const typename Op<T>::frag *>(__builtin_assume_aligned(p, 16));
+template <typename T, int R> __device__ __forceinline__ frag_of<T, R> load8(const T *p) {
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const bf16x8_t *>(p);
+    } else {
+        float x[8];
+        load_vec<8>(p, x);
+        return make_frag<T, R>(x);
+    }
 }
 
 // A tile of token rows of D values in LDS, without padding, as the asynchronous loads write it: lane after lane 16 bytes. The
@@ -98,19 +141,19 @@ template <typename T, int D> struct Tile {
     };
 
     // Operand rows r0 + l % R, contraction values 16 s + 8 (l / 32) + j (32 rows) or 32 s + 8 (l / 16) + j (16 rows).
-    template <int R> static __device__ __forceinline__ typename Op<T>::frag row(const unsigned char *t, int r0, int s, const Lane<R> &ln) {
+    template <int R> static __device__ __forceinline__ frag_of<T, R> row(const unsigned char *t, int r0, int s, const Lane<R> &ln) {
         const unsigned char *p = t + r0 * ROWB;
         const int x = ln.row ^ (s * (64 / R) * int(sizeof(T)) / 2 << 4);
         if constexpr (sizeof(T) == 2) {
             return *reinterpret_cast<const bf16x8_t *>(p + x);
         } else {
             const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p + x), b = *reinterpret_cast<const f32x4_t *>(p + (x ^ 16));
-            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            return make_frag<T, R>({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
         }
     }
     // Operand rows are the tile's columns c0 + l % R; element j is tile row r0 + 4 (l / R) + j % 4, and 256 / R rows on
     // for j >= 4: the order in which two 4-row groups of an accumulator lie in a lane. r0 is a multiple of 16.
-    template <int R> static __device__ __forceinline__ typename Op<T>::frag col(unsigned char *t, int r0, int c0, const Lane<R> &ln) {
+    template <int R> static __device__ __forceinline__ frag_of<T, R> col(unsigned char *t, int r0, int c0, const Lane<R> &ln) {
         constexpr int NEXT = 256 / R, FLIP = R == 32 ? 2 << 4 : 0;  // of the permutation, eight rows on
         unsigned char *p = t + r0 * ROWB;
         const int x = ln.col ^ (c0 * int(sizeof(T)) >> 4 << 4);
@@ -120,11 +163,11 @@ template <typename T, int D> struct Tile {
             const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + NEXT * ROWB + (x ^ FLIP)));
             return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            typename Op<T>::frag f;
+            float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 f[j] = *reinterpret_cast<const float *>(p + (j % 4 + j / 4 * NEXT) * ROWB + (x ^ (j % 4 << 6) ^ (j / 4 * FLIP)));
-            return f;
+            return make_frag<T, R>(f);
         }
     }
     // Four consecutive values from column c on (a multiple of 4) of row r.
@@ -177,7 +220,7 @@ __device__ __forceinline__ float halves_sum(float x) {
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i / 4) + 4 * (lane / 32) + i % 4; }
 // Eight accumulators as the operand of step s (of two).
 template <typename T> __device__ __forceinline__ typename Op<T>::frag acc_frag(const f32x16_t &x, int s) {
-    return Op<T>::pack(x[8 * s], x[8 * s + 1], x[8 * s + 2], x[8 * s + 3], x[8 * s + 4], x[8 * s + 5], x[8 * s + 6], x[8 * s + 7]);
+    return Op<T>::pack({x[8 * s], x[8 * s + 1], x[8 * s + 2], x[8 * s + 3], x[8 * s + 4], x[8 * s + 5], x[8 * s + 6], x[8 * s + 7]});
 }
 
 // A wavefront's 32 rows, given transposed in accumulators, through its own LDS room to `rows` rows of `stride` elements, times f; zeros where not live.

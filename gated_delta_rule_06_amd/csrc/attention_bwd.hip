@@ -77,11 +77,13 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     float d = 0.f;
 #pragma unroll
     for (int s = 0; s < QS; ++s) {
-        qf[s] = load8<T>(q + own * D + 16 * s + 8 * half);
-        df[s] = load8<T>(dout + own * D + 16 * s + 8 * half);
-        const frag of = load8<T>(o + own * D + 16 * s + 8 * half);
+        qf[s] = load8<T, 32>(q + own * D + 16 * s + 8 * half);
+        df[s] = load8<T, 32>(dout + own * D + 16 * s + 8 * half);
+        float x[8], y[8];
+        load_vec<8>(o + own * D + 16 * s + 8 * half, x);
+        load_vec<8>(dout + own * D + 16 * s + 8 * half, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d = fmaf(Op<T>::get(of, j), Op<T>::get(df[s], j), d);
+        for (int j = 0; j < 8; ++j) d = fmaf(x[j], y[j], d);
     }
     d = halves_sum(d);
     const float l = lse[own];
@@ -203,7 +205,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
                 float c[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) c[i] = acc_row(8 * s + i, lane) == (lane & 31) ? f : 0.f;
-                const frag diagonal = Op<T>::pack(c[0], c[1], c[2], c[3], c[4], c[5], c[6], c[7]);
+                const frag diagonal = Op<T>::pack(c);
 #pragma unroll
                 for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(room, 32 * x + 16 * s, 32 * n, ln), diagonal, acc[n]);
             }
@@ -276,8 +278,8 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     frag kf[QS], vf[QS];
 #pragma unroll
     for (int s = 0; s < QS; ++s) {
-        kf[s] = load8<T>(k + own * D + 16 * s + 8 * half);
-        vf[s] = load8<T>(v + own * D + 16 * s + 8 * half);
+        kf[s] = load8<T, 32>(k + own * D + 16 * s + 8 * half);
+        vf[s] = load8<T, 32>(v + own * D + 16 * s + 8 * half);
     }
     f32x16_t dka[NO] = {}, dva[NO] = {};
 

@@ -67,7 +67,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
     float scale2) {
     using C = Step<T, D>;
     using Ti = Tile<T, D>;
-    using frag = typename Op<T>::frag;
+    using frag = typename Op<T>::frag16;
     constexpr int WAVES = C::WAVES, TILE = C::TILE, QS = D / 32, NO = D / 16;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
 #pragma unroll
     for (int s = 0; s < QS; ++s) {
         qf[s] = frag{};
-        if (col < heads) qf[s] = load8<T>(q + (static_cast<size_t>(b) * H + h0 + col) * D + 32 * s + 8 * g);
+        if (col < heads) qf[s] = load8<T, 16>(q + (static_cast<size_t>(b) * H + h0 + col) * D + 32 * s + 8 * g);
     }
     f32x4_t acc[NO] = {};
     float m = LOWEST, l = 0.f;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
                 x[u][i] = __builtin_amdgcn_exp2f(fmaf(x[u][i], scale2, -m));
                 l += x[u][i];
             }
-        const frag p = Op<T>::pack(x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]);
+        const frag p = Op<T>::pack16({x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]});
         if (more)
             own_loads_done<LOADS>();
         else
