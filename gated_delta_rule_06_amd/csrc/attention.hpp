@@ -195,6 +195,18 @@ template <typename T, int D> struct Tile {
 // Keeps what follows it in a branch there: the compiler would rather make selects of it for everybody.
 #define KEEP_BRANCH asm volatile("")
 
+// Order of a stretch of code that multiplies operands as it reads them: one step's reads first (and FIRST others), then in turn a step's products and the reads of
+// the step after it. The compiler's own order waits for each operand right after asking for it.
+template <int STEPS, int READS, int PRODUCTS, int FIRST = 0> __device__ __forceinline__ void read_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, FIRST + READS, 0);
+#pragma unroll
+    for (int s = 1; s < STEPS; ++s) {
+        __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS, 0);
+}
+
 // Waits for every load of this wavefront; the barrier behind it makes all wavefronts' tiles visible.
 __device__ __forceinline__ void loads_done() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
