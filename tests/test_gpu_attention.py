@@ -105,6 +105,46 @@ def test_packed_sequences(device, dt, d, window):
     check(q, k, v, do, oa.spans(N, offsets, tokens), off, lens=tokens, window=window)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(32, 32), (64, 32)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_plenty_of_blocks(device, d, H, Hk, window):
+    """So many heads and sequences that bfloat16 takes 128 rows to a workgroup for queries and keys: packed, and padded with lengths."""
+    lens = [0, 1, 129, 128, 33, 0, 140, 127, 64, 0, 31, 65]
+    offsets = [0]
+    for n in lens:
+        offsets.append(offsets[-1] + n)
+    N = offsets[-1] + 5
+    q, k, v, do = make(device, BF, (N,), H, Hk, d, d + H)
+    for x in (q, k, v, do):
+        x[offsets[-1]:] = float("nan")
+    check(q, k, v, do, oa.spans(N, offsets), torch.tensor(offsets, dtype=torch.int32, device=device), window=window)
+    B, T = 8, 135
+    q, k, v, do = make(device, BF, (B, T), H, Hk, d, d + H + 1)
+    lens = [135, 0, 1, 128, 129, 97, 32, 134]
+    for b, n in enumerate(lens):
+        for x in (q, k, v, do):
+            x[b, n:] = float("nan")
+    check(q, k, v, do, [(b * T, n) for b, n in enumerate(lens)], lens=torch.tensor(lens, dtype=torch.int32, device=device), window=window)
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (FL, 64), (FL, 128)])
+def test_long_rows_with_many_heads(device, dt, d):
+    """Rows with more tiles of keys than are in flight at once, in many workgroups; the last rows of several sequences."""
+    q, k, v, do = make(device, dt, (2, 517), 45, 45, d, 77)
+    heads = [0, 22, 44]
+    o, lse = muir.attention_fwd(q, k, v)
+    g = muir.attention_bwd(q, k, v, o, lse, do=do)
+    Q, K, V, G = (flat(x)[:, heads].cpu() for x in (q, k, v, do))
+    where = [(0, 517), (517, 517)]
+    want, wl = oa.forward(Q, K, V, where)
+    bo, bl = forward_bounds(Q, K, V, where)
+    assert ((flat(o)[:, heads].double().cpu() - want).abs() <= bo).all() and ((lse.flatten(0, 1)[:, heads].double().cpu() - wl).abs() <= bl).all()
+    want, bounds = oa.backward(Q, K, V, G, where), backward_bounds(Q, K, V, G, where)
+    for n in muir.ATTENTION_GRADS:
+        assert ((flat(g[n])[:, heads].double().cpu() - want[n]).abs() <= bounds[n]).all(), n
+
+
 def test_many_short_sequences(device):
     """More sequences than lanes that look for them, many empty."""
     g = torch.Generator().manual_seed(3)

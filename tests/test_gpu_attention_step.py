@@ -155,3 +155,19 @@ def test_cache_past_32_bits(device):
     o = muir.decode_step_attention(q, k, v, kc, vc, table, lens)
     near = muir.decode_step_attention(q, k, v, ks, vs, torch.where(table >= 0, table - far, table), lens)
     assert torch.equal(o, near) and same(kc[far:], ks) and same(vc[far:], vs)
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (FL, 64), (FL, 128)])
+def test_large_cache(device, dt, d):
+    """Caches of more than 256 MB, read past the last-level cache: the bits that a small cache gives, which other tests check."""
+    Hk, page = 2, 64
+    pages = (1 << 28) // (2 * Hk * page * d * dt.itemsize) + 20
+    q, k, v, ks, vs, table, lens = setup(device, dt, [0, 1, 70, 900, 64], 6, Hk, d, page, d)
+    kc, vc = (torch.full((pages, Hk, page, d), float("nan"), dtype=dt, device=device) for _ in range(2))
+    far = pages - ks.shape[0]
+    kc[far:], vc[far:] = ks, vs
+    for window in (0, 100):
+        o = muir.decode_step_attention(q, k, v, kc, vc, torch.where(table >= 0, table + far, table), lens, window=window)
+        near = muir.decode_step_attention(q, k, v, ks, vs, table, lens, window=window)
+        assert torch.isfinite(o).all() and torch.equal(o, near) and same(kc[far:], ks) and same(vc[far:], vs)
+    assert torch.isnan(kc[:far]).all() and torch.isnan(vc[:far]).all()
