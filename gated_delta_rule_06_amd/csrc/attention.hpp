@@ -25,8 +25,9 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// A running maximum before any key: below every score, and finite, so that differences from it stay numbers.
-constexpr float LOWEST = -1e30f;
+// A running maximum before any key: below scores of any size that a sum of products leaves exact, and finite, so that differences from it stay
+// numbers.
+constexpr float LOWEST = -3e38f;
 
 // Eight contraction values of one operand row: lane l has row l % 32, and its element j is contraction index 8 (l / 32) + j
 // of a product's 16 (frag), or row l % 16 and index 8 (l / 16) + j of 32 (frag16).

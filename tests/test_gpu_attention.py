@@ -167,6 +167,22 @@ def test_scores_far_apart(device, dt):
     check(q, k, v, do, [(b * T, T) for b in range(3)], scale=1.5)
 
 
+@pytest.mark.parametrize("dt", [BF, FL])
+@pytest.mark.parametrize("T,H", [(1, 1), (5, 1), (70, 1), (100, 300)])
+def test_scores_near_the_lowest(device, dt, T, H):
+    """Every score the same and about -2e32: exponentials are 1, so o is the mean of the values seen, their sum off by at most n w."""
+    q, k, v, _ = make(device, dt, (1, T), H, H, 64, T)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[..., 0] = 2.0 ** 57, -2.0 ** 53
+    o, lse = muir.attention_fwd(q, k, v)
+    n = torch.arange(1, T + 1)[:, None, None]
+    V = v[0].double().cpu()
+    off = (o[0].double().cpu() - V.cumsum(0) / n).abs()
+    u = torch.finfo(dt).eps / 2
+    assert (off <= (u + 2 * (n + 8) * 2.0 ** -24) * V.abs().cumsum(0) / n).all() and torch.isfinite(lse).all()
+
+
 def test_no_rows(device):
     x = torch.zeros(2, 0, 2, 64, device=device)
     o, lse = muir.attention_fwd(x, x, x)

@@ -91,6 +91,21 @@ def test_read_only(device):
     assert (o[0] == 0).all()
 
 
+@pytest.mark.parametrize("dt", [BF, FL])
+@pytest.mark.parametrize("B,n", [(200, 40), (1, 3000)])
+def test_scores_near_the_lowest(device, dt, B, n):
+    """Every score the same and about -2e32 (as of a prompt): o is the mean of the cached values."""
+    q, _, _, kc, vc, table, lens = setup(device, dt, [n] * B, 2, 1, 64, 64, 4, extra=0)
+    q.zero_()
+    kc.zero_()
+    q[..., 0], kc[..., 0] = 2.0 ** 57, -2.0 ** 53
+    o = muir.decode_step_attention(q, None, None, kc, vc, table, lens)
+    u = torch.finfo(dt).eps / 2
+    for b in range(B):
+        V = oa.cached(vc.cpu(), table.cpu(), b, n)[0][:, 0].double()
+        assert ((o[b].double().cpu() - V.mean(0)).abs() <= (u + 2 * (n + 8) * W) * V.abs().mean(0)).all()
+
+
 def test_left_out_and_missing(device):
     """Negative lengths and full tables take no part; tokens in no page are not seen, and a new token in none is not kept."""
     q, k, v, kc, vc, table, lens = setup(device, BF, [50, -1, 64, 63, 20, 40, -2 ** 31, 2 ** 31 - 1][:6], 4, 2, 64, 16, 8)
