@@ -931,7 +931,8 @@ def attention_fwd(q, k, v, offsets=None, *, lens=None, window: int = 0, scale=No
     bfloat16, d 64 or 128; ``scale`` defaults to d ** -0.5. Returns (o, lse): o like q, and the
     logarithm of each row's sum of exponentials, float32 [..., H], which :func:`attention_bwd`
     takes. Rows that are no token have o = 0 and lse = -infinity. A NaN or infinity in a token's v
-    can reach the o of up to 127 tokens before it.
+    can reach the o of tokens up to 127 before it, and with a window up to 127 behind those that see
+    it; in float32 an infinity comes as NaN.
     """
     import torch
     sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)

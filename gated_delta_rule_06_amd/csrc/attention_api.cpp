@@ -10,8 +10,9 @@ namespace {
 
 using namespace muir;
 
-// Workgroups of a launch, which has 256 threads each and less than 2^32 in all.
-constexpr long long kMaxBlocks = (1 << 24) - 1;
+// Workgroups of a launch, which has 256 threads each (a step 512) and less than 2^32 in all.
+constexpr long long kMaxBlocks = (1 << 24) - 1, kMaxStepBlocks = (1 << 23) - 1;
+constexpr float kMinScale = 0x1p-64f;  // lse over the scale is still a float32
 constexpr int kMaxH = 1 << 15;     // 64 rows are addressed with 32-bit offsets
 constexpr int kMaxRows = 1 << 30;  // places of rows, and a few blocks behind them, are ints
 
@@ -35,7 +36,7 @@ muir_status_t check_rows(const char *fn, int N, int S, const int *offsets, int p
 
 muir_status_t check_scores(const char *fn, int window, float scale) {
     if (window < 0) return fail(MUIR_ERR_SHAPE, "%s: window must be >= 0 (got %d)", fn, window);
-    if (!(scale > 0.f) || isinf(scale)) return fail(MUIR_ERR_SHAPE, "%s: scale must be finite and above 0", fn);
+    if (!(scale >= kMinScale) || isinf(scale)) return fail(MUIR_ERR_SHAPE, "%s: scale must be finite and at least 2^-64", fn);
     return MUIR_OK;
 }
 
@@ -52,7 +53,7 @@ size_t offset_bytes(int S) { return (static_cast<size_t>(S) + 1) * 4; }
 bool step_sizes_ok(int B, int H, int Hk, int d, int page, int width, muir_dtype_t type) {
     return B >= 1 && H >= 1 && Hk >= 1 && H % Hk == 0 && H <= kMaxH && (d == 64 || d == 128) && known(type) && width >= 1 && page >= 16 &&
            page <= 256 && (page & (page - 1)) == 0 && static_cast<long long>(width) * page <= (1 << 30) &&
-           static_cast<long long>(B) * Hk * ((H / Hk + 15) / 16) <= kMaxBlocks;
+           static_cast<long long>(B) * Hk * ((H / Hk + 15) / 16) <= kMaxStepBlocks;
 }
 
 }  // namespace

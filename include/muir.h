@@ -571,10 +571,12 @@ muir_status_t muir_matvec_q4(
  *                                        0..N). NULL: N / S rows each, a padded batch [S, N / S, ...]
  *   lens     [S] int32 or NULL           tokens of each sequence, from its first row on (clamped to its rows; NULL: all of them)
  *   lse      [N, H] float32 or NULL      which muir_attention_bwd takes
- *   H a multiple of Hk; d 64 or 128; window >= 0, 0 for no limit; scale finite and above 0 (usually d^(-1/2)); N >= 0
+ *   H a multiple of Hk; d 64 or 128; window >= 0, 0 for no limit; scale finite and at least 2^-64 (usually d^(-1/2)); N >= 0
  *
  * Rows that are no token (behind a sequence's length, or behind the last sequence) have o = 0 and lse = -infinity, and what k and v hold
- * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of up to 127 tokens before it (as 0 times it).
+ * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of tokens up to 127 before it, and with a window
+ * up to 127 behind the last that sees it (as 0 times it). float32 products are made of three bf16 terms: an infinity in them comes as NaN.
+ * Offsets that do not ascend leave rows of the outputs unset, and never touch anything outside them.
  * bf16: exp(s_ij - m_i) is rounded to bf16 before it multiplies v_j; sums, maxima and lse are float32. Errors as for muir_chunk_fwd,
  * and MUIR_ERR_UNSUPPORTED for H above 2^15, N above 2^30 or (N / 128 + S + 1) H
  * above 2^24 - 1 (float32: N / 32).
@@ -593,7 +595,8 @@ muir_status_t muir_attention_fwd(
  *   workspace: muir_attention_bwd_workspace_size(...) bytes
  *
  * Rows that are no token have gradients 0, and dout and o are not looked at there. Every sum is float32, in a fixed order. In bf16 p and ds
- * are rounded to bf16 before the products that sum them. A NaN or infinity in a token can reach the gradients of tokens up to 127 before and behind those that see it.
+ * are rounded to bf16 before the products that sum them, and D takes in what the rounding of o left out. A NaN or infinity in a token can
+ * reach the gradients of tokens up to 127 before and behind those that see it.
  */
 size_t muir_attention_bwd_workspace_size(int N, int S, int H, int Hk, int d, muir_dtype_t qkv);
 muir_status_t muir_attention_bwd(
@@ -629,7 +632,8 @@ muir_status_t muir_cache_append(
  *
  * A sequence with lens[b] < 0, or whose table has no room for its tokens, takes no part: o is 0 and nothing is written. Tokens in no page are
  * not seen (and a new one is not kept); where none is seen o is 0. What a page holds behind the last token reaches nothing. The page that a new token
- * goes to must not be read by another sequence of the same call; pages before it may be shared.
+ * goes to must not be read by another sequence of the same call; pages before it may be shared. MUIR_ERR_UNSUPPORTED where
+ * B Hk ceil(H / Hk / 16) is above 2^23 - 1.
  */
 size_t muir_decode_step_attention_workspace_size(int B, int H, int Hk, int d, int page, int width,
                                                  muir_dtype_t type);

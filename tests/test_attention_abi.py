@@ -31,7 +31,7 @@ SIZE_ARGS = dict(N=1000, S=5, H=6, Hk=3, d=64, window=0, scale=0.125, dt=BF)
 BAD_SIZES = [
     (dict(N=-1), 2), (dict(S=0), 2), (dict(H=0), 2), (dict(Hk=0), 2), (dict(Hk=4), 2), (dict(d=32), 3), (dict(d=96), 3), (dict(d=256), 3),
     (dict(dt=2), 3), (dict(window=-1), 2), (dict(scale=0.0), 2), (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2),
-    (dict(scale=float("inf")), 2), (dict(N=(1 << 30) + 1, H=1, Hk=1), 3), (dict(N=1 << 30), 3), (dict(S=1 << 24), 3), (dict(H=1 << 16, Hk=1), 3),
+    (dict(scale=float("inf")), 2), (dict(scale=2.0 ** -65), 2), (dict(N=(1 << 30) + 1, H=1, Hk=1), 3), (dict(N=1 << 30), 3), (dict(S=1 << 24), 3), (dict(H=1 << 16, Hk=1), 3),
     (dict(N=1001, offsets=None), 2),
 ]
 FWD = ["q", "k", "v", "offsets", "lens", "o", "lse", *SIZES]
@@ -83,7 +83,7 @@ STEP_ARGS = dict({n: fake(i) for i, n in enumerate(STEP[:8])}, B=5, H=6, Hk=3, d
 
 @pytest.mark.parametrize("over,status", CACHE + [
     (dict(B=0), 2), (dict(H=7), 2), (dict(window=-3), 2), (dict(scale=0.0), 2), (dict(k=None), 1), (dict(v=None), 1), (dict(q=None), 1), (dict(lens=None), 1),
-    (dict(o=None), 1), (dict(B=1 << 24, Hk=1, H=1), 3), (dict(ws=None), 4), (dict(wsb=16), 4), (dict(o=fake(0)), 5), (dict(o=fake(3)), 5),
+    (dict(o=None), 1), (dict(B=1 << 24, Hk=1, H=1), 3), (dict(B=1 << 23, Hk=1, H=1), 3), (dict(scale=2.0 ** -65), 2), (dict(ws=None), 4), (dict(wsb=16), 4), (dict(o=fake(0)), 5), (dict(o=fake(3)), 5),
     (dict(k_cache=fake(2)), 5), (dict(ws=fake(4)), 5), (dict(q=fake(0, 8)), 2), (dict(table=fake(5, 1)), 2),
 ])
 def test_step_refusals(over, status):
