@@ -113,6 +113,10 @@ template <typename T, int R> __device__ __forceinline__ frag_of<T, R> load8(cons
     }
 }
 
+// The transposing read. Through a function of a `restrict` pointer, as plain reads of LDS carry their type: without either the compiler takes it
+// to read what asynchronous loads on their way are writing, and waits for all of them.
+__device__ __forceinline__ s16x4_t read_transposed(lds_s16x4 *__restrict__ p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
+
 // A tile of token rows of D values in LDS, without padding, as the asynchronous loads write it: lane after lane 16 bytes. The
 // 16-byte pieces of a row are permuted by its number so that reading one piece of 16 rows (operand rows) and 64 bytes of
 // eight rows (the transposing reads) both take every bank evenly. The permutation repeats every 16 rows.
@@ -160,8 +164,8 @@ template <typename T, int D> struct Tile {
         const int x = ln.col ^ (c0 * int(sizeof(T)) >> 4 << 4);
         if constexpr (sizeof(T) == 2) {
             // The transposing read gives lane m of sixteen the column m of the four rows whose 32 bytes the lanes address.
-            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + x));
-            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + NEXT * ROWB + (x ^ FLIP)));
+            const s16x4_t lo = read_transposed((lds_s16x4 *)(p + x));
+            const s16x4_t hi = read_transposed((lds_s16x4 *)(p + NEXT * ROWB + (x ^ FLIP)));
             return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             float f[8];
