@@ -202,9 +202,7 @@ template <typename T, int D, bool SPLIT> hipError_t launch(const AttentionCall &
 }
 
 template <typename T, int D> hipError_t launch(const AttentionCall &c, void *o, float *lse, hipStream_t stream) {
-    if constexpr (sizeof(T) == 2)
-        if (!attention_split(c.N, c.S, c.H)) return launch<T, D, false>(c, o, lse, stream);
-    return launch<T, D, true>(c, o, lse, stream);
+    return attention_split(c.N, c.S, c.H, D, c.window) ? launch<T, D, true>(c, o, lse, stream) : launch<T, D, false>(c, o, lse, stream);
 }
 
 }  // namespace

@@ -421,9 +421,9 @@ template <typename T, int D> hipError_t launch(const AttentionCall &c, const Att
     float *tops = static_cast<float *>(workspace), *deltas = tops + up256(static_cast<size_t>(c.N) * c.H * 4) / 4;
     hipError_t err;
     if constexpr (sizeof(T) == 2) {
-        err = attention_split(c.N, c.S, c.H) ? launch_dq<T, D, true>(c, g, tops, deltas, stream) : launch_dq<T, D, false>(c, g, tops, deltas, stream);
+        err = attention_split(c.N, c.S, c.H, D, c.window) ? launch_dq<T, D, true>(c, g, tops, deltas, stream) : launch_dq<T, D, false>(c, g, tops, deltas, stream);
         if (err == hipSuccess)
-            err = attention_split(c.N, c.S, c.Hk) ? launch_dkv<T, D, true>(c, g, tops, deltas, stream) : launch_dkv<T, D, false>(c, g, tops, deltas, stream);
+            err = attention_split(c.N, c.S, c.Hk, D, c.window) ? launch_dkv<T, D, true>(c, g, tops, deltas, stream) : launch_dkv<T, D, false>(c, g, tops, deltas, stream);
     } else {
         err = launch_dq<T, D, true>(c, g, tops, deltas, stream);
         if (err == hipSuccess) err = launch_dkv<T, D, true>(c, g, tops, deltas, stream);

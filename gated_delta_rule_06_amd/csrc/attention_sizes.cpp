@@ -6,12 +6,22 @@
 
 namespace muir {
 
-// Where 128 rows to a workgroup make fewer than two of them to a compute unit, blocks of 32 rows whose wavefronts share the keys (or the queries) fill the
-// card better: forward and backward of bf16 B1 T2048 H12 d128, 216 such workgroups, 31 and 89 us against 52 and 138 with 128 rows; at T4096 H16 (544) both
-// 104 us; at B4 T1024 H16 (592) 46 and 133 against 43 and 101. In float32 the products take so long that rows are never too few for it: d64 is
-// faster at every size measured (B1 T128 H12 7.3 and 20 us against 15 and 43, B8 T4096 H16 2.24 and 7.38 ms against 2.38 and 7.82), d128 up to
-// B4 T1024 H16 (201 and 666 us against 218 and 830), and at B8 T4096 H16 7 and 3 % slower.
-bool attention_split(int N, int S, int heads) { return attention_blocks(N, S, 128) * heads <= 400; }
+// bf16: 128 rows to a workgroup, or blocks of 32 whose four wavefronts share the keys (or the queries). The first reads each key a quarter as often; the
+// second fills the card with few rows, and does not wait for the workgroup with the most keys, which without a window has twice the mean. Measured,
+// forward and backward in us, of blocks of 32 and of 128 rows, by the number W of the latter:
+//   d128, T <= 1024:      W 300 (T1024 H30) 24.8, 76 and 29.4, 84     W 400 (T1024 H40) 30.9, 96 and 30.7, 90
+//   d128, T >= 2048:      W 544 (T4096 H16) 108, 308 and 119, 345     W 680 (T4096 H20) 135, 401 and 152, 390
+//   d128, a short window: W 136 (T4096 H4, 512) 13.3, 41 and 21.2, 57 W 204 (T4096 H6, 512) 23.6, 68 and 22.3, 59
+//   d64, a quarter more:  W 400 (T1024 H40) 16.6, 53 and 20.7, 59     W 720 (T2048 H40) 45.1, 133 and 45.8, 138
+//                         W 136 (T4096 H4, 512) 9.3, 25 and 13.9, 38  W 272 (T4096 H8, 512) 13.5, 43 and 14.5, 39
+// Lengths are taken for equal, as they lie on the device.
+// float32: the same in the forward (d64 B4 T1024 H16, W 592, 77 and 80, B8 T4096 H16 1728 and 1600; d128 163 and 146, 3856 and 3199). The backward has
+// blocks of 32 only: d64 233 and 260, 5570 and 5728; d128 546 and 643, and only the largest gains by 128 (13036 and 12467).
+bool attention_split(int N, int S, int heads, int d, int window) {
+    const int length = N / S;
+    const int most = window && window <= length / 2 ? 160 : length < 2048 ? 350 : 600;
+    return attention_blocks(N, S, 128) * heads <= (d == 64 ? most * 5 / 4 : most);
+}
 
 size_t attention_bwd_workspace_bytes(int N, int H) { return 2 * up256(static_cast<size_t>(N) * H * 4); }
 
