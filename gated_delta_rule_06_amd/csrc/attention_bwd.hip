@@ -8,7 +8,8 @@
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
 // (2-norm, relative) where one rounding is 0.0017. But sum_j ds_ij = 0, so dq's kernel finds e_i as the sum of its own ds, hands the
 // exact D on to dk, and takes e_i sum_j p_ij k_j off dq, of that sum only the largest p of each of a wavefront's halves: the rest is
-// small, and is times e_i. 0.0024 and 0.0024 then.
+// small, and is times e_i. 0.0024 and 0.0024 then. Where wavefronts share the keys the same product adds what the ds of those eight keys lost when they
+// were rounded, most of what a row's ds lose: dq 0.0019 (with 128 rows that costs 4 % of dq's time, and is left out).
 #include "attention.hpp"
 #include "attention_kernels.hpp"
 #include "launch.hpp"
@@ -92,8 +93,8 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     d = live ? d : 0.f;
     f32x16_t acc[NO] = {};
     float e[2] = {};  // sums of ds
-    // The lane's largest p so far, its last four bits the accumulator element that it was, and the first key of its 32.
-    uint32_t best = 0;
+    // The lane's largest p so far, where it was (the first key of its 32, and the accumulator's element), and (SPLIT) what its ds lost to bf16.
+    float best = 0.f, rest = 0.f;
     int best_at = 0;
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
@@ -125,13 +126,19 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
                 float most = x[0];
 #pragma unroll
                 for (int i = 1; i < 16; ++i) most = fmaxf(most, x[i]);
-                if (__any(most > __uint_as_float(best))) {  // seldom, after the first few
+                if (__any(most > best)) {  // seldom, after the first few dozen tiles
                     KEEP_BRANCH;
-                    uint32_t which = 0;
+                    int which = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) which = max(which, (__float_as_uint(x[i]) & ~15u) | static_cast<uint32_t>(i));
-                    best_at = which > best ? j * KEYS + 32 * t : best_at;
-                    best = max(best, which);
+                    for (int i = 0; i < 16; ++i) which = x[i] == most ? i : which;
+                    if constexpr (SPLIT) {
+                        float ds = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) ds = x[i] == most ? most * y[i] : ds;
+                        rest = most > best ? ds - static_cast<float>(static_cast<__bf16>(ds)) : rest;
+                    }
+                    best_at = most > best ? j * KEYS + 32 * t + which : best_at;
+                    best = fmaxf(best, most);
                 }
             }
 #pragma unroll
@@ -185,10 +192,11 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
             lds_barrier();
         }
         d += off;
-        // The keys come as two tiles of 32, one for each query and half, and the factors are a diagonal matrix: dq^T += k^T (-e p). A lane without
+        // The keys come as two tiles of 32, one for each query and half, and the factors are a diagonal matrix: dq^T += k^T (rest - e p). A lane without
         // a largest p takes its own token's key, times 0, and one whose query is no token, and may hold anything, some token's.
-        const int place = (best & 15u) / 4 * 8 + 4 * half + (best & 3u), mine = min(best >= 16u ? best_at + place : q_row, max(b.n - 1, 0));
-        const auto ps = __builtin_amdgcn_permlane32_swap(best & ~15u, best & ~15u, false, false);
+        const int place = best_at / 32 * 32 + best_at % 16 / 4 * 8 + 4 * half + best_at % 4, mine = min(best > 0.f ? place : q_row, max(b.n - 1, 0));
+        const auto ps = __builtin_amdgcn_permlane32_swap(__float_as_uint(best), __float_as_uint(best), false, false);
+        const auto rests = __builtin_amdgcn_permlane32_swap(__float_as_uint(rest), __float_as_uint(rest), false, false);
         unsigned char *room = smem + wv * 64 * Ti::ROWB;
 #pragma unroll
         for (int n = 0; n < 64 / Ti::RPI; ++n) {
@@ -199,7 +207,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
         own_loads_done<0>();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float f = -off * __uint_as_float(ps[x]);
+            const float f = fmaf(-off, __uint_as_float(ps[x]), __uint_as_float(rests[x]));
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 float c[8];
