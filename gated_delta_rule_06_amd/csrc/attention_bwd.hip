@@ -4,15 +4,15 @@
 // Two kernels, each with its sums in registers from the first to the last product, so no sum depends on an order and nothing is
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed): one kernel would have to add dq atomically, and its bits would depend on the
-// order. bf16 B8 T4096 H16 d128: dq 0.87 ms, dkv 1.03 ms, 950 and 1070 TFLOP/s of the products made; matrix cores busy in 50 and
+// order. bf16 B8 T4096 H16 d128: dq 0.89 ms, dkv 1.03 ms, 930 and 1070 TFLOP/s of the products made; matrix cores busy in 50 and
 // 57 % of the cycles at 1.6 to 1.8 GHz, two workgroups to a compute unit by registers (240 and 256) and LDS. Packed with a window of 512 (13731 rows,
-// H16 Hk4) 122 and 132 us, matrix cores busy in 33 and 35 %: 7 and 1.8 workgroups to a compute unit do not come out even.
+// H16 Hk4) 128 and 132 us, matrix cores busy in 33 and 35 %: 7 and 1.8 workgroups to a compute unit do not come out even.
 // bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
 // (2-norm, relative) where one rounding is 0.0017. But sum_j ds_ij = 0, so dq's kernel finds e_i as the sum of its own ds, hands the
 // exact D on to dk, and takes e_i sum_j p_ij k_j off dq, of that sum only the largest p of each of a wavefront's halves: the rest is
-// small, and is times e_i. 0.0024 and 0.0024 then. Where wavefronts share the keys the same product adds what the ds of those eight keys lost when they
-// were rounded, most of what a row's ds lose: dq 0.0019 (with 128 rows that costs 4 % of dq's time, and is left out).
+// small, and is times e_i. The same product adds what the ds of those keys lost when they were rounded, most of what a row's ds lose. dq is 0.0021 off
+// then, dk 0.0024.
 #include "attention.hpp"
 #include "attention_kernels.hpp"
 #include "launch.hpp"
@@ -96,10 +96,12 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     d = live ? d : 0.f;
     f32x16_t acc[NO] = {};
     float e[2] = {};  // sums of ds
-    // The lane's largest p so far, its last four bits the accumulator element that it was, the first key of its 32, and (SPLIT) what its ds lost to bf16.
+    // About the lane's largest p so far, its last four bits the accumulator element that it was, the first key of its 32, and what its ds lost to bf16.
+    // Only a p above `bar` is taken, 1/8 at first and half as much again as the last: of smaller ones there is little to correct, and each costs
+    // the wavefront a look at all its scores (from 1/16 on dq took 0.91 ms at B8 T4096 H16 d128 and was 0.0020 off, from 1/8 on 0.89 and 0.0021).
     uint32_t best = 0;
-    int best_at = 0;
-    float rest = 0.f;
+    int best_at = -1;
+    float rest = 0.f, bar = 0.125f;
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
         ln.again();
@@ -126,33 +128,33 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], scale2, top));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                y[i] *= x[i];
+                if constexpr (EXACT_D<T>) e[i & 1] += y[i];
+            }
             if constexpr (EXACT_D<T>) {
                 float most = x[0];
 #pragma unroll
                 for (int i = 1; i < 16; ++i) most = fmaxf(most, x[i]);
-                if (__any(most > __uint_as_float(best))) {  // seldom, after the first few dozen tiles
+                if (__any(most > bar)) {
                     KEEP_BRANCH;
                     uint32_t which = 0;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) which = max(which, (__float_as_uint(x[i]) & ~15u) | static_cast<uint32_t>(i));
-                    if constexpr (SPLIT) {
-                        float ds = 0.f;
+                    float ds = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) ds = (which & 15u) == static_cast<uint32_t>(i) ? x[i] * y[i] : ds;
-                        rest = which > best ? ds - static_cast<float>(static_cast<__bf16>(ds)) : rest;
-                    }
-                    best_at = which > best ? j * KEYS + 32 * t : best_at;
-                    best = max(best, which);
+                    for (int i = 0; i < 16; ++i) ds = (which & 15u) == static_cast<uint32_t>(i) ? y[i] : ds;
+                    const bool more = most > bar;
+                    rest = more ? ds - static_cast<float>(static_cast<__bf16>(ds)) : rest;
+                    best_at = more ? j * KEYS + 32 * t : best_at;
+                    best = more ? which : best;
+                    bar = more ? 1.5f * most : bar;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] *= y[i];
-                if constexpr (EXACT_D<T>) e[i & 1] += x[i];
-            }
-#pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const frag f = acc_frag<T>(x, s);
+                const frag f = acc_frag<T>(y, s);
 #pragma unroll
                 for (int n = 0; n < NO; ++n) acc[n] = Op<T>::mma(Ti::template col<32>(kt, 32 * t + 16 * s, 32 * n, ln), f, acc[n]);
             }
@@ -198,7 +200,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
         d += off;
         // The keys come as two tiles of 32, one for each query and half, and the factors are a diagonal matrix: dq^T += k^T (rest - e p). A lane without
         // a largest p takes its own token's key, times 0, and one whose query is no token, and may hold anything, some token's.
-        const int place = (best & 15u) / 4 * 8 + 4 * half + (best & 3u), mine = min(best >= 16u ? best_at + place : q_row, max(b.n - 1, 0));
+        const int place = (best & 15u) / 4 * 8 + 4 * half + (best & 3u), mine = min(best_at >= 0 ? best_at + place : q_row, max(b.n - 1, 0));
         const auto ps = __builtin_amdgcn_permlane32_swap(best & ~15u, best & ~15u, false, false);
         const auto rests = __builtin_amdgcn_permlane32_swap(__float_as_uint(rest), __float_as_uint(rest), false, false);
         unsigned char *room = smem + wv * 64 * Ti::ROWB;
