@@ -560,8 +560,8 @@ muir_status_t muir_matvec_q4(
     int group, muir_dtype_t x_type, muir_dtype_t scale_type, muir_stream_t stream);
 
 /*
- * Causal softmax attention over whole prompts, as the layers of a hybrid stack between the recurrent ones have it (Muir pages: a local
- * softmax window in front of the recurrent state). A token sees itself and the tokens before it in its sequence, all of
+ * Causal softmax attention over whole prompts, for the layers of a hybrid stack that lie between the recurrent ones (openai-hub page, its last
+ * section but one: a local softmax window, then the recurrent state). A token sees itself and the tokens before it in its sequence, all of
  * them or the last `window`:
  *     s_ij = scale q_i . k_j      lse_i = log sum_j exp s_ij      o_i = sum_j exp(s_ij - lse_i) v_j
  *

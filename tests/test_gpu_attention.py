@@ -224,6 +224,16 @@ def test_gradients_against_differences(device):
     assert abs(got - want) <= slack + 1e-6 * abs(want) + e * e * 1e3 * D.abs().sum()
 
 
+def test_without_lse(device):
+    """The C entry takes NULL for lse."""
+    q, k, v, _ = make(device, BF, (2, 90), 4, 2, 64, 3)
+    o = torch.full_like(q, float("nan"))
+    st = muir.lib().muir_attention_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, o.data_ptr(), None, 180, 2, 4, 2, 64, 0, 0.125, muir.MUIR_BF16,
+                                       torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(o, muir.attention_fwd(q, k, v)[0])
+
+
 def test_the_same_bits_again(device):
     q, k, v, do = make(device, BF, (2, 700), 8, 2, 128, 8)
     a = muir.attention_fwd(q, k, v)
