@@ -25,8 +25,9 @@ using namespace at;
 
 // SPLIT: a workgroup has 32 rows, and its wavefronts every WAVES-th tile of what they walk over, each in two tiles of its own, which are loaded anew as
 // soon as their last product has read them; their sums meet at the end.
-template <typename T, int D, bool SPLIT> struct Bwd {
-    static constexpr int WAVES = 4, ROWS = SPLIT ? 32 : 128;
+// dkv has eight of them where its workgroups are few and each has far to go.
+template <typename T, int D, bool SPLIT, int W = 4> struct Bwd {
+    static constexpr int WAVES = W, ROWS = SPLIT ? 32 : 128;
     static constexpr int STEP = SPLIT ? 32 : 64, TILE = STEP * D * int(sizeof(T));  // rows of the tiles walked over
     static constexpr int LDS = (SPLIT ? 2 * WAVES : 4) * TILE, STATS = (SPLIT ? 2 * WAVES : 4) * 64 * 4;  // lse and D, of as many tiles
     static constexpr int DQ_PER_CU = sizeof(T) * D == 512 ? 1 : 2, DKV_PER_CU = sizeof(T) * D == 512 ? 1 : 2;
@@ -240,12 +241,12 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
 
 // dk and dv of 128 keys of a key head, 32 to a wavefront, whose keys and values stay in registers, over the queries of all its heads. Scores have
 // queries as rows, so p and ds are the operands of dv^T += do^T p and dk^T += q^T ds as they are.
-template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::DKV_PER_CU)) void attention_dkv_kernel(
+template <typename T, int D, bool SPLIT, int W>
+__global__ __launch_bounds__((64 * W), (Bwd<T, D, SPLIT, W>::DKV_PER_CU)) void attention_dkv_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ tops,
     const float *__restrict__ deltas, Sequences seqs, T *__restrict__ dk, T *__restrict__ dv, int blocks, int H, int Hk, int window,
     float scale) {
-    using C = Bwd<T, D, SPLIT>;
+    using C = Bwd<T, D, SPLIT, W>;
     using Ti = Tile<T, D>;
     using frag = typename Op<T>::frag;
     constexpr int WAVES = C::WAVES, QR = C::STEP, TILE = C::TILE, QS = D / 16, NO = D / 32;
@@ -419,12 +420,12 @@ template <typename T, int D, bool SPLIT> hipError_t launch_dq(const AttentionCal
     return hipGetLastError();
 }
 
-template <typename T, int D, bool SPLIT> hipError_t launch_dkv(const AttentionCall &c, const AttentionGrads &g, float *tops, float *deltas, hipStream_t stream) {
-    using B = Bwd<T, D, SPLIT>;
-    const hipError_t err = allow_lds<&attention_dkv_kernel<T, D, SPLIT>>(B::LDS + B::STATS);
+template <typename T, int D, bool SPLIT, int W = 4> hipError_t launch_dkv(const AttentionCall &c, const AttentionGrads &g, float *tops, float *deltas, hipStream_t stream) {
+    using B = Bwd<T, D, SPLIT, W>;
+    const hipError_t err = allow_lds<&attention_dkv_kernel<T, D, SPLIT, W>>(B::LDS + B::STATS);
     if (err != hipSuccess) return err;
     const int blocks = c.N / B::ROWS + c.S + 1;
-    hipLaunchKernelGGL((attention_dkv_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), B::LDS + B::STATS,
+    hipLaunchKernelGGL((attention_dkv_kernel<T, D, SPLIT, W>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), B::LDS + B::STATS,
                        stream, static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v),
                        static_cast<const T *>(g.dout), tops, deltas, Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(g.dk),
                        static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
@@ -436,13 +437,15 @@ template <typename T, int D> hipError_t launch(const AttentionCall &c, const Att
     hipError_t err;
     if constexpr (sizeof(T) == 2) {
         err = attention_split(c.N, c.S, c.H, D, c.window) ? launch_dq<T, D, true>(c, g, tops, deltas, stream) : launch_dq<T, D, false>(c, g, tops, deltas, stream);
-        if (err == hipSuccess)
-            err = attention_split(c.N, c.S, c.Hk, D, c.window) ? launch_dkv<T, D, true>(c, g, tops, deltas, stream) : launch_dkv<T, D, false>(c, g, tops, deltas, stream);
+        if (err != hipSuccess) return err;
+        if (!attention_split(c.N, c.S, c.Hk, D, c.window)) return launch_dkv<T, D, false>(c, g, tops, deltas, stream);
     } else {
         err = launch_dq<T, D, true>(c, g, tops, deltas, stream);
-        if (err == hipSuccess) err = launch_dkv<T, D, true>(c, g, tops, deltas, stream);
+        if (err != hipSuccess) return err;
     }
-    return err;
+    if constexpr (sizeof(T) * D < 512)  // eight wavefronts' tiles would not fit LDS
+        if (attention_far(c.N, c.S, c.H, c.Hk, c.window)) return launch_dkv<T, D, true, 8>(c, g, tops, deltas, stream);
+    return launch_dkv<T, D, true>(c, g, tops, deltas, stream);
 }
 
 }  // namespace

@@ -18,6 +18,7 @@ struct AttentionCall {
 // Workgroups of a prompt kernel have 128 rows of one head, or 32 (split) where 128 would make too few of them, and in float32's backward.
 inline long long attention_blocks(int N, int S, int rows) { return static_cast<long long>(N) / rows + S + 1; }
 bool attention_split(int N, int S, int heads, int d, int window);
+bool attention_far(int N, int S, int H, int Hk, int window);
 hipError_t launch_attention_fwd(const AttentionCall &c, void *o, float *lse, hipStream_t stream);
 
 size_t attention_bwd_workspace_bytes(int N, int H);

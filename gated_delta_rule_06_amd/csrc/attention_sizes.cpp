@@ -23,6 +23,15 @@ bool attention_split(int N, int S, int heads, int d, int window) {
     return attention_blocks(N, S, 128) * heads <= (d == 64 ? most * 5 / 4 : most);
 }
 
+// Whether dk and dv of a block of 32 keys take eight wavefronts instead of four: where four would all run at once (two workgroups to a compute unit), the
+// one with the most tiles is what is waited for, and it has the queries of every head that shares the key. The backward in us with four and with eight:
+// bf16 d128 B1 T2048 H16 Hk4 (256 workgroups, 256 tiles) 141 and 114, B1 T512 H16 Hk4 (64, 64) 41.5 and 35.4, B1 T4096 H16 Hk4 (512, 512) 347 and 302,
+// B1 T2048 H16 Hk16 (1024, 64) 98.7 and 112.6, B1 T128 H16 Hk16 (64, 4) 17.9 and 18.5; float32 d64 B3 T777 H12 Hk6 (432, 48) 108.8 and 101.7.
+bool attention_far(int N, int S, int H, int Hk, int window) {
+    const long long length = N / S, seen = window && window < length ? window : length;
+    return static_cast<long long>(N / 32) * Hk <= 512 && H / Hk * seen >= 12 * 32;
+}
+
 size_t attention_bwd_workspace_bytes(int N, int H) { return 2 * up256(static_cast<size_t>(N) * H * 4); }
 
 // One workgroup to a compute unit, by its LDS: B1 T32768 H16 Hk4 d128 bf16 (page 64) 17.1 us with room for 256 workgroups, 20.7 with 512 (the parts then cost
