@@ -45,7 +45,7 @@ __global__ __launch_bounds__((64 * Fwd<T, D, SPLIT>::WAVES), (Fwd<T, D, SPLIT>::
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
     typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, H, Hk);
-    const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);  // late blocks of a sequence first: they see the most keys
+    const Block b = find_block<C::ROWS>(seqs, it.block, blocks);
     if (b.at >= b.rows) return;
     const int hk = it.h / (H / Hk);
     const uint32_t kv_stride = uint32_t(Hk) * Ti::ROWB;
@@ -204,7 +204,7 @@ template <typename T, int D, bool SPLIT> hipError_t launch(const AttentionCall &
     const int blocks = c.N / F::ROWS + c.S + 1;
     hipLaunchKernelGGL((attention_fwd_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * F::WAVES), F::LDS, stream,
                        static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v),
-                       Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(o), lse, blocks, c.H, c.Hk, c.window, c.scale * LOG2E);
+                       Sequences{c.offsets, c.lens, c.N, c.S, attention_by_place(c.offsets, c.N, c.S, c.window)}, static_cast<T *>(o), lse, blocks, c.H, c.Hk, c.window, c.scale * LOG2E);
     return hipGetLastError();
 }
 

@@ -289,19 +289,51 @@ __device__ __forceinline__ void store_sums(unsigned char *room, const f32x16_t (
     lds_barrier();
 }
 
-// Block `w` of `R` rows. All 64 lanes search together.
-template <int R> __device__ __forceinline__ Block find_block(const Sequences &q, int w) {
+// Sum and largest over a wavefront of values not below 0, for everybody.
+template <typename F> __device__ __forceinline__ int wave_all(int x, F f) {
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));  // from 1, 2, 4 and 8 lanes before, in rows of 16
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));  // a row's last lane to the next row
+    x = f(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));  // lane 31 to the upper half
+    return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ int wave_add(int x) {
+    return wave_all(x, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ int wave_max(int x) {
+    return wave_all(x, [](int a, int b) { return max(a, b); });
+}
+
+// Block `i` of a launch of `blocks` (FROM_END: of keys). All 64 lanes search together.
+template <int R, bool FROM_END = false> __device__ __forceinline__ Block find_block(const Sequences &q, int i, int blocks) {
+    if (!q.offsets) return equal_block(q, R, i, FROM_END);
     const int lane = threadIdx.x & 63;
-    const int s = search_sequence(q.S, [&](int lo, int step, int hi) {
-        const int i = lo + lane * step;
-        return __builtin_amdgcn_readfirstlane(static_cast<int>(__popcll(__ballot(i <= hi && q.first(i) / R + i <= w))));
-    });
-    Block b = block_in(q, R, w, s);
-    b.seq = __builtin_amdgcn_readfirstlane(b.seq);
-    b.lo = __builtin_amdgcn_readfirstlane(b.lo);
-    b.rows = __builtin_amdgcn_readfirstlane(b.rows);
-    b.n = __builtin_amdgcn_readfirstlane(b.n);
-    b.at = __builtin_amdgcn_readfirstlane(b.at);
+    Block b;
+    if (q.by_place && q.S < 64) {
+        const int lo = q.first(lane), rows = lane <= q.S ? q.rows(lane) : 0, n = lane < q.S ? q.tokens(lane) : 0, own = (rows + R - 1) / R;
+        auto count = [&](int p) { return wave_add(max(own - p, 0)); };
+        if (i >= count(0)) return no_block(q);
+        const int p = search_place(wave_max(own), i, count), rank = i - count(p + 1);
+        const uint64_t has = __ballot(own > p);
+        const bool mine = own > p && __popcll(has & ((uint64_t(1) << lane) - 1)) == rank;
+        const int s = __builtin_ctzll(__ballot(mine));
+        const int all = __builtin_amdgcn_readlane(own, s);
+        b = Block{s, __builtin_amdgcn_readlane(lo, s), __builtin_amdgcn_readlane(rows, s), __builtin_amdgcn_readlane(n, s), (FROM_END ? all - 1 - p : p) * R};
+    } else {
+        const int w = FROM_END ? i : blocks - 1 - i;  // their most work is at the end, or at the start
+        const int s = search_sequence(q.S, [&](int lo, int step, int hi) {
+            const int k = lo + lane * step;
+            return __builtin_amdgcn_readfirstlane(static_cast<int>(__popcll(__ballot(k <= hi && q.first(k) / R + k <= w))));
+        });
+        b = block_in(q, R, w, s);
+        b.seq = __builtin_amdgcn_readfirstlane(b.seq);
+        b.lo = __builtin_amdgcn_readfirstlane(b.lo);
+        b.rows = __builtin_amdgcn_readfirstlane(b.rows);
+        b.n = __builtin_amdgcn_readfirstlane(b.n);
+        b.at = __builtin_amdgcn_readfirstlane(b.at);
+    }
     return b;
 }
 

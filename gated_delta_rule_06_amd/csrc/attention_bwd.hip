@@ -55,7 +55,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
     typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, H, Hk);
-    const Block b = find_block<C::ROWS>(seqs, blocks - 1 - it.block);
+    const Block b = find_block<C::ROWS>(seqs, it.block, blocks);
     if (b.at >= b.rows) return;
     const int hk = it.h / (H / Hk);
     const uint32_t kv_stride = uint32_t(Hk) * Ti::ROWB;
@@ -254,7 +254,7 @@ __global__ __launch_bounds__((64 * W), (Bwd<T, D, SPLIT, W>::DKV_PER_CU)) void a
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
     typename Ti::template Lane<32> ln(lane);
     const Item it = find_item(blockIdx.x, blocks, Hk, Hk);
-    const Block b = find_block<C::ROWS>(seqs, it.block);
+    const Block b = find_block<C::ROWS, true>(seqs, it.block, blocks);
     if (b.at >= b.rows) return;
     const int G = H / Hk, h0 = it.h * G;
     const uint32_t q_stride = uint32_t(H) * Ti::ROWB;
@@ -415,7 +415,7 @@ template <typename T, int D, bool SPLIT> hipError_t launch_dq(const AttentionCal
     const int blocks = c.N / B::ROWS + c.S + 1;
     hipLaunchKernelGGL((attention_dq_kernel<T, D, SPLIT>), dim3(static_cast<unsigned>(blocks) * c.H), dim3(64 * B::WAVES), B::LDS, stream,
                        static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v), static_cast<const T *>(g.o),
-                       static_cast<const T *>(g.dout), g.lse, Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(g.dq), tops, deltas,
+                       static_cast<const T *>(g.dout), g.lse, Sequences{c.offsets, c.lens, c.N, c.S, attention_by_place(c.offsets, c.N, c.S, c.window)}, static_cast<T *>(g.dq), tops, deltas,
                        blocks, c.H, c.Hk, c.window, c.scale);
     return hipGetLastError();
 }
@@ -427,7 +427,7 @@ template <typename T, int D, bool SPLIT, int W = 4> hipError_t launch_dkv(const 
     const int blocks = c.N / B::ROWS + c.S + 1;
     hipLaunchKernelGGL((attention_dkv_kernel<T, D, SPLIT, W>), dim3(static_cast<unsigned>(blocks) * c.Hk), dim3(64 * B::WAVES), B::LDS + B::STATS,
                        stream, static_cast<const T *>(c.q), static_cast<const T *>(c.k), static_cast<const T *>(c.v),
-                       static_cast<const T *>(g.dout), tops, deltas, Sequences{c.offsets, c.lens, c.N, c.S}, static_cast<T *>(g.dk),
+                       static_cast<const T *>(g.dout), tops, deltas, Sequences{c.offsets, c.lens, c.N, c.S, attention_by_place(c.offsets, c.N, c.S, c.window)}, static_cast<T *>(g.dk),
                        static_cast<T *>(g.dv), blocks, c.H, c.Hk, c.window, c.scale);
     return hipGetLastError();
 }

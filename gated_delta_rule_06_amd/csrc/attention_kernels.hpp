@@ -19,6 +19,9 @@ struct AttentionCall {
 inline long long attention_blocks(int N, int S, int rows) { return static_cast<long long>(N) / rows + S + 1; }
 bool attention_split(int N, int S, int heads, int d, int window);
 bool attention_far(int N, int S, int H, int Hk, int window);
+// Whether a window is so short that most queries see as many keys as it has.
+bool attention_even(int N, int S, int window);
+bool attention_by_place(const int *offsets, int N, int S, int window);
 hipError_t launch_attention_fwd(const AttentionCall &c, void *o, float *lse, hipStream_t stream);
 
 size_t attention_bwd_workspace_bytes(int N, int H);

@@ -22,6 +22,7 @@ MUIR_HD int cut(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 struct Sequences {
     const int *offsets, *lens;
     int N, S;
+    bool by_place;  // the order in which blocks are taken, below
     MUIR_HD int first(int s) const {
         if (s <= 0) return 0;
         if (s > S) return N;
@@ -34,10 +35,41 @@ struct Sequences {
     MUIR_HD int tokens(int s) const { return s >= S ? 0 : lens ? cut(lens[s], 0, rows(s)) : rows(s); }
 };
 
-// Sequence of block `w` of `R` rows. Sequence s has the blocks from first(s) / R + s on: never fewer than it needs and at most one more, so no
-// sums over the lengths are needed. A launch has N / R + S + 1 blocks.
-// 64 sequences are looked at in a step: count(lo, step, hi) says how many of s = lo, lo + step, .. (64 of them, up to hi) have
-// first(s) / R + s <= w.
+// What a block of `R` rows has of a sequence: the sequence's first row, rows and tokens, and the block's first row in it. A block without rows, past its
+// sequence's or found by offsets that do not ascend, has at >= rows; at is never below 0.
+struct Block {
+    int seq, lo, rows, n, at;
+};
+MUIR_HD Block no_block(const Sequences &q) { return Block{q.S, q.N, 0, 0, 0}; }
+
+// A launch has N / R + S + 1 blocks, never fewer than the sequences need. By place, those with the most work go first: the place of a block in its
+// sequence says how many keys its queries see, and, counted from the end, how many queries its keys have (FROM_END), so blocks are taken place by place,
+// the highest first, each place over all the sequences that have it. Otherwise one sequence is taken after another, which suits a window: blocks are
+// worth about the same, and neighbours share their keys.
+//
+// Sequences of equal length need no search.
+MUIR_HD Block equal_block(const Sequences &q, int R, int i, bool from_end) {
+    const int rows = q.N / q.S, per = (rows + R - 1) / R;
+    if (i >= per * q.S) return no_block(q);
+    const int s = q.by_place ? i % q.S : i / per, up = q.by_place ? i / q.S : i % per;
+    return Block{s, s * rows, rows, q.tokens(s), (q.by_place && !from_end ? per - 1 - up : up) * R};
+}
+// The place of block `i`, where count(p) is how many blocks have place p or a higher one (i < count(0)), and none has `top`.
+template <typename Count> MUIR_HD int search_place(int top, int i, Count count) {
+    int lo = 0, hi = top;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (count(mid) > i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// One sequence after another, in rising order of their blocks: also where 64 of them and more would have to be counted by place. Sequence s has the blocks from first(s) / R + s on: at most one more
+// than it needs, so no sums over the lengths are needed. 64 sequences are looked at in a step: count(lo, step, hi) says how many of s = lo, lo + step, ..
+// (64 of them, up to hi) have first(s) / R + s <= w.
 template <typename Count> MUIR_HD int search_sequence(int S, Count count) {
     int lo = 0, hi = S;
     while (hi > lo) {
@@ -47,12 +79,7 @@ template <typename Count> MUIR_HD int search_sequence(int S, Count count) {
     }
     return lo;
 }
-
-// What block `w` of `R` rows has of sequence `s`, which it was found to be in: the sequence's first row, rows and tokens, and the block's first row in
-// it. A block without rows, past its sequence's or found by offsets that do not ascend, has at >= rows; at is never below 0.
-struct Block {
-    int seq, lo, rows, n, at;
-};
+// Block `w` of those, found to be in sequence `s`.
 MUIR_HD Block block_in(const Sequences &q, int R, int w, int s) {
     const int lo = q.first(s), rows = q.rows(s), at = (w - lo / R - s) * R;
     return Block{s, lo, rows, q.tokens(s), at < 0 ? rows : at};
@@ -60,7 +87,7 @@ MUIR_HD Block block_in(const Sequences &q, int R, int w, int s) {
 
 // Work item of a workgroup: consecutive workgroups go round the eight XCDs, so that the heads of one key head, all their blocks, run on
 // one of them, whose L2 then holds that head's keys and values; what is left over eight key heads goes round by blocks. Blocks
-// come in rising order.
+// come in their order.
 struct Item {
     int block, h;
 };

@@ -18,10 +18,17 @@ namespace muir {
 // float32: the same in the forward (d64 B4 T1024 H16, W 592, 77 and 80, B8 T4096 H16 1728 and 1600; d128 163 and 146, 3856 and 3199). The backward has
 // blocks of 32 only: d64 233 and 260, 5570 and 5728; d128 546 and 643, and only the largest gains by 128 (13036 and 12467).
 bool attention_split(int N, int S, int heads, int d, int window) {
-    const int length = N / S;
-    const int most = window && window <= length / 2 ? 160 : length < 2048 ? 350 : 600;
+    const int most = attention_even(N, S, window) ? 160 : N / S < 2048 ? 350 : 600;
     return attention_blocks(N, S, 128) * heads <= (d == 64 ? most * 5 / 4 : most);
 }
+
+bool attention_even(int N, int S, int window) { return window && window <= N / S / 2; }
+
+// Whether the blocks with the most to do go first. Without a window, in us, sequence after sequence and by place: bf16 B8 T4096 H16 d128 forward 580 and
+// 550, dq 870 and 851, dkv 1020 and 966; 24 packed sequences up to 4001, H16 Hk4, 425 and 397: the last sequence's largest blocks began when the card was
+// running empty. With a short window packed sequences are taken one after another, which keeps neighbours' keys in the caches: 9 up to 4096, H16
+// Hk4, window 512, dq 127 and 136, dkv 131 and 138; of a batch they are as near either way (B8 T4096 H12 d64 window 1024 129 and 126).
+bool attention_by_place(const int *offsets, int N, int S, int window) { return !offsets || !attention_even(N, S, window); }
 
 // Whether dk and dv of a block of 32 keys take eight wavefronts instead of four: where four would all run at once (two workgroups to a compute unit), the
 // one with the most tiles is what is waited for, and it has the queries of every head that shares the key. The backward in us with four and with eight:

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const unsigned char *
                                                            unsigned char *__restrict__ k_cache, unsigned char *__restrict__ v_cache, Pages pg,
                                                            Sequences seqs, const int *__restrict__ start) {
     constexpr int CH = ROWB / 16, TURNS = 4;
-    const Block b = find_block<APPEND_ROWS>(seqs, blockIdx.x);
+    const Block b = find_block<APPEND_ROWS>(seqs, blockIdx.x, gridDim.x);
     if (b.at >= b.n) return;
     const int base = start ? start[b.seq] : 0, pieces = min(b.n - b.at, APPEND_ROWS) * pg.Hk * CH;
     if (base < 0) return;
@@ -298,7 +298,7 @@ hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *
 hipError_t launch_cache_append(const CacheCall &c, const void *k, const void *v, const int *offsets, const int *lens, const int *start,
                                int N, int S, hipStream_t stream) {
     const int row = c.d * (c.bf16 ? 2 : 4), blocks = N / APPEND_ROWS + S + 1;
-    const Sequences s{offsets, lens, N, S};
+    const Sequences s{offsets, lens, N, S, false};
 #define MUIR_APPEND(R)                                                                                                           \
     if (row == R) {                                                                                                              \
         hipLaunchKernelGGL((cache_append_kernel<R>), dim3(blocks), dim3(256), 0, stream, static_cast<const unsigned char *>(k), \

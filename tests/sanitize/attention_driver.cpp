@@ -48,31 +48,68 @@ static void expect(int got, int want, int launches, const char *what) {
 
 template <typename T> static T *at(int i) { return reinterpret_cast<T *>((uintptr_t(1) << 40) + i * (uintptr_t(1) << 38)); }
 
-// The blocks of a call as the kernels find them: rows taken, each how often.
-static void check_blocks(const muir::at::Sequences &q, int R, bool ordered) {
-    std::vector<int> taken(q.N, 0), token(q.N, 0);
-    const int blocks = q.N / R + q.S + 1;
-    for (int w = 0; w < blocks; ++w) {
-        const int s = muir::at::search_sequence(q.S, [&](int lo, int step, int hi) {
-            int n = 0;
-            for (int lane = 0; lane < 64; ++lane) {
-                const int64_t i = int64_t(lo) + int64_t(lane) * step;
-                n += i <= hi && q.first(int(i)) / R + i <= w;
-            }
-            return n;
-        });
-        CHECK(s >= 0 && s <= q.S);
-        const muir::at::Block x = muir::at::block_in(q, R, w, s);
-        CHECK(x.seq == s && x.lo >= 0 && x.rows >= 0 && x.lo + x.rows <= q.N && x.n >= 0 && x.n <= x.rows && x.at >= 0);
-        for (int r = x.at; r < x.at + R && r < x.rows; ++r) {
-            ++taken[x.lo + r];
-            token[x.lo + r] += r < x.n;
+// Block `i` of a launch as the kernels find it, the lanes one after another.
+static muir::at::Block find_block(const muir::at::Sequences &q, int R, int i, int blocks, bool from_end) {
+    if (!q.offsets) return muir::at::equal_block(q, R, i, from_end);
+    if (q.by_place && q.S < 64) {
+        std::vector<int> own(64, 0);
+        int top = 0;
+        for (int s = 0; s <= q.S; ++s) {
+            own[s] = (q.rows(s) + R - 1) / R;
+            top = own[s] > top ? own[s] : top;
         }
+        auto count = [&](int p) {
+            int n = 0;
+            for (int x : own) n += x > p ? x - p : 0;
+            return n;
+        };
+        if (i >= count(0)) return muir::at::no_block(q);
+        const int p = muir::at::search_place(top, i, count);
+        int rank = i - count(p + 1);
+        CHECK(rank >= 0);
+        for (int s = 0; s <= q.S; ++s)
+            if (own[s] > p && rank-- == 0) return {s, q.first(s), q.rows(s), q.tokens(s), (from_end ? own[s] - 1 - p : p) * R};
+        CHECK(false);
+        return muir::at::no_block(q);
     }
-    if (!ordered) return;
-    for (int s = 0; s <= q.S; ++s)
-        for (int r = 0; r < q.rows(s); ++r) CHECK(token[q.first(s) + r] == (r < q.tokens(s)));
-    for (int x : taken) CHECK(x == 1);
+    const int w = from_end ? i : blocks - 1 - i;
+    const int s = muir::at::search_sequence(q.S, [&](int lo, int step, int hi) {
+        int n = 0;
+        for (int lane = 0; lane < 64; ++lane) {
+            const int64_t k = int64_t(lo) + int64_t(lane) * step;
+            n += k <= hi && q.first(int(k)) / R + k <= w;
+        }
+        return n;
+    });
+    CHECK(s >= 0 && s <= q.S);
+    return muir::at::block_in(q, R, w, s);
+}
+
+// The blocks of a call: rows taken, each how often, and, where they are taken place by place, the most work first.
+static void check_blocks(muir::at::Sequences q, int R, bool ordered) {
+    const int blocks = q.N / R + q.S + 1;
+    for (int turn = 0; turn < 4; ++turn) {
+        const bool from_end = turn % 2;
+        q.by_place = turn / 2;
+        std::vector<int> taken(q.N, 0), token(q.N, 0);
+        int before = INT_MAX;
+        for (int i = 0; i < blocks; ++i) {
+            const muir::at::Block x = find_block(q, R, i, blocks, from_end);
+            CHECK(x.seq >= 0 && x.seq <= q.S && x.lo >= 0 && x.rows >= 0 && x.lo + x.rows <= q.N && x.n >= 0 && x.n <= x.rows && x.at >= 0);
+            for (int r = x.at; r < x.at + R && r < x.rows; ++r) {
+                ++taken[x.lo + r];
+                token[x.lo + r] += r < x.n;
+            }
+            if (x.at >= x.rows || !q.by_place || (q.offsets && q.S >= 64)) continue;
+            const int work = from_end ? (x.rows + R - 1) / R - x.at / R : x.at / R;
+            CHECK(work <= before);
+            before = work;
+        }
+        if (!ordered) continue;
+        for (int s = 0; s <= q.S; ++s)
+            for (int r = 0; r < q.rows(s); ++r) CHECK(token[q.first(s) + r] == (r < q.tokens(s)));
+        for (int x : taken) CHECK(x == 1);
+    }
 }
 
 static void check_layout() {
@@ -86,11 +123,11 @@ static void check_layout() {
             lens[s] = pick(-3, most + 3);
         }
         const int N = offsets[S] + pick(0, 300), R = round % 3 == 0 ? 128 : round % 3 == 1 ? 32 : 8;
-        check_blocks({offsets.data(), nullptr, N, S}, R, true);
-        check_blocks({offsets.data(), lens.data(), N, S}, R, true);
-        check_blocks({nullptr, lens.data(), S * most, S}, R, true);
+        check_blocks({offsets.data(), nullptr, N, S, false}, R, true);
+        check_blocks({offsets.data(), lens.data(), N, S, false}, R, true);
+        check_blocks({nullptr, lens.data(), S * most, S, false}, R, true);
         for (int &x : offsets) x = pick(0, 3) ? pick(-N - 5, 2 * N + 5) : pick(0, 1) ? INT_MAX : INT_MIN;
-        check_blocks({offsets.data(), lens.data(), N, S}, R, false);
+        check_blocks({offsets.data(), lens.data(), N, S, false}, R, false);
     }
     for (int Hk : {1, 2, 7, 8, 9, 16, 17})
         for (int G : {1, 3, 4})
