@@ -10,8 +10,8 @@
 // they are as exact in float32 and bf16 as below 1.
 //
 // What bounds it. d128: the matrix cores and the card's power. B1 T32768 H16 4.0 to 4.1 ms, 1080 TFLOP/s, where a large library product makes 1361: matrix
-// cores busy in 64 % of the cycles, vector instructions in 69 %, at a clock of 1.4 GHz; B8 T4096 H16 583 us, 943 TFLOP/s. d64: vector instructions, of
-// which there are as many to half the products: B8 T4096 H12 window 1024 128 us, vector 72 %, matrix 38 %. Few rows: the walk of the last rows' workgroup.
+// cores busy in 64 % of the cycles, vector instructions in 69 %, at a clock of 1.4 GHz; B8 T4096 H16 550 us, 1000 TFLOP/s, 58 and 66 % at 1.6 GHz. d64: vector instructions, of
+// which there are as many to half the products: B8 T4096 H12 window 1024 126 us, vector 73 %, matrix 39 %. Few rows: the walk of the last rows' workgroup.
 // Sizes tried, in us: d64 tiles of 64 keys against 32, B8 T4096 H16 331 and 351; d128 the other way, 4350 and 4160 at B1 T32768 H16, since 64 keys leave
 // two workgroups to a compute unit instead of three. Two blocks of 32 queries to a wavefront, which halves the reads of LDS: 4.2 against 4.3 ms there,
 // 515 against 430 for 24 packed sequences, so not kept.

@@ -4,9 +4,9 @@
 // Two kernels, each with its sums in registers from the first to the last product, so no sum depends on an order and nothing is
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed): one kernel would have to add dq atomically, and its bits would depend on the
-// order. bf16 B8 T4096 H16 d128: dq 0.89 ms, dkv 1.03 ms, 930 and 1070 TFLOP/s of the products made; matrix cores busy in 50 and
-// 57 % of the cycles at 1.6 to 1.8 GHz, two workgroups to a compute unit by registers (240 and 256) and LDS. Packed with a window of 512 (13731 rows,
-// H16 Hk4) 128 and 132 us, matrix cores busy in 33 and 35 %: 7 and 1.8 workgroups to a compute unit do not come out even.
+// order. bf16 B8 T4096 H16 d128: dq 0.85 ms, dkv 0.97 ms, 980 and 1130 TFLOP/s of the products made; matrix cores busy in 55 and
+// 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (244 and 256) and LDS. Packed with a window of 512 (13731 rows,
+// H16 Hk4) 129 and 133 us, matrix cores busy in 31 and 35 %: 6.8 and 1.7 workgroups to a compute unit do not come out even.
 // bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
 // (2-norm, relative) where one rounding is 0.0017. But sum_j ds_ij = 0, so dq's kernel finds e_i as the sum of its own ds, hands the
