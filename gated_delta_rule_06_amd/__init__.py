@@ -46,16 +46,18 @@ class MuirError(RuntimeError):
 
 
 _lib = None
+torch = None  # imported with the library: naming this package does not need it
 
 
 def lib():
     """The loaded ``libmuir.so`` (raises if it has not been built)."""
-    global _lib
+    global _lib, torch
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(
                 f"{LIB_PATH} is missing: build it with "
                 "`python -m gated_delta_rule_06_amd._build` (hipcc, gfx950)")
+        import torch
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
         L.muir_chunk_fwd_workspace_size.argtypes = [i] * 6 + [i]
@@ -583,8 +585,7 @@ def _is(t, name, dtype, shape, index):
 
 def _call(fn, index, *args):
     """One library call on device ``index``'s current stream, with that device current."""
-    import torch
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -608,14 +609,21 @@ def _out(t, name, dtype, shape, like):
 
 def _workspace(t, need, like):
     """(pointer's tensor, bytes): ``t`` checked, a new one, or none where none is needed."""
+    if t is None and not need:
+        return None, 0
     import torch
     if t is None:
-        return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
     _is(t, "workspace", torch.uint8, t.shape, like.get_device())
     return t, t.numel()
 
 
 def _rank(t, name, n):
+    try:
+        if t.dim() == n:
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -878,7 +886,6 @@ def matvec_q4(x, w, scale, zero=None, *, group: int = 128, y=None):
 
 def _sequences(x, name, offsets, lens):
     """(rows N, sequences S, device index) of [B, T, heads, d] or packed [N, heads, d] rows."""
-    import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape, i = x.shape, x.get_device()
@@ -906,15 +913,19 @@ def _attention_inputs(q, k, v, offsets, lens, window, scale):
     _rank(k, "k", len(shape))
     Hk = k.shape[-2]
     kshape = (*shape[:-2], Hk, d)
-    _is(q, "q", dt, shape, i)
+    if i < 0 or not q.is_contiguous():
+        _is(q, "q", dt, shape, i)
     _is(k, "k", dt, kshape, i)
     _is(v, "v", dt, kshape, i)
-    return (N, S, H, Hk, d), int(window), d ** -0.5 if scale is None else float(scale), _dtype_code(q), i
+    return (N, S, H, Hk, d), int(window), d ** -0.5 if scale is None else float(scale), _code(dt, q), i
+
+
+def _code(dt, t):
+    return MUIR_BF16 if dt is torch.bfloat16 else MUIR_F32 if dt is torch.float32 else _dtype_code(t)
 
 
 def _like(t, name, like, i):
     """``t`` checked as an output shaped and typed as ``like``, or a new tensor."""
-    import torch
     if t is None:
         return torch.empty_like(like)
     _is(t, name, like.dtype, like.shape, i)
@@ -934,14 +945,14 @@ def attention_fwd(q, k, v, offsets=None, *, lens=None, window: int = 0, scale=No
     can reach the o of tokens up to 127 before it, and with a window up to 127 behind those that see
     it; in float32 an infinity comes as NaN.
     """
-    import torch
+    L = _lib or lib()
     sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)
     o = _like(o, "o", q, i)
     if lse is None:
-        lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
     else:
         _is(lse, "lse", torch.float32, q.shape[:-1], i)
-    _call(lib().muir_attention_fwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(offsets),
+    _call(L.muir_attention_fwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(offsets),
           _at(lens), o.data_ptr(), lse.data_ptr(), *sizes, window, scale, code)
     return o, lse
 
@@ -962,7 +973,7 @@ def attention_bwd(q, k, v, o, lse, offsets=None, *, do, lens=None, window: int =
     ``ATTENTION_GRADS``, shaped and typed as the inputs (shared heads summed); rows that are no
     token have gradients 0. ``out`` may hold pre-allocated tensors under those keys.
     """
-    import torch
+    L = _lib or lib()
     sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)
     _is(o, "o", q.dtype, q.shape, i)
     _is(do, "do", q.dtype, q.shape, i)
@@ -970,14 +981,13 @@ def attention_bwd(q, k, v, o, lse, offsets=None, *, do, lens=None, window: int =
     out = out or {}
     dq, dk, dv = (_like(out.get(n), "d" + n, x, i) for n, x in (("q", q), ("k", k), ("v", v)))
     workspace, size = _workspace(workspace, attention_bwd_workspace_size(*sizes, code), q)
-    _call(lib().muir_attention_bwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+    _call(L.muir_attention_bwd, i, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
           lse.data_ptr(), _at(offsets), _at(lens), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), *sizes, window, scale, code, _at(workspace), size)
     return {**out, "q": dq, "k": dk, "v": dv}
 
 
 def _cache_inputs(k_cache, v_cache, table, B, Hk, d, dtype, i):
-    import torch
     _rank(k_cache, "k_cache", 4)
     _rank(table, "table", 2)
     pages, _, page, _ = k_cache.shape
@@ -998,17 +1008,17 @@ def cache_append(k, v, k_cache, v_cache, table, offsets=None, *, lens=None, star
     whose place lies behind the table, or where the table has no page (an entry outside
     0..pages - 1), are left out.
     """
-    import torch
+    L = _lib or lib()
     N, S, i = _sequences(k, "k", offsets, lens)
     shape, dt = k.shape, k.dtype
     Hk, d = shape[-2:]
     _is(k, "k", dt, shape, i)
     _is(v, "v", dt, shape, i)
-    code = _dtype_code(k)
+    code = _code(dt, k)
     pages, page, width = _cache_inputs(k_cache, v_cache, table, S, Hk, d, dt, i)
     if start is not None:
         _is(start, "start", torch.int32, (S,), i)
-    _call(lib().muir_cache_append, i, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+    _call(L.muir_cache_append, i, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), _at(offsets), _at(lens), _at(start), N, S, Hk, d,
           pages, page, width, code)
 
@@ -1030,13 +1040,13 @@ def decode_step_attention(q, k, v, k_cache, v_cache, table, lens, *, window: int
     it). Returns o [B,H,d]. A sequence with a negative length, or without room in its table, takes
     no part: its o is 0.
     """
-    import torch
+    L = _lib or lib()
     _rank(q, "q", 3)
     _rank(k_cache, "k_cache", 4)
     B, H, d = q.shape
     Hk, i, dt = k_cache.shape[1], q.get_device(), q.dtype
     _is(q, "q", dt, (B, H, d), i)
-    code = _dtype_code(q)
+    code = _code(dt, q)
     if (k is None) != (v is None):
         raise ValueError("k and v come together")
     if k is not None:
@@ -1047,7 +1057,7 @@ def decode_step_attention(q, k, v, k_cache, v_cache, table, lens, *, window: int
     o = _like(o, "o", q, i)
     workspace, size = _workspace(
         workspace, decode_step_attention_workspace_size(B, H, Hk, d, page, width, code), q)
-    _call(lib().muir_decode_step_attention, i, q.data_ptr(), _at(k), _at(v), k_cache.data_ptr(),
+    _call(L.muir_decode_step_attention, i, q.data_ptr(), _at(k), _at(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), o.data_ptr(), B, H, Hk, d, pages,
           page, width, int(window), d ** -0.5 if scale is None else float(scale), code,
           _at(workspace), size)
