@@ -128,6 +128,22 @@ def test_plenty_of_blocks(device, d, H, Hk, window):
     check(q, k, v, do, [(b * T, n) for b, n in enumerate(lens)], lens=torch.tensor(lens, dtype=torch.int32, device=device), window=window)
 
 
+@pytest.mark.parametrize("dt,H,Hk", [(BF, 4, 1), (BF, 32, 32), (FL, 4, 2)])
+@pytest.mark.parametrize("S", [1, 62, 63, 64, 65, 130])
+@pytest.mark.parametrize("window", [0, 3])
+def test_sequence_counts(device, dt, H, Hk, S, window):
+    """As many packed sequences as lanes count at once, one fewer, more; some empty, rows behind the last, tokens left out by lengths."""
+    g = torch.Generator().manual_seed(S)
+    n = torch.randint(0, 12, (S,), generator=g)
+    n[S // 2] = 140
+    n[::5] = 0
+    offsets = torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)]).int()
+    lens = (n - torch.randint(0, 3, (S,), generator=g)).clamp_min(0).int()
+    N = int(offsets[-1]) + 40
+    q, k, v, do = make(device, dt, (N,), H, Hk, 64, S)
+    check(q, k, v, do, oa.spans(N, offsets.tolist(), lens.tolist()), offsets.to(device), lens=lens.to(device), window=window)
+
+
 @pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (FL, 64), (FL, 128)])
 def test_long_rows_with_many_heads(device, dt, d):
     """Rows with more tiles of keys than are in flight at once, in many workgroups; the last rows of several sequences."""
