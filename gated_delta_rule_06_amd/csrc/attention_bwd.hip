@@ -105,7 +105,7 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     float rest = 0.f, bar = 0.125f;
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
-        ln.again();
+        if constexpr (sizeof(T) == 4 || !SPLIT) ln.again();
         const bool masked = (j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window);
 #pragma unroll
         for (int t = 0; t < KEYS / 32; ++t) {
