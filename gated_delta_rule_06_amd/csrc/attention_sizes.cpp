@@ -44,8 +44,11 @@ size_t attention_bwd_workspace_bytes(int N, int H) { return 2 * up256(static_cas
 // One workgroup to a compute unit, by its LDS: B1 T32768 H16 Hk4 d128 bf16 (page 64) 17.1 us with room for 256 workgroups, 20.7 with 512 (the parts then cost
 // more than they gain), 18.8 with half as many wavefronts. bf16 heads of 64 take half of the LDS; where the parts stay long, room for 512 pays:
 // B64 T8000 H16 Hk4 66 us against 74, while B16 T1000 H12 (192 workgroups) has 9.0 unsplit and 10.8 in two. A part has 256 keys at least, a tile for
-// each wavefront.
+// each wavefront. Up to 128 KB of keys a second launch costs more than it saves: B4 H16 Hk4 by calls, and in a graph, whole and in parts, bf16 d128 T511 7.9
+// and 11.0, 7.3 and 8.3; d64 T1023 8.0 and 11.6, 8.4 and 8.0; float32 d64 T511 9.3 and 11.6, 9.9 and 9.7; beyond, bf16 d128 T1023 9.5 and 11.3, 10.1 and
+// 8.3, T2047 15.6 and 11.1, 16.3 and 8.5.
 int attention_step_parts(int B, int H, int Hk, int d, int capacity, bool bf16) {
+    if (static_cast<long long>(capacity) * d * (bf16 ? 2 : 4) <= 128 << 10) return 1;
     const long long groups = static_cast<long long>(B) * Hk * ((H / Hk + 15) / 16), most = capacity / 256;
     long long parts = std::min(most, 256 / groups);
     if (bf16 && d == 64) parts = std::max(parts, std::min<long long>(512 / groups, capacity / 2048));

@@ -282,7 +282,8 @@ hipError_t launch_parts(const CacheCall &c, const void *q, const void *k, const 
 template <typename T, int D>
 hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *v, const int *lens, void *o, int B, int H, int window,
                   float scale, void *workspace, hipStream_t stream) {
-    const int parts = attention_step_parts(B, H, c.Hk, D, c.width * c.page, sizeof(T) == 2);
+    // With a window there is less to divide, never more than the workspace has room for.
+    const int room = c.width * c.page, parts = attention_step_parts(B, H, c.Hk, D, window ? min(room, window) : room, sizeof(T) == 2);
     float *part_o = static_cast<float *>(workspace), *part_s = part_o + static_cast<size_t>(B) * H * parts * D;
     const bool big = 2 * static_cast<size_t>(c.pages) * c.Hk * c.page * D * sizeof(T) > size_t(256) << 20;
     const hipError_t err = big ? launch_parts<T, D, true>(c, q, k, v, lens, o, B, H, parts, window, scale, part_o, part_s, stream)

@@ -186,3 +186,10 @@ def test_large_cache(device, dt, d):
         near = muir.decode_step_attention(q, k, v, ks, vs, table, lens, window=window)
         assert torch.isfinite(o).all() and torch.equal(o, near) and same(kc[far:], ks) and same(vc[far:], vs)
     assert torch.isnan(kc[:far]).all() and torch.isnan(vc[:far]).all()
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (FL, 64), (FL, 128)])
+@pytest.mark.parametrize("window", [1, 255, 600, 1500, 2047])
+def test_windows_over_a_long_cache(device, dt, d, window):
+    """A window leaves fewer parts than the workspace, whose size knows of no window, has room for."""
+    check(*setup(device, dt, [2500, 1, 900], 4, 2, d, 32, window), window=window)
