@@ -5,7 +5,7 @@
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed): one kernel would have to add dq atomically, and its bits would depend on the
 // order. bf16 B8 T4096 H16 d128: dq 0.85 ms, dkv 0.97 ms, 980 and 1130 TFLOP/s of the products made; matrix cores busy in 55 and
-// 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (244 and 256) and LDS. Packed with a window of 512 (13731 rows,
+// 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (228 and 256) and LDS. Packed with a window of 512 (13731 rows,
 // H16 Hk4) 129 and 133 us, matrix cores busy in 31 and 35 %: 6.8 and 1.7 workgroups to a compute unit do not come out even.
 // bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
@@ -105,10 +105,12 @@ __global__ __launch_bounds__((64 * Bwd<T, D, SPLIT>::WAVES), (Bwd<T, D, SPLIT>::
     float rest = 0.f, bar = 0.125f;
 
     auto step = [&](int j, unsigned char *kt, unsigned char *vt, auto values_done) __attribute__((always_inline)) {
-        if constexpr (sizeof(T) == 4 || !SPLIT) ln.again();
+        if constexpr (sizeof(T) == 4) ln.again();
         const bool masked = (j + 1) * KEYS - 1 > r0 || (window && r0 + 31 - j * KEYS >= window);
 #pragma unroll
         for (int t = 0; t < KEYS / 32; ++t) {
+            // No query sees any of these 32 keys. d64 B8 T4096 H16 1005 -> 967 us for the whole backward, d128 as before with 30 registers fewer.
+            if (!SPLIT && (j * KEYS + 32 * t > r0 + 31 || (window && r0 + 1 - (j * KEYS + 32 * (t + 1)) >= window))) continue;
             f32x16_t x = {}, y;
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = -d;
