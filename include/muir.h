@@ -576,7 +576,9 @@ muir_status_t muir_matvec_q4(
  * Rows that are no token (behind a sequence's length, or behind the last sequence) have o = 0 and lse = -infinity, and what k and v hold
  * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of tokens up to 127 before it, and with a window
  * up to 127 behind the last that sees it (as 0 times it). float32 products are made of three bf16 terms: an infinity in them comes as NaN.
- * Offsets that do not ascend leave rows of the outputs unset, and never touch anything outside them.
+ * Offsets that do not ascend leave rows of the outputs unset, and never touch anything outside them. Scores of up to 2^29 in size are taken
+ * rightly by the forward and the step; beyond, what float32 rounds off a score is more than an exponential of it takes. The backward makes
+ * exponentials from lse, whose rounding they have in them: 2^-24 of the score's size.
  * bf16: exp(s_ij - m_i) is rounded to bf16 before it multiplies v_j; sums, maxima and lse are float32. Errors as for muir_chunk_fwd,
  * and MUIR_ERR_UNSUPPORTED for H above 2^15, N above 2^30 or (N / 128 + S + 1) H
  * above 2^24 - 1 (float32: N / 32).

@@ -199,6 +199,25 @@ def test_scores_near_the_lowest(device, dt, T, H):
     assert (off <= (u + 2 * (n + 8) * 2.0 ** -24) * V.abs().cumsum(0) / n).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("dt", [BF, FL])
+@pytest.mark.parametrize("T,H", [(60, 1), (100, 300)])
+@pytest.mark.parametrize("up", [True, False])
+def test_large_scores(device, dt, T, H, up):
+    """Scores of up to 2^29, some 2^22 apart, rising or falling along the keys: each query has one key, the last it sees or the first. The score's own rounding
+    is in both of numerator and denominator. bf16: the exponential is rounded once and so is the output, two half steps, and a few of float32. float32: the
+    product of three terms leaves out three parts of up to 2^-24 each and adds six, then come a reciprocal, its product with the sum and the storing:
+    12 times 2^-24."""
+    q, k, v, _ = make(device, dt, (1, T), H, H, 64, T)
+    q.zero_()
+    k.zero_()
+    q[..., 0] = 2.0 ** 16
+    k[0, :, :, 0] = ((1 if up else -1) * torch.arange(T, device=device)[:, None] * 2.0 ** 9).to(dt)
+    o, lse = muir.attention_fwd(q, k, v)
+    want = v[0].double().cpu() if up else v[0, :1].double().cpu().expand(T, H, 64)
+    bound = 2.1 * 2.0 ** -8 if dt is BF else 12 * 2.0 ** -24
+    assert ((o[0].double().cpu() - want).abs() <= bound * want.abs()).all() and torch.isfinite(lse).all()
+
+
 def test_no_rows(device):
     x = torch.zeros(2, 0, 2, 64, device=device)
     o, lse = muir.attention_fwd(x, x, x)
