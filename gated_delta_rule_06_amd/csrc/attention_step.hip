@@ -122,13 +122,14 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
         const int p0 = tile * 32;
         own_loads_done<LOADS>();  // the values were asked for after the keys
         u32x4_t new_value;
-        const bool has_new = kn && p0 <= old && old < p0 + 32 && n > old;
-        if (has_new && lane < Ti::CH) {  // the new token's row
+        // The new token's row, where its page is there. A row that is not put in stays zeros: its p is 0, and what it multiplies has to be finite.
+        const bool has_new = kn && p0 <= old && old < p0 + 32 && n > old && (good >> ((old - p0) >> 4) & 1);
+        if (has_new && lane < Ti::CH) {
             const size_t at = (static_cast<size_t>(b) * pg.Hk + hk) * D + lane * (16 / sizeof(T));
             const u32x4_t new_key = *reinterpret_cast<const u32x4_t *>(kn + at);
             new_value = *reinterpret_cast<const u32x4_t *>(vn + at);
             *reinterpret_cast<u32x4_t *>(kt + Ti::at(old - p0, lane)) = new_key;
-            if (set == 0 && (good >> ((old - p0) >> 4) & 1)) {
+            if (set == 0) {
                 const size_t row = pg.row(pg.id(b, old), hk, old) * D + lane * (16 / sizeof(T));
                 *reinterpret_cast<u32x4_t *>(k_cache + row) = new_key;
                 *reinterpret_cast<u32x4_t *>(v_cache + row) = new_value;
