@@ -180,6 +180,8 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
         else
             own_loads_done<0>();
         if (has_new && lane < Ti::CH) *reinterpret_cast<u32x4_t *>(vt + Ti::at(old - p0, lane)) = new_value;
+        if (p0 < begin)  // values before the window, times p = 0, must be finite (the permutation stays inside a row)
+            for (int i = lane; i < (begin - p0) * Ti::CH; i += 64) *reinterpret_cast<u32x4_t *>(vt + 16 * i) = u32x4_t{};
         wave_lds_sync();
 #pragma unroll
         for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, ln), p, acc[i]);

@@ -633,7 +633,7 @@ muir_status_t muir_cache_append(
  *   workspace: muir_decode_step_attention_workspace_size(...) bytes (0 where no sequence is split)
  *
  * A sequence with lens[b] < 0, or whose table has no room for its tokens, takes no part: o is 0 and nothing is written. Tokens in no page are
- * not seen (and a new one is not kept); where none is seen o is 0. What a page holds behind the last token reaches nothing. The page that a new token
+ * not seen (and a new one is not kept); where none is seen o is 0. What the cache holds behind the last token or before the window reaches nothing. The page that a new token
  * goes to must not be read by another sequence of the same call; pages before it may be shared. MUIR_ERR_UNSUPPORTED where
  * B Hk ceil(H / Hk / 16) is above 2^23 - 1.
  */
