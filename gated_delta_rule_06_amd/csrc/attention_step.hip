@@ -5,7 +5,8 @@
 // while values are multiplied, the next values while keys are); they meet in LDS at the end. Where sequences and key heads do not fill the card a sequence is cut into parts, which a second kernel
 // joins. Reading the cache once bounds it: B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.37 GB, 207 to 217 us, 6.3 to 6.6 TB/s; B1 T32768 H16 Hk4, 67 MB, 13.6 us
 // and 3.8 for the join. Scores are made transposed (16 keys by 16 heads), so that two score tiles are the operand
-// of the product with the values, as in the prompt kernels; p is rounded to bf16 there in bf16.
+// of the product with the values, as in the prompt kernels. In bf16 p goes into it as two terms: rounded once, o would be 0.0020 off (2-norm, relative, B256)
+// where its own rounding is 0.0017, and reading hides the second product (217 us both; B1 T32768 16.2 and 16.4 a call, 16 MB of cache 10.8 and 11.0).
 // Rows behind the last token, and pages that the table does not have, are never read: their keys come as zeros and are masked.
 #include "attention.hpp"
 #include "attention_kernels.hpp"
@@ -58,6 +59,14 @@ template <typename T, int D> struct Step {
     static constexpr int ROOM = 2 * TILE, LDS = WAVES * ROOM;  // a tile of keys and one of values for each wavefront
     static_assert(ROOM >= 16 * D * 4 + 128, "outputs, maxima and sums of 16 heads pass through the tiles' room");
 };
+
+// What eight values lose when they are packed to bf16, as the second term of two.
+__device__ __forceinline__ bf16x8_t rounded_off(const float (&x)[8]) {
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = x[j] - static_cast<float>(static_cast<__bf16>(x[j]));
+    return Op<bf16_t>::pack(r);
+}
 
 // BIG: the cache is larger than the 256 MB that the last-level cache holds, so none of it is there when it comes to be read, and its loads go past the caches:
 // B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.3 GB, 207 us (6.3 TB/s) against 233. A cache of 190 MB read again and again takes 33 us with ordinary loads, 38 so.
@@ -174,7 +183,8 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
                 x[u][i] = __builtin_amdgcn_exp2f(fmaf(x[u][i], scale2, -m));
                 l += x[u][i];
             }
-        const frag p = Op<T>::pack16({x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]});
+        const float ps[8] = {x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
+        const frag p = Op<T>::pack16(ps);
         if (more)
             own_loads_done<LOADS>();
         else
@@ -184,7 +194,11 @@ __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kerne
             for (int i = lane; i < (begin - p0) * Ti::CH; i += 64) *reinterpret_cast<u32x4_t *>(vt + 16 * i) = u32x4_t{};
         wave_lds_sync();
 #pragma unroll
-        for (int i = 0; i < NO; ++i) acc[i] = Op<T>::mma16(Ti::template col<16>(vt, 0, 16 * i, ln), p, acc[i]);
+        for (int i = 0; i < NO; ++i) {
+            const frag vf = Ti::template col<16>(vt, 0, 16 * i, ln);
+            if constexpr (sizeof(T) == 2) acc[i] = Op<T>::mma16(vf, rounded_off(ps), acc[i]);
+            acc[i] = Op<T>::mma16(vf, p, acc[i]);
+        }
         own_reads_done();
         if (more) fetch(v_cache, tile + WAVES, vt);
         good = good_next;

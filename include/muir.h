@@ -634,7 +634,8 @@ muir_status_t muir_cache_append(
  *
  * A sequence with lens[b] < 0, or whose table has no room for its tokens, takes no part: o is 0 and nothing is written. Tokens in no page are
  * not seen (and a new one is not kept); where none is seen o is 0. What the cache holds behind the last token or before the window reaches nothing. The page that a new token
- * goes to must not be read by another sequence of the same call; pages before it may be shared. MUIR_ERR_UNSUPPORTED where
+ * goes to must not be read by another sequence of the same call; pages before it may be shared. In bf16 the exponentials are taken as two bf16 terms
+ * each, which leave out 2^-16 of them. MUIR_ERR_UNSUPPORTED where
  * B Hk ceil(H / Hk / 16) is above 2^23 - 1.
  */
 size_t muir_decode_step_attention_workspace_size(int B, int H, int Hk, int d, int page, int width,
