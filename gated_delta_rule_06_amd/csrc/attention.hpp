@@ -24,7 +24,7 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LN2 = 0.6931471805599453f;
 // A running maximum before any key: below scores of any size that a sum of products leaves exact, and finite, so that differences from it stay
 // numbers.
 constexpr float LOWEST = -3e38f;

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "attention_kernels.hpp"
+#include "attention_layout.hpp"
 #include "muir.h"
 #include "op_checks.hpp"
 
@@ -36,7 +37,8 @@ muir_status_t check_rows(const char *fn, int N, int S, const int *offsets, int p
 
 muir_status_t check_scores(const char *fn, int window, float scale) {
     if (window < 0) return fail(MUIR_ERR_SHAPE, "%s: window must be >= 0 (got %d)", fn, window);
-    if (!(scale >= kMinScale) || isinf(scale)) return fail(MUIR_ERR_SHAPE, "%s: scale must be finite and at least 2^-64", fn);
+    if (!(scale >= kMinScale) || isinf(scale * at::LOG2E))
+        return fail(MUIR_ERR_SHAPE, "%s: scale must be at least 2^-64, and times log2(e) finite", fn);
     return MUIR_OK;
 }
 

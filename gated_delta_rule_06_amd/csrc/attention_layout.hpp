@@ -15,6 +15,8 @@
 namespace muir {
 namespace at {
 
+constexpr float LOG2E = 1.4426950408889634f;  // the kernels take exponentials to base 2, with it in the scale
+
 MUIR_HD int cut(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
 // Rows of one call's sequences. Sequence s has the rows first(s) .. first(s + 1), of which the first `lens[s]` are tokens; "sequence" S is

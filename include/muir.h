@@ -571,7 +571,7 @@ muir_status_t muir_matvec_q4(
  *                                        0..N). NULL: N / S rows each, a padded batch [S, N / S, ...]
  *   lens     [S] int32 or NULL           tokens of each sequence, from its first row on (clamped to its rows; NULL: all of them)
  *   lse      [N, H] float32 or NULL      which muir_attention_bwd takes
- *   H a multiple of Hk; d 64 or 128; window >= 0, 0 for no limit; scale finite and at least 2^-64 (usually d^(-1/2)); N >= 0
+ *   H a multiple of Hk; d 64 or 128; window >= 0, 0 for no limit; scale at least 2^-64 and at most 2.3586e38 (usually d^(-1/2)); N >= 0
  *
  * Rows that are no token (behind a sequence's length, or behind the last sequence) have o = 0 and lse = -infinity, and what k and v hold
  * there reaches nothing. Inside a sequence a NaN or infinity in a token's v can reach the o of tokens up to 127 before it, and with a window
