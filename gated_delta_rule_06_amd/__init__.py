@@ -917,7 +917,13 @@ def _attention_inputs(q, k, v, offsets, lens, window, scale):
         _is(q, "q", dt, shape, i)
     _is(k, "k", dt, kshape, i)
     _is(v, "v", dt, kshape, i)
-    return (N, S, H, Hk, d), int(window), d ** -0.5 if scale is None else float(scale), _code(dt, q), i
+    return (N, S, H, Hk, d), _window(window), d ** -0.5 if scale is None else float(scale), _code(dt, q), i
+
+
+def _window(window):
+    """``window`` as a C int, which ctypes would cut to its low bits: beyond any length it is no limit, and negative stays so."""
+    w = int(window)
+    return w if 0 <= w < 2 ** 31 else 2 ** 31 - 1 if w > 0 else -1
 
 
 def _code(dt, t):
@@ -1059,6 +1065,6 @@ def decode_step_attention(q, k, v, k_cache, v_cache, table, lens, *, window: int
         workspace, decode_step_attention_workspace_size(B, H, Hk, d, page, width, code), q)
     _call(L.muir_decode_step_attention, i, q.data_ptr(), _at(k), _at(v), k_cache.data_ptr(),
           v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), o.data_ptr(), B, H, Hk, d, pages,
-          page, width, int(window), d ** -0.5 if scale is None else float(scale), code,
+          page, width, _window(window), d ** -0.5 if scale is None else float(scale), code,
           _at(workspace), size)
     return o
