@@ -68,8 +68,13 @@ __device__ __forceinline__ bf16x8_t rounded_off(const float (&x)[8]) {
     return Op<bf16_t>::pack(r);
 }
 
-// BIG: the cache is larger than the 256 MB that the last-level cache holds, so none of it is there when it comes to be read, and its loads go past the caches:
-// B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.3 GB, 207 us (6.3 TB/s) against 233. A cache of 190 MB read again and again takes 33 us with ordinary loads, 38 so.
+// BIG: the cache is larger than the 256 MB that the last-level cache holds, so of a program that works its way through it nothing is there when it comes to be
+// read again, and its loads go past the caches: B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.3 GB, 207 us (6.3 TB/s) against 233. A cache of 190 MB read again and
+// again takes 33 us with ordinary loads, 38 so. Calls that read a part of 4 GB, other pages each time, with ordinary loads and so, and the same pages again
+// (H16 Hk4 d128 bf16): 16 MB (B1 T8000) 11.2 and 10.8, 8.8 and 10.3; 67 MB (B1 T32767) 19.0 and 17.1, 16.7 and 15.3; 131 MB (B16 T4000) 29.0 and 25.8,
+// 24.6 and 24.3; 393 MB (B64 T3000) 70.9 and 62.3, 65.9 and 62.0. So only small calls over the same pages lose, and those a program of several
+// layers does not make. Where a key head has more than 16 query heads, the workgroups of its sets read the same keys, and the caches serve all but the
+// first (likewise): H64 Hk2 d128 bf16 B16 T4000 26.7 and 27.2, 26.7 and 25.0; B256 T4000 289 and 321, 287 and 320; H40 Hk1 d64 B128 T4000 60 and 73, 61 and 74.
 template <typename T, int D, bool BIG>
 __global__ __launch_bounds__((Step<T, D>::WAVES * 64)) void attention_step_kernel(
     const T *__restrict__ q, const T *__restrict__ kn, const T *__restrict__ vn, T *k_cache, T *v_cache, Pages pg,
@@ -302,7 +307,7 @@ hipError_t launch(const CacheCall &c, const void *q, const void *k, const void *
     // With a window there is less to divide, never more than the workspace has room for.
     const int room = c.width * c.page, parts = attention_step_parts(B, H, c.Hk, D, window ? min(room, window) : room, sizeof(T) == 2);
     float *part_o = static_cast<float *>(workspace), *part_s = part_o + static_cast<size_t>(B) * H * parts * D;
-    const bool big = 2 * static_cast<size_t>(c.pages) * c.Hk * c.page * D * sizeof(T) > size_t(256) << 20;
+    const bool big = H / c.Hk <= 16 && 2 * static_cast<size_t>(c.pages) * c.Hk * c.page * D * sizeof(T) > size_t(256) << 20;
     const hipError_t err = big ? launch_parts<T, D, true>(c, q, k, v, lens, o, B, H, parts, window, scale, part_o, part_s, stream)
                                : launch_parts<T, D, false>(c, q, k, v, lens, o, B, H, parts, window, scale, part_o, part_s, stream);
     if (err != hipSuccess || parts == 1) return err;
