@@ -977,7 +977,9 @@ def attention_bwd(q, k, v, o, lse, offsets=None, *, do, lens=None, window: int =
 
     Inputs as for the forward, its o and lse, and ``do`` (dL/do, like q). Returns a dict keyed by
     ``ATTENTION_GRADS``, shaped and typed as the inputs (shared heads summed); rows that are no
-    token have gradients 0. ``out`` may hold pre-allocated tensors under those keys.
+    token have gradients 0. ``out`` may hold pre-allocated tensors under those keys. In bfloat16 o
+    and lse must be what the forward gives for these very keys (not merged with other keys'): do . o
+    is put right by what the call itself sums.
     """
     L = _lib or lib()
     sizes, window, scale, code, i = _attention_inputs(q, k, v, offsets, lens, window, scale)

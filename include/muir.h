@@ -597,7 +597,9 @@ muir_status_t muir_attention_fwd(
  *   workspace: muir_attention_bwd_workspace_size(...) bytes
  *
  * Rows that are no token have gradients 0, and dout and o are not looked at there. Every sum is float32, in a fixed order. In bf16 p and ds
- * are rounded to bf16 before the products that sum them, and D takes in what the rounding of o left out. A NaN or infinity in a token can
+ * are rounded to bf16 before the products that sum them, and D is not do_i . o_i but sum_j p_ij do_i . v_j over the keys of this call, which takes in what the
+ * rounding of o left out. So in bf16 o and lse have to be those of the forward with these very keys: merged with other keys' (blocks of a longer sequence, a
+ * sink) they give wrong dq and dk, where float32, which takes do_i . o_i as it is, gives this call's part. A NaN or infinity in a token can
  * reach the gradients of tokens up to 127 before and behind those that see it.
  */
 size_t muir_attention_bwd_workspace_size(int N, int S, int H, int Hk, int d, muir_dtype_t qkv);
