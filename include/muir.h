@@ -615,7 +615,7 @@ muir_status_t muir_attention_bwd(
  *   k_cache, v_cache  [pages, Hk, page, d] dtype `type`: row p % page of page table[s][p / page] holds token p of sequence s
  *   table             [S, width] int32   pages of each sequence; an entry outside 0 .. pages - 1 is no page
  *   start             [S] int32 or NULL  place of each sequence's first token (NULL: 0; below 0: the sequence is left out)
- *   page 16, 32, 64, 128 or 256; width * page up to 2^30
+ *   page 16, 32, 64, 128 or 256; width * page up to 2^30; MUIR_ERR_UNSUPPORTED for N above 2^30 or N / 8 + S + 1 above 2^24 - 1
  *
  * Tokens whose place lies behind the table or in no page are left out. Where a page occurs twice among the places written, either token may be kept.
  */
