@@ -4,14 +4,16 @@
 // A workgroup has 128 query rows of one head, 32 to a wavefront, whose queries stay in registers; keys and values come in tiles through LDS,
 // the next tile's loads (straight to LDS) in flight. Scores are made transposed, S^T = K Q^T, so a lane holds scores of one query: the maximum and the
 // sum are sums inside the lane and over the two halves of the wavefront, and the accumulators of P^T are the operand of O^T += V^T P^T.
-// bf16: p is rounded to bf16 for that product (half a step, 2^-9 of each term, of either sign), its sum is taken before the rounding, and
-// everything else is float32.
+// bf16: p is rounded to bf16 for that product (half a step, at most 2^-8 of each term, of either sign), its sum is taken before the rounding, and
+// everything else is float32. o is 0.0022 off by it (2-norm, relative) where its own rounding is 0.0017. With p as two terms it would be that, at the price of
+// a third product beside every two: B1 T32768 H16 d128 3.99 -> 5.63 ms, 24 packed sequences up to 4001 H16 Hk4 402 -> 542 us, d64 with a window of 1024
+// 127 -> 174.
 // The output is rescaled only where a row's maximum grew by more than 2^8 over the reference its exponentials are taken from; up to there
 // they are as exact in float32 and bf16 as below 1.
 //
-// What bounds it. d128: the matrix cores and the card's power. B1 T32768 H16 4.0 to 4.1 ms, 1080 TFLOP/s, where a large library product makes 1361: matrix
-// cores busy in 64 % of the cycles, vector instructions in 69 %, at a clock of 1.4 GHz; B8 T4096 H16 550 us, 1000 TFLOP/s, 58 and 66 % at 1.6 GHz. d64: vector instructions, of
-// which there are as many to half the products: B8 T4096 H12 window 1024 126 us, vector 73 %, matrix 39 %. Few rows: the walk of the last rows' workgroup.
+// What bounds it. d128: the matrix cores and the card's power. B1 T32768 H16 3.95 to 4.0 ms, 1100 TFLOP/s, where a large library product makes 1361: matrix
+// cores busy in 67 % of the cycles, vector instructions in 67 %, at a clock of 1.4 GHz; B8 T4096 H16 540 us, 1020 TFLOP/s, 60 and 64 % at 1.6 GHz. d64: vector instructions, of
+// which there are as many to half the products: B8 T4096 H12 window 1024 127 us, vector 75 %, matrix 40 %. Few rows: the walk of the last rows' workgroup.
 // Sizes tried, in us: d64 tiles of 64 keys against 32, B8 T4096 H16 331 and 351; d128 the other way, 4350 and 4160 at B1 T32768 H16, since 64 keys leave
 // two workgroups to a compute unit instead of three. Two blocks of 32 queries to a wavefront, which halves the reads of LDS: 4.2 against 4.3 ms there,
 // 515 against 430 for 24 packed sequences, so not kept.

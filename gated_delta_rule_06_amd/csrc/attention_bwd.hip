@@ -4,15 +4,16 @@
 // Two kernels, each with its sums in registers from the first to the last product, so no sum depends on an order and nothing is
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed): one kernel would have to add dq atomically, and its bits would depend on the
-// order. bf16 B8 T4096 H16 d128: dq 0.85 ms, dkv 0.97 ms, 980 and 1130 TFLOP/s of the products made; matrix cores busy in 55 and
-// 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (228 and 256) and LDS. Packed with a window of 512 (13731 rows,
-// H16 Hk4) 129 and 133 us, matrix cores busy in 31 and 35 %: 6.8 and 1.7 workgroups to a compute unit do not come out even.
+// order (in float32, over blocks of 128 keys, it would go to memory and back 16 times at T4096: 8.6 GB at B8 H16 d128, more than the whole backward's time).
+// bf16 B8 T4096 H16 d128: dq 0.84 ms, dkv 0.97 ms, 985 and 1140 TFLOP/s of the products made; matrix cores busy in 53 and 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (228 and 256) and LDS. Packed with a window of 512 (13731 rows,
+// H16 Hk4) 129 to 139 and 133 to 143 us, matrix cores busy in 30 and 36 %: 6.8 and 1.7 workgroups to a compute unit do not come out even.
 // bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off
 // (2-norm, relative) where one rounding is 0.0017. But sum_j ds_ij = 0, so dq's kernel finds e_i as the sum of its own ds, hands the
 // exact D on to dk, and takes e_i sum_j p_ij k_j off dq, of that sum only the largest p of each of a wavefront's halves: the rest is
 // small, and is times e_i. The same product adds what the ds of those keys lost when they were rounded, most of what a row's ds lose. dq is 0.0021 off
-// then, dk 0.0024.
+// then, dk 0.0024, dv 0.0023. With ds as two terms dq and dk would be 0.0018 and 0.0017, with p too dv 0.0017: forward and backward of B8 T4096 H16 d128
+// 2.41 -> 2.80 and 3.11 ms, packed with a window of 512 326 -> 371 and 413 us.
 #include "attention.hpp"
 #include "attention_kernels.hpp"
 #include "launch.hpp"
