@@ -632,6 +632,7 @@ muir_status_t muir_cache_append(
  *   k, v     [B, Hk, d] dtype `type`, or both NULL: nothing is appended, and the query attends to the tokens that are there
  *   k_cache, v_cache, table [B, width], page as for muir_cache_append
  *   lens     [B] int32   tokens in the cache before the call; the new one is token lens[b]
+ *   window, scale as for muir_attention_fwd
  *   workspace: muir_decode_step_attention_workspace_size(...) bytes (0 where no sequence is split)
  *
  * A sequence with lens[b] < 0, or whose table has no room for its tokens, takes no part: o is 0 and nothing is written. Tokens in no page are
