@@ -5,7 +5,8 @@
 // added atomically: dq walks a query block's keys, dk and dv walk a key block's queries, of all the heads that share it. Scores
 // and do . v are made in both (7 products of which 5 are needed): one kernel would have to add dq atomically, and its bits would depend on the
 // order (in float32, over blocks of 128 keys, it would go to memory and back 16 times at T4096: 8.6 GB at B8 H16 d128, more than the whole backward's time).
-// bf16 B8 T4096 H16 d128: dq 0.84 ms, dkv 0.97 ms, 985 and 1140 TFLOP/s of the products made; matrix cores busy in 53 and 63 % of the cycles at 1.7 GHz, two workgroups to a compute unit by registers (228 and 256) and LDS. Packed with a window of 512 (13731 rows,
+// bf16 B8 T4096 H16 d128: dq 0.84 ms, dkv 0.97 ms, 985 and 1140 TFLOP/s of the products made; matrix cores busy in 53 and 63 % of the cycles at 1.7 GHz,
+// two workgroups to a compute unit by registers (228 and 256) and LDS. Packed with a window of 512 (13731 rows,
 // H16 Hk4) 129 to 139 and 133 to 143 us, matrix cores busy in 30 and 36 %: 6.8 and 1.7 workgroups to a compute unit do not come out even.
 // bf16: p and ds are rounded to bf16 for the products that sum them (half a step of each term, of either sign); everything else is
 // float32. D from the rounded o is off by some e_i, and where one key has most of a row's p its ds is what that leaves: dq and dk would be 0.0029 to 0.0032 off

@@ -5,7 +5,8 @@
 // while values are multiplied, the next values while keys are); they meet in LDS at the end. Where sequences and key heads do not fill the card a sequence is cut into parts, which a second kernel
 // joins. Reading the cache once bounds it: B256 T4001 (mixed) H16 Hk4 d128 bf16, 1.37 GB, 207 to 218 us, 6.3 to 6.6 TB/s; B1 T32768 H16 Hk4, 67 MB, 13.9 us
 // and 2.9 to 3.9 for the join. How many parts is decided by the batch and the table's room, not by lengths, which lie on the device: one sequence of 32767 among 63
-// of 100 (H16 Hk4 d128 bf16, 80 MB) is walked by a workgroup to a key head and takes 285 us, among 31 146, among 7 43, alone 15; 64 of 100 take 5.6. Scores are made transposed (16 keys by 16 heads), so that two score tiles are the operand
+// of 100 (H16 Hk4 d128 bf16, 80 MB) is walked by a workgroup to a key head and takes 285 us, among 31 146, among 7 43, alone 15; 64 of 100
+// take 5.6. Scores are made transposed (16 keys by 16 heads), so that two score tiles are the operand
 // of the product with the values, as in the prompt kernels. In bf16 p goes into it as two terms: rounded once, o would be 0.0020 off (2-norm, relative, B256)
 // where its own rounding is 0.0017, and reading hides the second product (217 us both; B1 T32768 16.2 and 16.4 a call, 16 MB of cache 10.8 and 11.0).
 // Rows behind the last token, and pages that the table does not have, are never read: their keys come as zeros and are masked.
